@@ -462,6 +462,142 @@ int qlinear_int8_grouped_gemm(const void* a, const void* b, const float* a_scale
                               int64_t num_groups, int64_t max_tokens_per_group,
                               int64_t num_experts, int64_t T, int64_t N, int64_t K, void* stream);
 
+/*
+ * W4A16 matmul with integer codes and group scales:
+ *     out[m, n] = alpha * sum_k x[m, k] * (code(n, k) - zero[n, k / g]) * scale[n, k / g]
+ * w_packed: uint8 [N, (K + 1) / 2], code(n, 2j) in the low nibble of byte j
+ * and code(n, 2j + 1) in the high nibble (for odd K the last high nibble is
+ * ignored), codes 0 .. 15; w_scale: bfloat16 [N, G] and w_zero: uint8 [N, G]
+ * or NULL (every zero point 8), G = ceil(K / g) groups of g = group_size
+ * consecutive k, the last one shorter where K % g != 0.  group_size is a
+ * power of two >= 32, or any value >= K (one group per row).  x: bfloat16
+ * [M, K]; out: [M, N] of out_dtype (F32 or BF16); any K >= 1.  w_packed and
+ * w_zero need no alignment, the others that of their type.  Each group is
+ * summed in float32 over exact products and scaled then, so no weight is
+ * rounded.  alpha and `epilogue` (NULL = none) as in qlinear_fp8_gemm_ws.
+ * M = 0 is allowed and does nothing.
+ */
+int qlinear_int4_gemm(const void* w_packed, const void* w_scale, const void* w_zero, const void* x,
+                      void* out, int out_dtype, int64_t M, int64_t N, int64_t K,
+                      int64_t group_size, float alpha, const qlinear_epilogue* epilogue,
+                      void* stream);
+
+/*
+ * Grouped (MoE) W4A16 matmul with integer codes: the operands of
+ * qlinear_int4_gemm per expert (w_packed: uint8 [num_experts, N, (K + 1) / 2],
+ * w_scale: bfloat16 and w_zero: uint8 [num_experts, N, G]), and the groups of
+ * rows of qlinear_fp8_grouped_gemm.  a_offsets, expert_ids, num_groups,
+ * max_tokens_per_group, inactive / empty groups (zeros / nothing), untouched
+ * rows, preconditions and bounds behaviour: exactly as there.  T = 0 is
+ * allowed and does nothing.
+ */
+int qlinear_int4_grouped_gemm(const void* w_packed, const void* w_scale, const void* w_zero,
+                              const void* x, const uint32_t* a_offsets,
+                              const int32_t* expert_ids, void* out, int out_dtype,
+                              int64_t num_groups, int64_t max_tokens_per_group,
+                              int64_t num_experts, int64_t T, int64_t N, int64_t K,
+                              int64_t group_size, void* stream);
+
+/*
+ * Mixture-of-experts router: for each of T tokens the top_k experts with the
+ * largest logits, largest first, equal logits by the lower expert, and their
+ * softmax weights
+ *     weights[t, j] = exp(l[t, e_j]) / sum_e exp(l[t, e])
+ * where the sum runs over the token's chosen experts (renormalize != 0) or
+ * over all of them (renormalize = 0).  A logit of -inf masks its expert: it
+ * is never chosen.  Where fewer than top_k experts are left, the remaining
+ * slots get expert id -1 and weight 0 (a row of which nothing is left has
+ * only such slots).  A NaN logit is never chosen either but makes all weights
+ * of its token NaN; a logit of +inf makes them NaN by the formula.
+ * logits: [T, E] of logits_dtype (F32 or BF16); expert_ids: int32 [T, top_k];
+ * weights: float32 [T, top_k]; 1 <= E <= 1024, 1 <= top_k <= min(E, 64);
+ * T * top_k < 2^31.  Softmax in float32.  T = 0 is allowed and does nothing.
+ */
+int qlinear_moe_route(const void* logits, int logits_dtype, int32_t* expert_ids, float* weights,
+                      int64_t T, int64_t E, int64_t top_k, int renormalize, void* stream);
+
+/*
+ * Gradient of qlinear_moe_route with respect to the logits: with p the
+ * softmax (over the chosen experts if renormalize != 0, else over all), a_e
+ * the gradient of expert e's weight (0 where e was not chosen),
+ *     grad_logits[t, e] = p_e * (a_e - sum_i p_i a_i),
+ * 0 for masked experts and, renormalised, for those not chosen.  expert_ids
+ * as qlinear_moe_route gave them (ids outside 0 .. E-1 are skipped, and so is
+ * their gradient); grad_weights: float32 [T, top_k]; grad_logits: [T, E] of
+ * logits_dtype, written in full.
+ */
+int qlinear_moe_route_backward(const void* logits, int logits_dtype, const int32_t* expert_ids,
+                               const float* grad_weights, void* grad_logits, int64_t T, int64_t E,
+                               int64_t top_k, int renormalize, void* stream);
+
+/*
+ * Sort of token slots by expert.  A slot is s = t * top_k + j; the sorted
+ * rows are in expert order, slots of one expert in slot order (stable), so
+ * rows a_offsets[e] .. a_offsets[e + 1] - 1 belong to expert e, as the grouped
+ * matmuls take them with expert_ids 0 .. num_experts - 1.  Slots whose id lies
+ * outside 0 .. num_experts - 1 (-1: dropped) fill the rows from
+ * a_offsets[num_experts] on, in slot order.
+ *     row_slot[r] = s of row r       (dropped: ~s, that is -1 - s)
+ *     slot_row[s] = r of slot s      (dropped: ~r)
+ * expert_ids: int32 [slots]; a_offsets: uint32 [num_experts + 1]; row_slot and
+ * slot_row: int32 [slots]; 0 <= slots < 2^31, 1 <= num_experts <= 1024.
+ * workspace: at least the bytes of qlinear_moe_sort_workspace_size, 16-byte
+ * aligned (NULL with 0 where that is 0), as the workspace of the *_ws calls;
+ * a smaller one is QLINEAR_ERR_INVALID_ARG.
+ */
+int qlinear_moe_sort_workspace_size(int64_t slots, int64_t num_experts, int64_t* bytes);
+int qlinear_moe_sort(const int32_t* expert_ids, uint32_t* a_offsets, int32_t* row_slot,
+                     int32_t* slot_row, int64_t slots, int64_t num_experts, void* workspace,
+                     int64_t workspace_bytes, void* stream);
+
+/*
+ * Token rows into expert order: out[slot_row[t, j]] = x[t] for every slot; a
+ * dropped slot (slot_row = ~r) clears row r.  x: [T, H]; out: [T * top_k, H],
+ * written in full, both of dtype (F32 or BF16); slot_row: int32 [T, top_k] as
+ * qlinear_moe_sort gives it (rows outside 0 .. T * top_k - 1 are skipped).
+ * The gradient with respect to x is qlinear_moe_combine without weights.
+ * T = 0 is allowed and does nothing; 1 <= top_k <= 64, T * top_k < 2^31.
+ */
+int qlinear_moe_gather(const void* x, const int32_t* slot_row, void* out, int dtype, int64_t T,
+                       int64_t top_k, int64_t H, void* stream);
+
+/*
+ * Rows in expert order back to tokens, weighted:
+ *     out[t] = sum_j weights[t, j] * rows[slot_row[t, j]]
+ * over the token's slots that were not dropped, in slot order, in float32,
+ * rounded once; a token without such a slot gets zeros.  A dropped slot's row
+ * and weight are not read.  rows: [T * top_k, H] of rows_dtype; weights: float32 [T, top_k]
+ * or NULL (all 1); out: [T, H] of out_dtype (each F32 or BF16).  Otherwise as
+ * qlinear_moe_gather.
+ */
+int qlinear_moe_combine(const void* rows, int rows_dtype, const int32_t* slot_row,
+                        const float* weights, void* out, int out_dtype, int64_t T, int64_t top_k,
+                        int64_t H, void* stream);
+
+/*
+ * Gradients of qlinear_moe_combine:
+ *     grad_rows[slot_row[t, j]] = weights[t, j] * grad_out[t]
+ *     grad_weights[t, j]        = sum_h grad_out[t, h] * rows[slot_row[t, j], h]
+ * (a dropped slot: its row cleared, its gradient 0).  grad_out: [T, H], rows
+ * and grad_rows: [T * top_k, H], all of dtype (F32 or BF16); grad_weights:
+ * float32 [T, top_k], summed in float32.  Every row is written.
+ */
+int qlinear_moe_combine_backward(const void* grad_out, const void* rows, int dtype,
+                                 const int32_t* slot_row, const float* weights, void* grad_rows,
+                                 float* grad_weights, int64_t T, int64_t top_k, int64_t H,
+                                 void* stream);
+
+/*
+ * Gated activation of an expert's (or any) feed-forward layer:
+ *     y[m, f] = silu(x[m, f]) * x[m, F + f],   silu(g) = g / (1 + exp(-g)),
+ * and its gradient with respect to x.  x and grad_x: [M, 2F] (gate columns
+ * first); y and grad_y: [M, F], all of dtype (F32 or BF16); float32 inside,
+ * rounded once.  M = 0 is allowed and does nothing.
+ */
+int qlinear_swiglu(const void* x, void* y, int dtype, int64_t M, int64_t F, void* stream);
+int qlinear_swiglu_backward(const void* grad_y, const void* x, void* grad_x, int dtype, int64_t M,
+                            int64_t F, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

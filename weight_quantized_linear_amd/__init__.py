@@ -36,6 +36,16 @@ __all__ = [
     "nvfp4_dequant",
     "int8_quantize_act",
     "int8_gemm",
+    "int4_gemm",
+    "int4_grouped_gemm",
+    "moe_route",
+    "moe_route_backward",
+    "moe_sort",
+    "moe_gather",
+    "moe_combine",
+    "moe_combine_backward",
+    "swiglu",
+    "swiglu_backward",
     "PATHS",
     "gemm_workspace_bytes",
     "WEIGHT_FP8",
@@ -92,6 +102,17 @@ EXPORTED = {
     "qlinear_nvfp4_gemm_ws": [_p, _p, _p, _p, _i, _i64, _i64, _i64, _f, _EP, _i, _p, _i64, _p],
     "qlinear_bf16_gemm_ws": [_p, _p, _p, _i, _i64, _i64, _i64, _f, _EP, _i, _p, _i64, _p],
     "qlinear_fp8_gemm_noalloc": [_p, _p, _p, _i, _i64, _i64, _i64, _f, _EP, _i, _p],
+    "qlinear_int4_gemm": [_p, _p, _p, _p, _p, _i, _i64, _i64, _i64, _i64, _f, _EP, _p],
+    "qlinear_int4_grouped_gemm": [_p, _p, _p, _p, _p, _p, _p, _i, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _p],
+    "qlinear_moe_route": [_p, _i, _p, _p, _i64, _i64, _i64, _i, _p],
+    "qlinear_moe_route_backward": [_p, _i, _p, _p, _p, _i64, _i64, _i64, _i, _p],
+    "qlinear_moe_sort_workspace_size": [_i64, _i64, ctypes.POINTER(_i64)],
+    "qlinear_moe_sort": [_p, _p, _p, _p, _i64, _i64, _p, _i64, _p],
+    "qlinear_moe_gather": [_p, _p, _p, _i, _i64, _i64, _i64, _p],
+    "qlinear_moe_combine": [_p, _i, _p, _p, _p, _i, _i64, _i64, _i64, _p],
+    "qlinear_moe_combine_backward": [_p, _p, _i, _p, _p, _p, _p, _i64, _i64, _i64, _p],
+    "qlinear_swiglu": [_p, _p, _i, _i64, _i64, _p],
+    "qlinear_swiglu_backward": [_p, _p, _p, _i, _i64, _i64, _p],
 }
 
 WEIGHT_FP8, WEIGHT_NVFP4, WEIGHT_BF16 = 0, 1, 2
@@ -548,3 +569,262 @@ def int8_grouped_gemm(a: torch.Tensor, b: torch.Tensor, a_scale: torch.Tensor | 
     _check(st, "qlinear_int8_grouped_gemm")
     return out
 
+
+
+def _int4_operands(w_packed, w_scale, w_zero, x, group_size: int, lead: str):
+    """The checked int4 operands (w, scale, zero pointer, x, K, groups); ``lead`` names
+    the leading dimension of an expert stack ("" for one matrix)."""
+    w = _as_u8(w_packed, "w_packed")
+    sc = _as_bf16(w_scale, "w_scale")
+    x = _as_bf16(x, "x")
+    for t, name in ((w, "w_packed"), (sc, "w_scale"), (x, "x")):
+        _require(t, name)
+    dims = 3 if lead else 2
+    if w.dim() != dims or x.dim() != 2:
+        raise ValueError(f"w_packed must be [{lead}N, (K + 1) / 2] and x [M, K]")
+    k = x.shape[1]
+    if not (group_size >= k or (group_size >= 32 and group_size & (group_size - 1) == 0)):
+        raise ValueError("group_size must be a power of two >= 32, or at least K")
+    groups = -(-k // group_size) if group_size > 0 else 0
+    if w.shape[-1] != (k + 1) // 2 or tuple(sc.shape) != (*w.shape[:-1], groups):
+        raise ValueError(f"w_packed must be [{lead}N, (K + 1) / 2] and w_scale [{lead}N, ceil(K / group_size)]")
+    zero = None
+    if w_zero is not None:
+        _require(w_zero, "w_zero")
+        if w_zero.dtype != torch.uint8 or w_zero.shape != sc.shape:
+            raise ValueError("w_zero must be uint8 of w_scale's shape")
+        zero = _ptr(w_zero)
+    return w, sc, zero, x, k
+
+
+def int4_gemm(w_packed: torch.Tensor, w_scale: torch.Tensor, x: torch.Tensor, w_zero: torch.Tensor | None = None,
+              group_size: int = 128, out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+              alpha: float = 1.0, row_scale: torch.Tensor | None = None, col_scale: torch.Tensor | None = None,
+              bias: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+              activation: str = "none") -> torch.Tensor:
+    """out[M, N] = alpha * x[M, K] @ D^T with D = (code - zero) * scale, 4-bit codes
+    packed [N, (K + 1) / 2] (even k in the low nibble), one bfloat16 scale and one uint8
+    zero point (None: 8) per ``group_size`` consecutive k (``qlinear_int4_gemm``);
+    epilogue as ``fp8_gemm``."""
+    w, sc, zero, x, k = _int4_operands(w_packed, w_scale, w_zero, x, group_size, "")
+    m, n = x.shape[0], w.shape[0]
+    out = _out(out, (m, n), out_dtype, x.device)
+    d = _epilogue(m, n, row_scale, col_scale, bias, residual, activation) if m else None
+    if m == 0:
+        return out
+    st = lib.qlinear_int4_gemm(_ptr(w), _ptr(sc), zero, _ptr(x), _ptr(out), _OUT_CODES[out_dtype], m, n, k,
+                               int(group_size), float(alpha), _epi_ref(d), _stream(x))
+    _check(st, "qlinear_int4_gemm")
+    return out
+
+
+def int4_grouped_gemm(w_packed: torch.Tensor, w_scale: torch.Tensor, x: torch.Tensor, a_offsets: torch.Tensor,
+                      expert_ids: torch.Tensor, w_zero: torch.Tensor | None = None, group_size: int = 128,
+                      out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+                      max_tokens_per_group: int | None = None) -> torch.Tensor:
+    """Grouped MoE W4A16 with integer codes (``qlinear_int4_grouped_gemm``): rows
+    a_offsets[z] .. a_offsets[z+1]-1 of x times D_e^T, e = expert_ids[z], D_e as in
+    ``int4_gemm`` from the expert stack w_packed [E, N, (K + 1) / 2], w_scale and w_zero
+    [E, N, ceil(K / group_size)].  Rows outside every group keep whatever ``out`` held
+    (a new ``out`` starts uninitialised)."""
+    w, sc, zero, x, k = _int4_operands(w_packed, w_scale, w_zero, x, group_size, "E, ")
+    _require(a_offsets, "a_offsets")
+    _require(expert_ids, "expert_ids")
+    if a_offsets.dtype not in (torch.int32, torch.uint32) or expert_ids.dtype != torch.int32:
+        raise TypeError("a_offsets must be uint32/int32 and expert_ids int32")
+    g = expert_ids.numel()
+    if a_offsets.numel() != g + 1:
+        raise ValueError("a_offsets needs num_groups + 1 entries")
+    e, n, _ = w.shape
+    t = x.shape[0]
+    if max_tokens_per_group is None:
+        max_tokens_per_group = t
+    out = _out(out, (t, n), out_dtype, x.device)
+    if t == 0:
+        return out
+    st = lib.qlinear_int4_grouped_gemm(_ptr(w), _ptr(sc), zero, _ptr(x), _ptr(a_offsets), _ptr(expert_ids), _ptr(out),
+                                       _OUT_CODES[out_dtype], g, int(max_tokens_per_group), e, t, n, k,
+                                       int(group_size), _stream(x))
+    _check(st, "qlinear_int4_grouped_gemm")
+    return out
+
+
+def _float_tensor(t: torch.Tensor, what: str, shape=None):
+    _require(t, what)
+    if t.dtype not in _OUT_CODES:
+        raise TypeError(f"{what} must be float32 or bfloat16, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _typed(t: torch.Tensor, what: str, dtype: torch.dtype, shape):
+    _require(t, what)
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+
+
+def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, expert_ids: torch.Tensor | None = None,
+              weights: torch.Tensor | None = None):
+    """The top_k experts of every token by logit, largest first, and their softmax
+    weights, over the chosen experts (renormalize) or over all (``qlinear_moe_route``)
+    -> (expert_ids int32 [T, top_k], weights f32 [T, top_k]).  A logit of -inf masks its
+    expert; slots for which no expert is left get id -1 and weight 0."""
+    _float_tensor(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    t, e = logits.shape
+    expert_ids = _out(expert_ids, (t, top_k), torch.int32, logits.device)
+    weights = _out(weights, (t, top_k), torch.float32, logits.device)
+    if t == 0:
+        return expert_ids, weights
+    st = lib.qlinear_moe_route(_ptr(logits), _OUT_CODES[logits.dtype], _ptr(expert_ids), _ptr(weights), t, e,
+                               int(top_k), int(bool(renormalize)), _stream(logits))
+    _check(st, "qlinear_moe_route")
+    return expert_ids, weights
+
+
+def moe_route_backward(logits: torch.Tensor, expert_ids: torch.Tensor, grad_weights: torch.Tensor,
+                       renormalize: bool = True, grad_logits: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of ``moe_route``'s weights with respect to the logits
+    (``qlinear_moe_route_backward``), in the logits' dtype."""
+    _float_tensor(logits, "logits")
+    if logits.dim() != 2 or expert_ids.dim() != 2:
+        raise ValueError("logits must be [T, E] and expert_ids [T, top_k]")
+    t, e = logits.shape
+    k = expert_ids.shape[1]
+    _typed(expert_ids, "expert_ids", torch.int32, (t, k))
+    _typed(grad_weights, "grad_weights", torch.float32, (t, k))
+    grad_logits = _out(grad_logits, (t, e), logits.dtype, logits.device)
+    if t == 0:
+        return grad_logits
+    st = lib.qlinear_moe_route_backward(_ptr(logits), _OUT_CODES[logits.dtype], _ptr(expert_ids), _ptr(grad_weights),
+                                        _ptr(grad_logits), t, e, k, int(bool(renormalize)), _stream(logits))
+    _check(st, "qlinear_moe_route_backward")
+    return grad_logits
+
+
+def moe_sort(expert_ids: torch.Tensor, num_experts: int, workspace: torch.Tensor | None = None):
+    """Stable sort of the slots of expert_ids [T, top_k] by expert (``qlinear_moe_sort``)
+    -> (a_offsets int32 [num_experts + 1], row_slot int32 [T * top_k], slot_row int32
+    [T, top_k]).  Rows a_offsets[e] .. a_offsets[e + 1] - 1 belong to expert e; slots with
+    an id outside 0 .. num_experts - 1 are dropped: they fill the rows behind, and both
+    maps hold the complement (~) for them.  ``workspace``: a device tensor of at least the
+    bytes of ``qlinear_moe_sort_workspace_size`` (None: allocated)."""
+    _require(expert_ids, "expert_ids")
+    if expert_ids.dtype != torch.int32 or expert_ids.dim() != 2:
+        raise TypeError("expert_ids must be int32 [T, top_k]")
+    slots, dev = expert_ids.numel(), expert_ids.device
+    need = _i64(0)
+    _check(lib.qlinear_moe_sort_workspace_size(slots, int(num_experts), ctypes.byref(need)),
+           "qlinear_moe_sort_workspace_size")
+    offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
+    row_slot = torch.empty(slots, dtype=torch.int32, device=dev)
+    slot_row = torch.empty(tuple(expert_ids.shape), dtype=torch.int32, device=dev)
+    if slots == 0:
+        return offsets.zero_(), row_slot, slot_row
+    if workspace is None and need.value > 0:
+        workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
+    nbytes = 0
+    if workspace is not None:
+        _require(workspace, "workspace")
+        nbytes = workspace.numel() * workspace.element_size()
+    st = lib.qlinear_moe_sort(_ptr(expert_ids), _ptr(offsets), _ptr(row_slot), _ptr(slot_row), slots, int(num_experts),
+                              None if workspace is None else _ptr(workspace), nbytes, _stream(expert_ids))
+    _check(st, "qlinear_moe_sort")
+    return offsets, row_slot, slot_row
+
+
+def moe_gather(x: torch.Tensor, slot_row: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Token rows x [T, H] into expert order, [T * top_k, H] (``qlinear_moe_gather``): row
+    slot_row[t, j] is token t; the rows of dropped slots are zeros.  Its gradient is
+    ``moe_combine`` without weights."""
+    _float_tensor(x, "x")
+    if x.dim() != 2 or slot_row.dim() != 2:
+        raise ValueError("x must be [T, H] and slot_row [T, top_k]")
+    t, h = x.shape
+    k = slot_row.shape[1]
+    _typed(slot_row, "slot_row", torch.int32, (t, k))
+    out = _out(out, (t * k, h), x.dtype, x.device)
+    if t == 0:
+        return out
+    st = lib.qlinear_moe_gather(_ptr(x), _ptr(slot_row), _ptr(out), _OUT_CODES[x.dtype], t, k, h, _stream(x))
+    _check(st, "qlinear_moe_gather")
+    return out
+
+
+def moe_combine(rows: torch.Tensor, slot_row: torch.Tensor, weights: torch.Tensor | None = None,
+                out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None) -> torch.Tensor:
+    """Rows in expert order [T * top_k, H] back to tokens [T, H], summed with the router's
+    weights (None: all 1) over the slots that were not dropped (``qlinear_moe_combine``);
+    out_dtype defaults to the rows' dtype."""
+    _float_tensor(rows, "rows")
+    if rows.dim() != 2 or slot_row.dim() != 2:
+        raise ValueError("rows must be [T * top_k, H] and slot_row [T, top_k]")
+    t, k = slot_row.shape
+    _typed(slot_row, "slot_row", torch.int32, (t, k))
+    h = rows.shape[1]
+    _float_tensor(rows, "rows", (t * k, h))
+    if weights is not None:
+        _typed(weights, "weights", torch.float32, (t, k))
+    out_dtype = rows.dtype if out_dtype is None else out_dtype
+    if out_dtype not in _OUT_CODES:
+        raise TypeError("out_dtype must be float32 or bfloat16")
+    out = _out(out, (t, h), out_dtype, rows.device)
+    if t == 0:
+        return out
+    st = lib.qlinear_moe_combine(_ptr(rows), _OUT_CODES[rows.dtype], _ptr(slot_row),
+                                 None if weights is None else _ptr(weights), _ptr(out), _OUT_CODES[out_dtype], t, k, h,
+                                 _stream(rows))
+    _check(st, "qlinear_moe_combine")
+    return out
+
+
+def moe_combine_backward(grad_out: torch.Tensor, rows: torch.Tensor, slot_row: torch.Tensor, weights: torch.Tensor,
+                         grad_rows: torch.Tensor | None = None, grad_weights: torch.Tensor | None = None):
+    """Gradients of ``moe_combine`` (``qlinear_moe_combine_backward``) -> (grad_rows
+    [T * top_k, H] in the rows' dtype, grad_weights f32 [T, top_k])."""
+    _float_tensor(grad_out, "grad_out")
+    if grad_out.dim() != 2 or slot_row.dim() != 2:
+        raise ValueError("grad_out must be [T, H] and slot_row [T, top_k]")
+    t, h = grad_out.shape
+    k = slot_row.shape[1]
+    _typed(slot_row, "slot_row", torch.int32, (t, k))
+    _typed(rows, "rows", grad_out.dtype, (t * k, h))
+    _typed(weights, "weights", torch.float32, (t, k))
+    grad_rows = _out(grad_rows, (t * k, h), rows.dtype, rows.device)
+    grad_weights = _out(grad_weights, (t, k), torch.float32, rows.device)
+    if t == 0:
+        return grad_rows, grad_weights
+    st = lib.qlinear_moe_combine_backward(_ptr(grad_out), _ptr(rows), _OUT_CODES[rows.dtype], _ptr(slot_row),
+                                          _ptr(weights), _ptr(grad_rows), _ptr(grad_weights), t, k, h, _stream(rows))
+    _check(st, "qlinear_moe_combine_backward")
+    return grad_rows, grad_weights
+
+
+def swiglu(x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """silu(x[:, :F]) * x[:, F:] of x [M, 2F] (``qlinear_swiglu``)."""
+    _float_tensor(x, "x")
+    if x.dim() != 2 or x.shape[1] % 2 != 0:
+        raise ValueError("x must be [M, 2F]")
+    m, f = x.shape[0], x.shape[1] // 2
+    out = _out(out, (m, f), x.dtype, x.device)
+    if m == 0:
+        return out
+    st = lib.qlinear_swiglu(_ptr(x), _ptr(out), _OUT_CODES[x.dtype], m, f, _stream(x))
+    _check(st, "qlinear_swiglu")
+    return out
+
+
+def swiglu_backward(grad_y: torch.Tensor, x: torch.Tensor, grad_x: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of ``swiglu`` with respect to x [M, 2F] (``qlinear_swiglu_backward``)."""
+    _float_tensor(x, "x")
+    if x.dim() != 2 or x.shape[1] % 2 != 0:
+        raise ValueError("x must be [M, 2F]")
+    m, f = x.shape[0], x.shape[1] // 2
+    _typed(grad_y, "grad_y", x.dtype, (m, f))
+    grad_x = _out(grad_x, (m, 2 * f), x.dtype, x.device)
+    if m == 0:
+        return grad_x
+    st = lib.qlinear_swiglu_backward(_ptr(grad_y), _ptr(x), _ptr(grad_x), _OUT_CODES[x.dtype], m, f, _stream(x))
+    _check(st, "qlinear_swiglu_backward")
+    return grad_x

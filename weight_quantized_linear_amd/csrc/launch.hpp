@@ -169,4 +169,31 @@ hipError_t launch_int8_gemm(const int8_t* a, const int8_t* b, const float* a_sca
 hipError_t launch_fp8_materialize(const uint8_t* w, void* out, int out_bf16, int64_t count,
                                   hipStream_t s);
 
+// int4.hip: integer codes with group scales (zero: null for 8).
+hipError_t launch_int4_gemm(const uint8_t* w, const uint16_t* scale, const uint8_t* zero, const uint16_t* x, void* out,
+                            int out_bf16, int64_t M, int64_t N, int64_t K, int64_t group, float alpha, int num_cus,
+                            hipStream_t s, const Epilogue& epi);
+hipError_t launch_int4_grouped(const uint8_t* w, const uint16_t* scale, const uint8_t* zero, const uint16_t* x,
+                               const uint32_t* a_offsets, const int32_t* expert_ids, void* out, int out_bf16,
+                               int64_t G, int64_t E, int64_t T, int64_t N, int64_t K, int64_t group, int num_cus,
+                               hipStream_t s);
+
+// moe.hip
+hipError_t launch_moe_route(const void* logits, int bf16, int32_t* ids, float* weights, int64_t T, int64_t E,
+                            int64_t top_k, int renorm, hipStream_t s);
+hipError_t launch_moe_route_backward(const void* logits, int bf16, const int32_t* ids, const float* dw, void* dlogits,
+                                     int64_t T, int64_t E, int64_t top_k, int renorm, hipStream_t s);
+size_t moe_sort_ws_bytes(int64_t S, int64_t E);
+hipError_t launch_moe_sort(const int32_t* ids, int32_t* offsets, int32_t* row_slot, int32_t* slot_row, int64_t S,
+                           int64_t E, int32_t* ws, hipStream_t s);
+hipError_t launch_moe_gather(const void* x, const int32_t* slot_row, void* out, int bf16, int64_t T, int64_t top_k,
+                             int64_t H, hipStream_t s);
+hipError_t launch_moe_combine(const void* rows, int bf16, const int32_t* slot_row, const float* weights, void* out,
+                              int out_bf16, int64_t T, int64_t top_k, int64_t H, hipStream_t s);
+hipError_t launch_moe_combine_backward(const void* dy, const void* rows, int bf16, const int32_t* slot_row,
+                                       const float* weights, void* drows, float* dweights, int64_t T, int64_t top_k,
+                                       int64_t H, hipStream_t s);
+// dy null: the activation; else its gradient.
+hipError_t launch_swiglu(const void* x, const void* dy, void* out, int bf16, int64_t M, int64_t F, hipStream_t s);
+
 }  // namespace qlinear

@@ -281,6 +281,21 @@ int bf16_gemm_impl(const void* w, const void* x, void* out, int out_dtype, int64
                                   size_t(ws_bytes), s, epi));
 }
 
+// int4 groups: a power of two >= 32, or one group per row.
+bool int4_group_ok(int64_t g, int64_t K) { return g >= K || (g >= 32 && (g & (g - 1)) == 0); }
+
+// Limits of the expert calls: the router keeps a token's logits in one wave's
+// registers and pick j in lane j; slots and rows are int32.
+constexpr int64_t kMaxRouted = 1024, kMaxTopK = 64, kMaxSlots = std::numeric_limits<int32_t>::max();
+
+bool permute_sizes_ok(int64_t T, int64_t top_k, int64_t H) {
+  return T >= 0 && top_k >= 1 && top_k <= kMaxTopK && T <= kMaxSlots / top_k && H > 0 && fits(T ? T : 1, top_k, H);
+}
+
+bool route_sizes_ok(int64_t T, int64_t E, int64_t top_k) {
+  return E >= 1 && E <= kMaxRouted && top_k <= E && permute_sizes_ok(T, top_k, E);
+}
+
 }  // namespace
 
 extern "C" {
@@ -558,6 +573,166 @@ int qlinear_bf16_gemm_ws(const void* w, const void* x, void* out, int out_dtype,
                          float alpha, const qlinear_epilogue* epilogue, int path, void* workspace,
                          int64_t workspace_bytes, void* stream) {
   return bf16_gemm_impl(w, x, out, out_dtype, M, N, K, alpha, path, workspace, workspace_bytes, stream, epilogue);
+}
+
+int qlinear_int4_gemm(const void* w_packed, const void* w_scale, const void* w_zero, const void* x, void* out,
+                      int out_dtype, int64_t M, int64_t N, int64_t K, int64_t group_size, float alpha,
+                      const qlinear_epilogue* epilogue, void* stream) {
+  if (!w_packed || !w_scale || !x || !out) return QLINEAR_ERR_INVALID_ARG;
+  if (M < 0 || N <= 0 || K <= 0 || !int4_group_ok(group_size, K) || !fits(N, K) || !fits(M ? M : 1, K) ||
+      !fits(M ? M : 1, N))
+    return QLINEAR_ERR_INVALID_ARG;
+  if (!float_out_ok(out_dtype) || !aligned(x, 2) || !aligned(w_scale, 2) || !aligned(out, out_size(out_dtype)))
+    return QLINEAR_ERR_INVALID_ARG;
+  Epilogue epi;
+  if (int st = to_epilogue(epilogue, M ? M : 1, N, &epi)) return st;
+  int num_cus = 0;
+  if (int st = current_device(&num_cus)) return st;
+  if (M == 0) return QLINEAR_OK;
+  return finish(launch_int4_gemm(static_cast<const uint8_t*>(w_packed), static_cast<const uint16_t*>(w_scale),
+                                 static_cast<const uint8_t*>(w_zero), static_cast<const uint16_t*>(x), out,
+                                 out_dtype == QLINEAR_BF16, M, N, K, group_size, alpha, num_cus,
+                                 static_cast<hipStream_t>(stream), epi));
+}
+
+int qlinear_int4_grouped_gemm(const void* w_packed, const void* w_scale, const void* w_zero, const void* x,
+                              const uint32_t* a_offsets, const int32_t* expert_ids, void* out, int out_dtype,
+                              int64_t num_groups, int64_t max_tokens_per_group, int64_t num_experts, int64_t T,
+                              int64_t N, int64_t K, int64_t group_size, void* stream) {
+  if (!w_packed || !w_scale || !x || !a_offsets || !expert_ids || !out) return QLINEAR_ERR_INVALID_ARG;
+  // The kernel counts row tiles (at most T + num_groups) in int32.
+  if (num_groups <= 0 || num_groups > 65535 || max_tokens_per_group < 0 || num_experts <= 0 || T < 0 ||
+      T > (int64_t(1) << 30) || N <= 0 || K <= 0 || !int4_group_ok(group_size, K))
+    return QLINEAR_ERR_INVALID_ARG;
+  if (!fits(num_experts, N, K) || !fits(T ? T : 1, K) || !fits(T ? T : 1, N)) return QLINEAR_ERR_INVALID_ARG;
+  if (!float_out_ok(out_dtype) || !aligned(x, 2) || !aligned(w_scale, 2) || !aligned(out, out_size(out_dtype)) ||
+      !aligned(a_offsets, 4) || !aligned(expert_ids, 4))
+    return QLINEAR_ERR_INVALID_ARG;
+  int num_cus = 0;
+  if (int st = current_device(&num_cus)) return st;
+  if (T == 0) return QLINEAR_OK;
+  return finish(launch_int4_grouped(static_cast<const uint8_t*>(w_packed), static_cast<const uint16_t*>(w_scale),
+                                    static_cast<const uint8_t*>(w_zero), static_cast<const uint16_t*>(x), a_offsets,
+                                    expert_ids, out, out_dtype == QLINEAR_BF16, num_groups, num_experts, T, N, K,
+                                    group_size, num_cus, static_cast<hipStream_t>(stream)));
+}
+
+int qlinear_moe_route(const void* logits, int logits_dtype, int32_t* expert_ids, float* weights, int64_t T, int64_t E,
+                      int64_t top_k, int renormalize, void* stream) {
+  if (!logits || !expert_ids || !weights || !route_sizes_ok(T, E, top_k) || !float_out_ok(logits_dtype))
+    return QLINEAR_ERR_INVALID_ARG;
+  if (!aligned(logits, out_size(logits_dtype)) || !aligned(expert_ids, 4) || !aligned(weights, 4))
+    return QLINEAR_ERR_INVALID_ARG;
+  int num_cus = 0;
+  if (int st = current_device(&num_cus)) return st;
+  if (T == 0) return QLINEAR_OK;
+  return finish(launch_moe_route(logits, logits_dtype == QLINEAR_BF16, expert_ids, weights, T, E, top_k,
+                                 renormalize != 0, static_cast<hipStream_t>(stream)));
+}
+
+int qlinear_moe_route_backward(const void* logits, int logits_dtype, const int32_t* expert_ids,
+                               const float* grad_weights, void* grad_logits, int64_t T, int64_t E, int64_t top_k,
+                               int renormalize, void* stream) {
+  if (!logits || !expert_ids || !grad_weights || !grad_logits || !route_sizes_ok(T, E, top_k) ||
+      !float_out_ok(logits_dtype))
+    return QLINEAR_ERR_INVALID_ARG;
+  if (!aligned(logits, out_size(logits_dtype)) || !aligned(grad_logits, out_size(logits_dtype)) ||
+      !aligned(expert_ids, 4) || !aligned(grad_weights, 4))
+    return QLINEAR_ERR_INVALID_ARG;
+  int num_cus = 0;
+  if (int st = current_device(&num_cus)) return st;
+  if (T == 0) return QLINEAR_OK;
+  return finish(launch_moe_route_backward(logits, logits_dtype == QLINEAR_BF16, expert_ids, grad_weights, grad_logits,
+                                          T, E, top_k, renormalize != 0, static_cast<hipStream_t>(stream)));
+}
+
+int qlinear_moe_sort_workspace_size(int64_t slots, int64_t num_experts, int64_t* bytes) {
+  if (!bytes) return QLINEAR_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (slots < 0 || slots > kMaxSlots || num_experts <= 0 || num_experts > kMaxRouted) return QLINEAR_ERR_INVALID_ARG;
+  *bytes = int64_t(moe_sort_ws_bytes(slots, num_experts));
+  return QLINEAR_OK;
+}
+
+int qlinear_moe_sort(const int32_t* expert_ids, uint32_t* a_offsets, int32_t* row_slot, int32_t* slot_row,
+                     int64_t slots, int64_t num_experts, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!expert_ids || !a_offsets || !row_slot || !slot_row) return QLINEAR_ERR_INVALID_ARG;
+  int64_t need = 0;
+  if (int st = qlinear_moe_sort_workspace_size(slots, num_experts, &need)) return st;
+  if (int st = check_workspace(workspace, workspace_bytes)) return st;
+  if (workspace_bytes < need || !aligned(expert_ids, 4) || !aligned(a_offsets, 4) || !aligned(row_slot, 4) ||
+      !aligned(slot_row, 4))
+    return QLINEAR_ERR_INVALID_ARG;
+  int num_cus = 0;
+  if (int st = current_device(&num_cus)) return st;
+  return finish(launch_moe_sort(expert_ids, reinterpret_cast<int32_t*>(a_offsets), row_slot, slot_row, slots,
+                                num_experts, static_cast<int32_t*>(workspace), static_cast<hipStream_t>(stream)));
+}
+
+int qlinear_moe_gather(const void* x, const int32_t* slot_row, void* out, int dtype, int64_t T, int64_t top_k,
+                       int64_t H, void* stream) {
+  if (!x || !slot_row || !out || !permute_sizes_ok(T, top_k, H) || !float_out_ok(dtype))
+    return QLINEAR_ERR_INVALID_ARG;
+  if (!aligned(x, out_size(dtype)) || !aligned(out, out_size(dtype)) || !aligned(slot_row, 4))
+    return QLINEAR_ERR_INVALID_ARG;
+  int num_cus = 0;
+  if (int st = current_device(&num_cus)) return st;
+  if (T == 0) return QLINEAR_OK;
+  return finish(launch_moe_gather(x, slot_row, out, dtype == QLINEAR_BF16, T, top_k, H,
+                                  static_cast<hipStream_t>(stream)));
+}
+
+int qlinear_moe_combine(const void* rows, int rows_dtype, const int32_t* slot_row, const float* weights, void* out,
+                        int out_dtype, int64_t T, int64_t top_k, int64_t H, void* stream) {
+  if (!rows || !slot_row || !out || !permute_sizes_ok(T, top_k, H) || !float_out_ok(rows_dtype) ||
+      !float_out_ok(out_dtype))
+    return QLINEAR_ERR_INVALID_ARG;
+  if (!aligned(rows, out_size(rows_dtype)) || !aligned(out, out_size(out_dtype)) || !aligned(slot_row, 4) ||
+      (weights && !aligned(weights, 4)))
+    return QLINEAR_ERR_INVALID_ARG;
+  int num_cus = 0;
+  if (int st = current_device(&num_cus)) return st;
+  if (T == 0) return QLINEAR_OK;
+  return finish(launch_moe_combine(rows, rows_dtype == QLINEAR_BF16, slot_row, weights, out,
+                                   out_dtype == QLINEAR_BF16, T, top_k, H, static_cast<hipStream_t>(stream)));
+}
+
+int qlinear_moe_combine_backward(const void* grad_out, const void* rows, int dtype, const int32_t* slot_row,
+                                 const float* weights, void* grad_rows, float* grad_weights, int64_t T, int64_t top_k,
+                                 int64_t H, void* stream) {
+  if (!grad_out || !rows || !slot_row || !weights || !grad_rows || !grad_weights || !permute_sizes_ok(T, top_k, H) ||
+      !float_out_ok(dtype))
+    return QLINEAR_ERR_INVALID_ARG;
+  const size_t es = out_size(dtype);
+  if (!aligned(grad_out, es) || !aligned(rows, es) || !aligned(grad_rows, es) || !aligned(slot_row, 4) ||
+      !aligned(weights, 4) || !aligned(grad_weights, 4))
+    return QLINEAR_ERR_INVALID_ARG;
+  int num_cus = 0;
+  if (int st = current_device(&num_cus)) return st;
+  if (T == 0) return QLINEAR_OK;
+  return finish(launch_moe_combine_backward(grad_out, rows, dtype == QLINEAR_BF16, slot_row, weights, grad_rows,
+                                            grad_weights, T, top_k, H, static_cast<hipStream_t>(stream)));
+}
+
+int qlinear_swiglu(const void* x, void* y, int dtype, int64_t M, int64_t F, void* stream) {
+  if (!x || !y || M < 0 || F <= 0 || !fits(M ? M : 1, F) || !float_out_ok(dtype)) return QLINEAR_ERR_INVALID_ARG;
+  if (!aligned(x, out_size(dtype)) || !aligned(y, out_size(dtype))) return QLINEAR_ERR_INVALID_ARG;
+  int num_cus = 0;
+  if (int st = current_device(&num_cus)) return st;
+  if (M == 0) return QLINEAR_OK;
+  return finish(launch_swiglu(x, nullptr, y, dtype == QLINEAR_BF16, M, F, static_cast<hipStream_t>(stream)));
+}
+
+int qlinear_swiglu_backward(const void* grad_y, const void* x, void* grad_x, int dtype, int64_t M, int64_t F,
+                            void* stream) {
+  if (!grad_y || !x || !grad_x || M < 0 || F <= 0 || !fits(M ? M : 1, F) || !float_out_ok(dtype))
+    return QLINEAR_ERR_INVALID_ARG;
+  const size_t es = out_size(dtype);
+  if (!aligned(grad_y, es) || !aligned(x, es) || !aligned(grad_x, es)) return QLINEAR_ERR_INVALID_ARG;
+  int num_cus = 0;
+  if (int st = current_device(&num_cus)) return st;
+  if (M == 0) return QLINEAR_OK;
+  return finish(launch_swiglu(x, grad_y, grad_x, dtype == QLINEAR_BF16, M, F, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
