@@ -471,7 +471,7 @@ int qlinear_int8_grouped_gemm(const void* a, const void* b, const float* a_scale
  * or NULL (every zero point 8), G = ceil(K / g) groups of g = group_size
  * consecutive k, the last one shorter where K % g != 0.  group_size is a
  * power of two >= 32, or any value >= K (one group per row).  x: bfloat16
- * [M, K]; out: [M, N] of out_dtype (F32 or BF16); any K >= 1.  w_packed and
+ * [M, K]; out: [M, N] of out_dtype (F32 or BF16); 1 <= K < 2^23.  w_packed and
  * w_zero need no alignment, the others that of their type.  Each group is
  * summed in float32 over exact products and scaled then, so no weight is
  * rounded.  alpha and `epilogue` (NULL = none) as in qlinear_fp8_gemm_ws.

@@ -135,6 +135,13 @@ def test_int4_refusals(q):
         assert q.lib.qlinear_int4_grouped_gemm(*a) == q.ERR_INVALID_ARG, (i, bad)
 
 
+def test_int4_refuses_a_k_of_2_to_23(q):
+    a = [FAKE, FAKE, None, FAKE, FAKE, 0, 4, 8, 1 << 23, 1 << 23, 1.0, None, None]
+    assert q.lib.qlinear_int4_gemm(*a) == q.ERR_INVALID_ARG
+    a = [FAKE, FAKE, None, FAKE, FAKE, FAKE, FAKE, 0, 2, 4, 3, 4, 8, 1 << 23, 32, None]
+    assert q.lib.qlinear_int4_grouped_gemm(*a) == q.ERR_INVALID_ARG
+
+
 def test_moe_refusals(q):
     L, bad_arg = q.lib, q.ERR_INVALID_ARG
 

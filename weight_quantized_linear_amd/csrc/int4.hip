@@ -37,6 +37,41 @@ struct __attribute__((packed, aligned(2))) Halves16 {
 __device__ __forceinline__ u32x4 ldw16(const uint8_t* p) { return reinterpret_cast<const Bytes16*>(p)->v; }
 __device__ __forceinline__ u32x4 ldx16(const uint16_t* p) { return reinterpret_cast<const Halves16*>(p)->v; }
 
+template <typename T> struct __attribute__((packed, aligned(1))) Packed1 {
+  T v;
+};
+template <typename T> struct __attribute__((packed, aligned(2))) Packed2 {
+  T v;
+};
+template <typename T> __device__ __forceinline__ T ld_any1(const void* p) {
+  return reinterpret_cast<const Packed1<T>*>(p)->v;
+}
+template <typename T> __device__ __forceinline__ T ld_any2(const void* p) {
+  return reinterpret_cast<const Packed2<T>*>(p)->v;
+}
+
+// The first `left` (< 16) bytes at p, zeros behind: at most four loads, all in flight together.
+__device__ __forceinline__ u32x4 ld_bytes(const uint8_t* p, int left) {
+  left = left < 0 ? 0 : left;
+  uint64_t a = 0, rest = 0;
+  if (left & 8) a = ld_any1<uint64_t>(p);
+  if (left & 4) rest = ld_any1<uint32_t>(p + (left & 8));
+  if (left & 2) rest |= uint64_t(ld_any1<uint16_t>(p + (left & 12))) << (8 * (left & 4));
+  if (left & 1) rest |= uint64_t(p[left & 14]) << (8 * (left & 6));
+  const uint64_t lo = (left & 8) ? a : rest, hi = (left & 8) ? rest : 0;
+  return u32x4{uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32)};
+}
+// The first `left` (< 8) 16-bit values at p, zeros behind.
+__device__ __forceinline__ u32x4 ld_halves(const uint16_t* p, int left) {
+  left = left < 0 ? 0 : left;
+  uint64_t a = 0, rest = 0;
+  if (left & 4) a = ld_any2<uint64_t>(p);
+  if (left & 2) rest = ld_any2<uint32_t>(p + (left & 4));
+  if (left & 1) rest |= uint64_t(p[left & 6]) << (16 * (left & 2));
+  const uint64_t lo = (left & 4) ? a : rest, hi = (left & 4) ? rest : 0;
+  return u32x4{uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32)};
+}
+
 // Eight codes of a dword -> bfloat16 in the order 0 2 4 6 1 3 5 7.
 __device__ __forceinline__ u32x4 int4x8_to_bf16x8(uint32_t w) {
   const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
@@ -75,128 +110,7 @@ struct Int4Args {
 
 __device__ __forceinline__ float zero_at(const Int4Args& a, int64_t i) { return a.zero ? float(a.zero[i]) : 8.f; }
 
-// ---------------------------------------------------------------- GEMV
-
-// 1 <= M <= 4 on the vector ALU.  Each wave owns ROWS weight rows; lane l
-// takes the 32-code chunks c = l, l + 64, ... (16 bytes, inside one group),
-// U of them in flight.  The at most 31 codes behind the last whole chunk are
-// taken one per lane.
-template <int M, int ROWS, int U>
-__global__ __launch_bounds__(256) void int4_gemv_kernel(Int4Args a, const uint16_t* __restrict__ x,
-                                                        void* __restrict__ out, int out_bf16, int64_t N, int64_t K,
-                                                        float alpha, Epilogue epi) {
-  const int lane = threadIdx.x & (kWave - 1);
-  const int64_t wave = int64_t(blockIdx.x) * (blockDim.x / kWave) + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int64_t row0 = wave * ROWS;
-  if (row0 >= N) return;  // uniform per wave
-  const int64_t nchunks = K >> 5;
-  int64_t row[ROWS];
-#pragma unroll
-  for (int r = 0; r < ROWS; ++r) row[r] = row0 + r < N ? row0 + r : N - 1;  // tail rows re-read the last, never stored
-
-  float acc[M][ROWS];
-#pragma unroll
-  for (int m = 0; m < M; ++m)
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) acc[m][r] = 0.f;
-
-  for (int64_t c0 = 0; c0 < nchunks; c0 += int64_t(kWave) * U) {
-    u32x4 wv[U][ROWS];
-    float sv[U][ROWS], zv[U][ROWS];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t c = c0 + int64_t(u) * kWave + lane;
-      const bool ok = c < nchunks;
-      const int64_t g = (c << 5) >> a.shift;
-#pragma unroll
-      for (int r = 0; r < ROWS; ++r) {
-        wv[u][r] = ok ? ldw16(a.w + row[r] * a.row_bytes + c * 16) : u32x4{0u, 0u, 0u, 0u};
-        sv[u][r] = ok ? bf16_to_f32(a.scale[row[r] * a.groups + g]) : 0.f;
-        zv[u][r] = ok ? zero_at(a, row[r] * a.groups + g) : 0.f;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t c = c0 + int64_t(u) * kWave + lane;
-      const bool ok = c < nchunks;
-      u32x4 xv[M][4];
-      float xs[M];
-#pragma unroll
-      for (int m = 0; m < M; ++m) {
-        xs[m] = 0.f;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          xv[m][q] = decoder_order(ok ? ldx16(x + m * K + c * 32 + 8 * q) : u32x4{0u, 0u, 0u, 0u});
-          xs[m] = sum8(xv[m][q], xs[m]);
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < ROWS; ++r) {
-        float part[M];
-#pragma unroll
-        for (int m = 0; m < M; ++m) part[m] = 0.f;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const u32x4 codes = int4x8_to_bf16x8(wv[u][r][q]);
-#pragma unroll
-          for (int m = 0; m < M; ++m) part[m] = dot8(codes, xv[m][q], part[m]);
-        }
-#pragma unroll
-        for (int m = 0; m < M; ++m) acc[m][r] = fmaf(sv[u][r], fmaf(-zv[u][r], xs[m], part[m]), acc[m][r]);
-      }
-    }
-  }
-  const int64_t k = (nchunks << 5) + lane;
-  if (k < K) {
-    const int64_t g = k >> a.shift;
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      const uint32_t byte = a.w[row[r] * a.row_bytes + (k >> 1)];
-      const float code = float((k & 1) ? byte >> 4 : byte & 15u);
-      const float d = bf16_to_f32(a.scale[row[r] * a.groups + g]) * (code - zero_at(a, row[r] * a.groups + g));
-#pragma unroll
-      for (int m = 0; m < M; ++m) acc[m][r] = fmaf(d, bf16_to_f32(x[m * K + k]), acc[m][r]);
-    }
-  }
-#pragma unroll
-  for (int m = 0; m < M; ++m)
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      const float t = wave_sum(acc[m][r]);
-      if (lane == 0 && row0 + r < N) store_epi(out, m, row0 + r, N, t, alpha, out_bf16, epi);
-    }
-}
-
-// ---------------------------------------------------------------- matrix-core tile
-
-// A block computes BM = 16 MT rows by BN = 16 NT WN columns with 16x16x32
-// MFMA; WN waves stand side by side along N (each weight byte is read by one
-// wave, straight into its registers), WK waves split the 128-value strips of
-// K between them and add their tiles at the end.
-//
-// Weights: lane (n = l % 16, quarter h = l / 16) reads the 16 bytes k = 32 h
-// .. 32 h + 31 of its row's strip.  Two half-wave swap stages transpose the
-// 4x4 dwords over the quarters, after which dword t holds k = 32 t + 8 h ..
-// + 7: MFMA step t covers 32 consecutive k, so a group of 32 is a whole step.
-// Activation: the strip [BM][128] goes through registers into LDS in the
-// decoder's order (16-byte chunks XOR-permuted by row against bank
-// conflicts), and with it the float32 sum of each row over each group.
-// After the last step of a group: acc += scale * (group - zero * sum).
-constexpr int kStrip = 128;
-
-template <int MT, int NT, int WN, int WK> struct Int4Tile {
-  static constexpr int kBM = 16 * MT, kBN = 16 * NT * WN, kThreads = 64 * WN * WK;
-  static constexpr int kStagers = WK > 1 ? 64 : 64 * WN;  // threads that fill one activation buffer
-  static constexpr int kChunks = kBM * 16 / kStagers;     // 16-byte chunks per staging thread
-  static constexpr int kXBytes = kBM * kStrip * 2;
-  static constexpr int kBufs = WK > 1 ? 1 : 2;            // private buffers need no second one
-  static constexpr int kSumBytes = kBM * 4 * 4;           // [group of the strip][BM] float32
-  static constexpr int kOne = kXBytes + kSumBytes;
-  static constexpr int kRing = kOne * (WK > 1 ? WK : kBufs);
-  static constexpr int kReduce = WK > 1 ? WK * 64 * MT * NT * 16 : 0;
-  static constexpr int kLds = kRing > kReduce ? kRing : kReduce;
-  static_assert(WK == 1 || WN == 1, "either the columns or K are split over the waves");
-};
+constexpr int kStrip = 128;  // values of k that the four quarters of a wave take with one 16-byte load each
 
 // 4x4 transpose of dwords between register index and lane quarter.
 __device__ __forceinline__ u32x4 transpose_quarters(u32x4 v) {
@@ -206,6 +120,399 @@ __device__ __forceinline__ u32x4 transpose_quarters(u32x4 v) {
   const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
   return u32x4{c[0], c[1], d[0], d[1]};
 }
+
+// ---------------------------------------------------------------- streaming products of few rows
+
+// 1 <= M <= 16 rows of x: the weight is read once, straight into registers,
+// and the matrix cores contract it, so that a code costs its decoding alone
+// (7 vector instructions per 8 codes; the dot products would be 4 more).
+//
+// A wave owns NT tiles of 16 weight rows; lane (n = l % 16, quarter q = l / 16)
+// reads 16-byte chunks (32 codes) of row n, chunk 4 s + q of strip s, four
+// strips (a step of 512 codes) at a time.  The 16x16x32 MFMA takes codes as
+// its column operand: column n, and quarter q's 8 of 32 k slots hold dword t of
+// the lane's chunk.  The slots' order is free as long as x has the same.
+//
+// M <= 4 (kMasked): row 4 g + m of the other operand is x row m in the slots of
+// quarter g and zero elsewhere.  Four MFMAs then leave in lane (n, g) the
+// sum over that lane's own chunk for each m, to be scaled with the
+// lane's own group, whatever the group size: no lane exchanges, and only M of the
+// 4 results per lane to correct.  The quarters are added at the end.
+//
+// M <= 16 (!kMasked): row m is x row m; results of a group are complete only
+// over all quarters, so for groups below 128 the four dwords are transposed over
+// the quarters first, which makes MFMA t cover 32 consecutive k.
+//
+// x (decoder's order) and its sums over 32 or a group's values lie in LDS, kChunkK
+// values of k at a time; WK waves split the steps of a chunk and add their
+// sums through LDS at the end, where there are too few rows to fill the card.
+
+constexpr int kStep = 512;  // codes per lane quarter set and step: 4 strips
+
+template <int M, int NT, int WN, int WK> struct StreamLayout {
+  static constexpr bool kMasked = M <= 4;
+  static constexpr int kWaves = WN * WK, kThreads = 64 * kWaves;
+  static constexpr int kRows = kMasked ? M : 16;
+  static constexpr int kChunkK = kMasked ? 4096 : WK > 2 ? kStep * WK : 1024;
+  static constexpr int kZeros = kMasked ? 1024 : 0;  // what the rows outside a quarter read
+  static constexpr int kRowBytes = kChunkK * 2 + 16;
+  static constexpr int kSums = kZeros + kRows * kRowBytes;  // float32: masked [M][chunk / 32], else [chunk / 32][16]
+  static constexpr int kReduce = kWaves * NT * (kMasked ? M * 16 : 256) * 4;
+  static constexpr int kUse = kSums + kRows * (kChunkK / 32) * 4;
+  static constexpr int kLds = kUse > kReduce ? kUse : kReduce;
+  static constexpr int kAcc = kMasked ? M : 4;
+};
+
+// What a lane holds of one step of one row tile.  SH = log2(group) for 5, 6, 7;
+// 8 stands for all larger groups.  The scales and zero points of a step's groups
+// are neighbours in memory and come in one or two loads.
+template <int SH> struct StreamScales;
+template <> struct StreamScales<5> {
+  u32x4 s[2], z;
+};
+template <> struct StreamScales<6> {
+  u32x4 s;
+  u32x2 z;
+};
+template <> struct StreamScales<7> {
+  u32x2 s;
+  uint32_t z;
+};
+template <> struct StreamScales<8> {
+  uint16_t s[4];
+  uint8_t z[4];
+};
+
+template <int SH>
+__device__ __forceinline__ void load_scales(StreamScales<SH>& o, const Int4Args& a, int64_t row, int64_t step) {
+  if constexpr (SH == 8) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t g = row + ((step * kStep + u * kStrip) >> a.shift);
+      o.s[u] = a.scale[g];
+      o.z[u] = a.zero ? a.zero[g] : uint8_t(8);
+    }
+  } else {
+    const int64_t g = row + (step << (9 - SH));
+    const uint32_t eight = 0x08080808u;
+    if constexpr (SH == 5) {
+      o.s[0] = ld_any2<u32x4>(a.scale + g);
+      o.s[1] = ld_any2<u32x4>(a.scale + g + 8);
+      o.z = a.zero ? ld_any1<u32x4>(a.zero + g) : u32x4{eight, eight, eight, eight};
+    } else if constexpr (SH == 6) {
+      o.s = ld_any2<u32x4>(a.scale + g);
+      o.z = a.zero ? ld_any1<u32x2>(a.zero + g) : u32x2{eight, eight};
+    } else {
+      o.s = ld_any2<u32x2>(a.scale + g);
+      o.z = a.zero ? ld_any1<uint32_t>(a.zero + g) : eight;
+    }
+  }
+}
+
+// Scale and zero point of 32-code chunk c of strip u of the step.
+template <int SH>
+__device__ __forceinline__ void pick_scale(const StreamScales<SH>& o, int u, int c, float& s, float& z) {
+  if constexpr (SH == 8) {
+    s = bf16_to_f32(o.s[u]);
+    z = float(o.z[u]);
+  } else {
+    constexpr uint32_t kLow = 0x01000C0Cu, kHigh = 0x03020C0Cu;  // half of a dword into the upper half
+    uint32_t d;
+    if constexpr (SH == 5) {
+      d = (c & 2) ? o.s[u >> 1][2 * (u & 1) + 1] : o.s[u >> 1][2 * (u & 1)];
+      d = __builtin_amdgcn_perm(d, d, (c & 1) ? kHigh : kLow);
+      z = float((o.z[u] >> (8 * c)) & 255u);
+    } else if constexpr (SH == 6) {
+      d = o.s[u];
+      d = __builtin_amdgcn_perm(d, d, (c & 2) ? kHigh : kLow);
+      z = float(((o.z[u >> 1] >> (16 * (u & 1))) >> (4 * (c & 2))) & 255u);
+    } else {
+      d = (u & 1) ? o.s[u >> 1] & 0xFFFF0000u : o.s[u >> 1] << 16;
+      z = float((o.z >> (8 * u)) & 255u);
+    }
+    s = __uint_as_float(d);
+  }
+}
+
+// store(m, n, value): m < rows, n relative to the block's first row of weights.
+template <int M, int NT, int WN, int WK, int SH, typename Store>
+__device__ __forceinline__ void int4_stream_tile(char* lds, const Int4Args& a, const uint16_t* __restrict__ x, int rows,
+                                                 int64_t N, int64_t K, int64_t n0, Store&& store) {
+  using L = StreamLayout<M, NT, WN, WK>;
+  constexpr bool kMasked = L::kMasked;
+  // MFMAs per group inside a strip when the dwords are transposed.
+  constexpr int GS = SH == 5 ? 1 : SH == 6 ? 2 : 4;
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int ln = lane & 15, quarter = lane >> 4;
+  const int wn = wave / WK, wk = wave % WK;
+
+  const uint8_t* wrow[NT];
+  int64_t srow[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    int64_t n = n0 + (wn * NT + i) * 16 + ln;
+    n = n < N ? n : N - 1;  // rows past N re-read the last, never stored
+    wrow[i] = a.w + n * a.row_bytes + quarter * 16;
+    srow[i] = n * a.groups;
+  }
+  const int64_t steps = K / kStep;  // whole ones
+
+  struct Step {
+    u32x4 w[NT][4];
+    StreamScales<SH> sc[NT];
+  };
+  auto fetch = [&](Step& f, int64_t step) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) f.w[i][u] = ldw16(wrow[i] + step * (kStep / 2) + u * (kStrip / 2));
+      load_scales<SH>(f.sc[i], a, srow[i], step);
+    }
+  };
+
+  float acc[NT][L::kAcc];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int r = 0; r < L::kAcc; ++r) acc[i][r] = 0.f;
+
+  // Where this lane reads x and its sums in the staged chunk.
+  const bool mine = !kMasked || ((ln >> 2) == quarter && (ln & 3) < M);
+  const int xrow = kMasked ? (ln & 3) : ln;
+  const bool swapped = !kMasked && SH < 7;  // transposed dwords: MFMA t covers k = 32 t ..
+  const int xlane = L::kZeros + xrow * L::kRowBytes + (swapped ? 16 : 64) * quarter;
+  const int xt = swapped ? 64 : 16;  // bytes from one MFMA to the next
+  const float* sums = reinterpret_cast<const float*>(lds + L::kSums);
+
+  // One strip: k0 = its first value inside the chunk; scale(i, c, s, z) of row tile i, 32-code chunk c.
+  auto strip = [&](int xbase, int chunk0, const u32x4 (&w)[NT], auto&& scale) {
+    u32x4 xa[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) xa[t] = *reinterpret_cast<const u32x4*>(lds + xbase + t * xt);
+    if constexpr (kMasked) {
+      float xs[M];
+#pragma unroll
+      for (int m = 0; m < M; ++m) xs[m] = sums[m * (L::kChunkK / 32) + chunk0 + quarter];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        v4f part{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, xa[t]),
+                                                         __builtin_bit_cast(v8bf, int4x8_to_bf16x8(w[i][t])), part, 0, 0, 0);
+        float s, z;
+        scale(i, quarter, s, z);
+#pragma unroll
+        for (int m = 0; m < M; ++m) acc[i][m] = fmaf(s, fmaf(-z, xs[m], part[m]), acc[i][m]);
+      }
+    } else {
+      u32x4 wt[NT];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) wt[i] = swapped ? transpose_quarters(w[i]) : w[i];
+#pragma unroll
+      for (int g = 0; g < 4 / GS; ++g) {
+        v4f xs{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < GS; ++c)
+          xs += *reinterpret_cast<const v4f*>(sums + (chunk0 + g * GS + c) * 16 + quarter * 4);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          v4f part{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int t = g * GS; t < (g + 1) * GS; ++t)
+            part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, xa[t]),
+                                                           __builtin_bit_cast(v8bf, int4x8_to_bf16x8(wt[i][t])), part, 0, 0, 0);
+          float s, z;
+          scale(i, g * GS, s, z);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][r] = fmaf(s, fmaf(-z, xs[r], part[r]), acc[i][r]);
+        }
+      }
+    }
+  };
+
+  const int64_t chunks = (K + L::kChunkK - 1) / L::kChunkK;
+  for (int64_t ch = 0; ch < chunks; ++ch) {
+    const int64_t kc = ch * L::kChunkK;
+    const int64_t step_end = kc + L::kChunkK < K ? (kc + L::kChunkK) / kStep : steps;
+    const int64_t step0 = kc / kStep;
+    Step cur;
+    if (step0 + wk < step_end) fetch(cur, step0 + wk);  // in flight while x is staged
+    // x rows in the decoder's order, zeros past K, and the sums of 32 values.
+    const int klen = int(K - kc < L::kChunkK ? (K - kc + kStrip - 1) / kStrip * kStrip : L::kChunkK);
+    const int per_row = klen / 8;
+    for (int idx = threadIdx.x; idx < rows * per_row; idx += L::kThreads) {  // klen % 32 == 0: quads stay together
+      const int m = idx / per_row, c = idx % per_row;
+      const int64_t k = kc + c * 8;
+      const uint16_t* p = x + m * K + k;
+      const u32x4 v = decoder_order(k + 8 <= K ? ldx16(p) : ld_halves(p, int(K - k)));
+      *reinterpret_cast<u32x4*>(lds + L::kZeros + m * L::kRowBytes + c * 16) = v;
+      float s = dpp_add<0xB1>(sum8(v, 0.f));
+      s = dpp_add<0x4E>(s);
+      if ((c & 3) == 0) {
+        float* dst = reinterpret_cast<float*>(lds + L::kSums);
+        if constexpr (kMasked) dst[m * (L::kChunkK / 32) + (c >> 2)] = s;
+        else dst[(c >> 2) * 16 + m] = s;
+      }
+    }
+    if (ch == 0) {  // what rows without x read
+      if constexpr (kMasked) {
+        for (int i = threadIdx.x; i < L::kZeros / 16; i += L::kThreads)
+          *reinterpret_cast<u32x4*>(lds + i * 16) = u32x4{0u, 0u, 0u, 0u};
+      }
+      for (int m = rows; m < L::kRows; ++m) {
+        for (int c = threadIdx.x; c < L::kChunkK / 8; c += L::kThreads)
+          *reinterpret_cast<u32x4*>(lds + L::kZeros + m * L::kRowBytes + c * 16) = u32x4{0u, 0u, 0u, 0u};
+        for (int c = threadIdx.x; c < L::kChunkK / 32; c += L::kThreads) {
+          float* dst = reinterpret_cast<float*>(lds + L::kSums);
+          if constexpr (kMasked) dst[m * (L::kChunkK / 32) + c] = 0.f;
+          else dst[c * 16 + m] = 0.f;
+        }
+      }
+    }
+    wait_lds();
+    block_barrier();
+
+    for (int64_t step = step0 + wk; step < step_end; step += WK) {
+      Step next;
+      const bool more = step + WK < step_end;
+      if (more) fetch(next, step + WK);
+      const int off = int(step - step0) * kStep;
+      const int xbase = mine ? xlane + off * 2 : 0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        u32x4 w[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) w[i] = cur.w[i][u];
+        strip(xbase + u * kStrip * 2, off / 32 + u * 4, w,
+              [&](int i, int c, float& s, float& z) { pick_scale<SH>(cur.sc[i], u, c, s, z); });
+      }
+      if (more) cur = next;
+    }
+    // The strips behind the last whole step, guarded, by the wave whose turn it is.
+    if (ch == chunks - 1 && steps * kStep < K && wk == int(steps % WK)) {
+      for (int64_t k = steps * kStep; k < K; k += kStrip) {
+        const int64_t kw = k + quarter * 32;
+        u32x4 w[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const uint8_t* p = wrow[i] + (k >> 1);
+          const int64_t left = a.row_bytes - (kw >> 1);
+          w[i] = left >= 16 ? ldw16(p) : ld_bytes(p, int(left));
+        }
+        const int off = int(k - kc);
+        strip(mine ? xlane + off * 2 : 0, off / 32, w, [&](int i, int c, float& s, float& z) {
+          const int64_t g = (k + 32 * c) >> a.shift;
+          s = g < a.groups ? bf16_to_f32(a.scale[srow[i] + g]) : 0.f;
+          z = g < a.groups ? zero_at(a, srow[i] + g) : 0.f;
+        });
+      }
+    }
+    wait_lds();
+    block_barrier();  // every wave is done with this chunk of x
+  }
+
+  if constexpr (kMasked) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        acc[i][m] += __shfl_xor(acc[i][m], 16, kWave);
+        acc[i][m] += __shfl_xor(acc[i][m], 32, kWave);
+      }
+  }
+  if constexpr (WK > 1) {
+    // red[wn][wk][i][value][lane of the value]: the waves' sums are added in wave order.
+    constexpr int kVals = kMasked ? M * 16 : 256;
+    float* red = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      if constexpr (kMasked) {
+        if (quarter == 0)
+#pragma unroll
+          for (int m = 0; m < M; ++m) red[((wave * NT) + i) * kVals + m * 16 + ln] = acc[i][m];
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) red[((wave * NT) + i) * kVals + (quarter * 4 + r) * 16 + ln] = acc[i][r];
+      }
+    }
+    wait_lds();
+    block_barrier();
+    for (int idx = threadIdx.x; idx < WN * NT * kVals; idx += L::kThreads) {
+      const int w = idx / (NT * kVals), rest = idx % (NT * kVals);
+      const int i = rest / kVals, m = rest % kVals / 16, n = rest % 16;
+      if (m >= rows) continue;
+      float v = red[(w * WK * NT + i) * kVals + m * 16 + n];
+#pragma unroll
+      for (int o = 1; o < WK; ++o) v += red[((w * WK + o) * NT + i) * kVals + m * 16 + n];
+      store(m, (w * NT + i) * 16 + n, v);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int n = (wn * NT + i) * 16 + ln;
+      if constexpr (kMasked) {
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+          if (quarter == m && m < rows) store(m, n, acc[i][m]);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (quarter * 4 + r < rows) store(quarter * 4 + r, n, acc[i][r]);
+      }
+    }
+  }
+}
+
+template <int M, int NT, int WN, int WK, int SH>
+__global__ __launch_bounds__(64 * WN * WK) void int4_stream_kernel(Int4Args a, const uint16_t* __restrict__ x,
+                                                                   void* __restrict__ out, int out_bf16, int64_t rows,
+                                                                   int64_t N, int64_t K, float alpha, Epilogue epi) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int64_t n0 = int64_t(blockIdx.x) * (16 * NT * WN);
+  int4_stream_tile<M, NT, WN, WK, SH>(lds, a, x, int(rows), N, K, n0, [&](int m, int n, float v) {
+    if (n0 + n < N) store_epi(out, m, n0 + n, N, v, alpha, out_bf16, epi);
+  });
+}
+
+// ---------------------------------------------------------------- matrix-core tile
+
+// A block computes BM = 16 MT WM rows by BN = 16 NT WN columns with 16x16x32
+// MFMA.  WM x WN waves share each 128-value strip of x, or WK waves split the
+// strips between them and add their tiles at the end.
+//
+// Weights go straight into the registers of the wave that multiplies them: lane
+// (n = l % 16, quarter h = l / 16) reads the 16 bytes k = 32 h .. 32 h + 31 of its
+// row's strip, and two half-wave swap stages transpose the
+// 4x4 dwords over the quarters, after which dword t holds k = 32 t + 8 h ..
+// + 7: MFMA step t covers 32 consecutive k, so a group of 32 is a whole step.
+// Activation: the strip [BM][128] goes through registers into LDS in the
+// decoder's order (16-byte chunks XOR-permuted by row against bank
+// conflicts).
+//
+// After the last step of a group: acc += scale * group.  The zero points are
+// taken off by the matrix cores too: sum_groups sum_x * (zero * scale) is a
+// product over the groups.  A group's sum of x (float32, 24 bits) is three bfloat16 cut
+// from it, hi + mid + lo, and zero * scale (8 by 8 bits) is two, both exact, so six
+// of a quarter's eight k slots of one MFMA hold all products of one group,
+// and four groups need one instruction per 16x16 tile; on the
+// vector ALU, which the decoding and the scaling fill already, they would be 16.
+constexpr int kSlots = 4;  // groups per correction
+
+template <int MT, int NT, int WM, int WN, int WK> struct Int4Tile {
+  static constexpr int kBM = 16 * MT * WM, kBN = 16 * NT * WN, kThreads = 64 * WM * WN * WK;
+  static constexpr int kStagers = WK > 1 ? 64 : kThreads;  // threads that fill one activation buffer
+  static constexpr int kChunks = kBM * 16 / kStagers;      // 16-byte chunks per staging thread
+  static constexpr int kXBytes = kBM * kStrip * 2;
+  static constexpr int kBufs = WK > 1 ? 1 : 2;             // private buffers need no second one
+  static constexpr int kSumBytes = kSlots * kBM * 16;      // [slot][BM] pieces of the sums
+  static constexpr int kSums = kXBytes * kBufs;
+  static constexpr int kOne = kSums + 2 * kSumBytes;
+  static constexpr int kRing = kOne * WK;
+  static constexpr int kReduce = WK > 1 ? WK * 64 * MT * NT * 16 : 0;
+  static constexpr int kLds = kRing > kReduce ? kRing : kReduce;
+  static_assert(WK == 1 || WM * WN == 1, "either the tile or K is split over the waves");
+};
 
 // Sum over groups of 2^LOG neighbouring lanes (LOG = 2, 3, 4), in each lane.
 template <int LOG>
@@ -217,77 +524,109 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
+__device__ __forceinline__ float cut_bf16(float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); }
+
+// -s as (hi, mid, lo, hi, mid, lo, 0, 0), each exact in bfloat16.
+__device__ __forceinline__ u32x4 sum_pieces(float s) {
+  const float hi = cut_bf16(-s), rest = -s - hi, mid = cut_bf16(rest), lo = rest - mid;
+  const uint32_t h = __float_as_uint(hi), m = __float_as_uint(mid), l = __float_as_uint(lo);
+  return u32x4{h >> 16 | m, l >> 16 | h, m >> 16 | (l & 0xFFFF0000u), 0u};
+}
+// v as (hi, hi, hi, lo, lo, lo, 0, 0).
+__device__ __forceinline__ u32x4 factor_pieces(float v) {
+  const float hi = cut_bf16(v);
+  const uint32_t h = __float_as_uint(hi), l = __float_as_uint(v - hi) & 0xFFFF0000u;
+  return u32x4{h >> 16 | h, h >> 16 | l, l >> 16 | l, 0u};
+}
+
 // GS: MFMA steps per group inside a strip (1, 2, 4; 4 also for larger groups).
-// store(m, n, value): m relative to the tile's first row.
-template <int MT, int NT, int WN, int WK, int GS, typename Store>
+// store(m, n, value): m relative to the tile's first row.  Every thread of the
+// block calls it; the block's LDS is free when it begins.
+template <int MT, int NT, int WM, int WN, int WK, int GS, typename Store>
 __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const uint16_t* __restrict__ x, int64_t rows,
                                           int64_t N, int64_t K, int64_t n0, Store&& store) {
-  using L = Int4Tile<MT, NT, WN, WK>;
+  using L = Int4Tile<MT, NT, WM, WN, WK>;
   constexpr int G = 4 / GS;  // groups per strip
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int ln = lane & 15, quarter = lane >> 4;
-  const int wn = WK > 1 ? 0 : wave, wk = WK > 1 ? wave : 0;
+  const int wn = WK > 1 ? 0 : wave % WN, wm = WK > 1 ? 0 : wave / WN, wk = WK > 1 ? wave : 0;
   const int stager = WK > 1 ? lane : threadIdx.x;
-  const int nstrips = int((K + kStrip - 1) / kStrip);
-  const int live = int((rows + 15) / 16);  // 16-row tiles that hold a row
+  const int nstrips = int((K + kStrip - 1) / kStrip), nwhole = int(K / kStrip);
+  char* const mem = lds + wk * L::kOne;
 
-  const uint8_t* wrow[NT];
-  int64_t srow[NT];
+  // Uniform bases and 32-bit lane offsets (K < 2^23).
+  const uint8_t* const wbase = a.w + n0 * a.row_bytes;
+  const uint16_t* const sbase = a.scale + n0 * a.groups;
+  // Without zero points the scales' bytes are read in their place and not used.
+  const uint8_t* const zbase = (a.zero ? a.zero : reinterpret_cast<const uint8_t*>(a.scale)) + n0 * a.groups;
+  uint32_t woff[NT], soff[NT], xoff[L::kChunks];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    int64_t n = n0 + wn * 16 * NT + i * 16 + ln;
-    n = n < N ? n : N - 1;  // columns past N re-read the last row, never stored
-    wrow[i] = a.w + n * a.row_bytes;
-    srow[i] = n * a.groups;
+    const int n = wn * 16 * NT + i * 16 + ln;
+    const uint32_t row = n0 + n < N ? n : uint32_t(N - 1 - n0);  // columns past N re-read the last row, never stored
+    woff[i] = row * uint32_t(a.row_bytes) + quarter * 16;
+    soff[i] = row * uint32_t(a.groups);
+  }
+#pragma unroll
+  for (int j = 0; j < L::kChunks; ++j) {
+    const int m = (stager + j * L::kStagers) >> 4;
+    xoff[j] = uint32_t(m < rows ? m : rows - 1) * uint32_t(K) + (stager & 15) * 8;  // rows past the end likewise
   }
 
+  // A strip's G groups of a row are neighbours: their scales come in one load
+  // and stay packed, and so do their zero points.
   u32x4 wreg[NT], xreg[L::kChunks];
-  uint16_t sreg[NT][G];
-  uint8_t zreg[NT][G];
+  uint32_t sreg[NT][2];
+  uint16_t shalf[NT];  // in place of sreg where G = 1
+  uint32_t zreg[NT];
 
+  // A whole strip: no lane branches, so that nothing waits for a load before
+  // the strip after this one is staged.
   auto fetch = [&](int strip) {
-    const int64_t k = int64_t(strip) * kStrip;
-    const int64_t kw = k + quarter * 32;
+    const int64_t k = int64_t(strip) * kStrip, at = k >> a.shift;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      if (kw + 32 <= K) {
-        wreg[i] = ldw16(wrow[i] + (kw >> 1));
+      wreg[i] = ldw16(wbase + (k >> 1) + woff[i]);
+      const uint16_t* sp = sbase + at + soff[i];
+      const uint8_t* zp = zbase + at + soff[i];
+      if constexpr (G == 4) {
+        const u32x2 v = ld_any2<u32x2>(sp);
+        sreg[i][0] = v.x;
+        sreg[i][1] = v.y;
+        zreg[i] = ld_any1<uint32_t>(zp);
+      } else if constexpr (G == 2) {
+        sreg[i][0] = ld_any2<uint32_t>(sp);
+        zreg[i] = ld_any1<uint16_t>(zp);
       } else {
-        u32x4 v{0u, 0u, 0u, 0u};
-        for (int64_t b = kw >> 1; b < a.row_bytes; ++b) {
-          const int at = int(b - (kw >> 1));
-          const uint32_t byte = uint32_t(wrow[i][b]) << (8 * (at & 3));
-          if (at < 4) v.x |= byte;
-          else if (at < 8) v.y |= byte;
-          else if (at < 12) v.z |= byte;
-          else v.w |= byte;
-        }
-        wreg[i] = v;
-      }
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        int64_t at = (k + g * 32 * GS) >> a.shift;
-        at = srow[i] + (at < a.groups ? at : a.groups - 1);  // groups past K multiply zeros
-        sreg[i][g] = a.scale[at];
-        zreg[i][g] = a.zero ? a.zero[at] : uint8_t(8);
+        shalf[i] = *sp;
+        zreg[i] = *zp;
       }
     }
 #pragma unroll
-    for (int j = 0; j < L::kChunks; ++j) {
-      const int idx = stager + j * L::kStagers, m = idx >> 4;
-      const int64_t kx = k + (idx & 15) * 8;
-      u32x4 v{0u, 0u, 0u, 0u};
-      if (m < rows) {
-        const uint16_t* p = x + m * K + kx;
-        if (kx + 8 <= K) {
-          v = ldx16(p);
-        } else {
+    for (int j = 0; j < L::kChunks; ++j) xreg[j] = ldx16(x + k + xoff[j]);
+  };
+  // The last, partial strip: zeros behind K, and groups past K are nothing,
+  // whatever lies there.
+  auto fetch_tail = [&](int strip) {
+    const int64_t k = int64_t(strip) * kStrip, at = k >> a.shift;
+    const int left = int(K - k);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (kx + i < K) v[i >> 1] |= uint32_t(p[i]) << (16 * (i & 1));
-        }
-      }
-      xreg[j] = v;
+    for (int i = 0; i < NT; ++i) {
+      const int codes = left - quarter * 32;
+      const uint8_t* p = wbase + (k >> 1) + woff[i];
+      wreg[i] = codes >= 31 ? ldw16(p) : ld_bytes(p, (codes + 1) >> 1);
+      const int groups = int(a.groups - at < G ? a.groups - at : G);
+      const u32x4 v = ld_halves(sbase + at + soff[i], groups);
+      sreg[i][0] = v.x;
+      sreg[i][1] = v.y;
+      shalf[i] = uint16_t(v.x);
+      zreg[i] = ld_bytes(zbase + at + soff[i], groups).x;
+    }
+#pragma unroll
+    for (int j = 0; j < L::kChunks; ++j) {
+      const int values = left - (stager & 15) * 8;
+      const uint16_t* p = x + k + xoff[j];
+      xreg[j] = values >= 8 ? ldx16(p) : ld_halves(p, values);
     }
   };
 
@@ -296,64 +635,108 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[mt][i] = v4f{0.f, 0.f, 0.f, 0.f};
+  float zs[NT];  // zero * scale of this quarter's slot
+#pragma unroll
+  for (int i = 0; i < NT; ++i) zs[i] = 0.f;
+  for (int i = stager; i < 2 * L::kSumBytes / 16; i += L::kStagers)
+    *reinterpret_cast<u32x4*>(mem + L::kSums + i * 16) = u32x4{0u, 0u, 0u, 0u};
+  if constexpr (WK == 1) __syncthreads();  // a slot's first writer need not be its clearer
 
-  int buf = 0;
-  if (wk < nstrips) fetch(wk);
+  auto correct = [&](const char* sums) {
+    v8bf zb[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      zb[i] = __builtin_bit_cast(v8bf, factor_pieces(zs[i]));
+      zs[i] = 0.f;
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const v8bf xb = *reinterpret_cast<const v8bf*>(sums + (quarter * L::kBM + (wm * MT + mt) * 16 + ln) * 16);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[mt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, zb[i], acc[mt][i], 0, 0, 0);
+    }
+  };
+
+  int buf = 0, slot = 0, sbuf = 0;  // the strip's buffer; its first group's slot and their buffer
+  if (wk < nwhole) fetch(wk);
   for (int strip = wk; strip < nstrips; strip += WK) {
-    char* xs = lds + (WK > 1 ? wk : buf) * L::kOne;
-    float* sums = reinterpret_cast<float*>(xs + L::kXBytes);
+    if (strip >= nwhole) fetch_tail(strip);
+    // What is made of the loaded values is made from here on: the compiler
+    // would move the first shift of a scale behind its load, where it waits for memory
+    // in every strip.
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      if constexpr (G == 1) asm volatile("" : "+v"(shalf[i]), "+v"(zreg[i]));
+      else asm volatile("" : "+v"(sreg[i][0]), "+v"(zreg[i]));
+      if constexpr (G == 4) asm volatile("" : "+v"(sreg[i][1]));
+    }
+    char* xs = mem + buf * L::kXBytes;
+    char* sums = mem + L::kSums + sbuf * L::kSumBytes;
 #pragma unroll
     for (int j = 0; j < L::kChunks; ++j) {
       const int idx = stager + j * L::kStagers, m = idx >> 4, c = idx & 15;
       const u32x4 v = decoder_order(xreg[j]);
       *reinterpret_cast<u32x4*>(xs + m * (kStrip * 2) + ((c ^ (m & 15)) << 4)) = v;
       const float s = lanes_sum<(GS == 4 ? 4 : GS == 2 ? 3 : 2)>(sum8(v, 0.f));
-      if ((c & (4 * GS - 1)) == 0) sums[(c / (4 * GS)) * L::kBM + m] = s;
+      if ((c & (4 * GS - 1)) == 0)
+        *reinterpret_cast<u32x4*>(sums + ((slot + c / (4 * GS)) * L::kBM + m) * 16) = sum_pieces(s);
     }
     u32x4 w[NT];
-    float sc[NT][G], zc[NT][G];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      w[i] = transpose_quarters(wreg[i]);
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        sc[i][g] = bf16_to_f32(sreg[i][g]);
-        zc[i][g] = -float(zreg[i][g]);
-      }
-    }
-    if (strip + WK < nstrips) fetch(strip + WK);
-    wait_lds();
-    if constexpr (WK == 1) block_barrier();
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      v8bf codes[NT][GS];
+    uint32_t sp[NT][2];
+    v8bf codes[NT][GS];
+    auto scale = [&](int i, int g) { return __uint_as_float((g & 1) ? sp[i][g >> 1] & 0xFFFF0000u : sp[i][g >> 1] << 16); };
+    auto decode = [&](int g) {
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int t = 0; t < GS; ++t)
-          codes[i][t] = __builtin_bit_cast(v8bf, int4x8_to_bf16x8(w[i][g * GS + t]));
+        for (int t = 0; t < GS; ++t) codes[i][t] = __builtin_bit_cast(v8bf, int4x8_to_bf16x8(w[i][g * GS + t]));
+    };
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        if (mt >= live) break;  // uniform over the block
-        v4f part[NT];
+    for (int i = 0; i < NT; ++i) {
+      w[i] = transpose_quarters(wreg[i]);
+      sp[i][0] = G == 1 ? shalf[i] : sreg[i][0];
+      if constexpr (G == 4) sp[i][1] = sreg[i][1];
+      if (!a.zero) zreg[i] = 0x08080808u;
 #pragma unroll
-        for (int t = 0; t < GS; ++t) {
-          const int c = (g * GS + t) * 4 + quarter;
-          const v8bf xa = *reinterpret_cast<const v8bf*>(xs + (mt * 16 + ln) * (kStrip * 2) + ((c ^ ln) << 4));
+      for (int g = 0; g < G; ++g) zs[i] = quarter == slot + g ? scale(i, g) * float((zreg[i] >> (8 * g)) & 255u) : zs[i];
+    }
+    decode(0);
+    if (strip + WK < nwhole) fetch(strip + WK);
+    wait_lds();
+    if constexpr (WK == 1) block_barrier();
+    {
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
-            part[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa, codes[i][t], t == 0 ? v4f{0.f, 0.f, 0.f, 0.f} : part[i],
-                                                              0, 0, 0);
+      for (int g = 0; g < G; ++g) {
+        if (g > 0) decode(g);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          v4f part[NT];
+#pragma unroll
+          for (int t = 0; t < GS; ++t) {
+            const int c = (g * GS + t) * 4 + quarter;
+            const v8bf xa =
+                *reinterpret_cast<const v8bf*>(xs + ((wm * MT + mt) * 16 + ln) * (kStrip * 2) + ((c ^ ln) << 4));
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+              part[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa, codes[i][t], t == 0 ? v4f{0.f, 0.f, 0.f, 0.f} : part[i],
+                                                                0, 0, 0);
+          }
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            const float s = scale(i, g);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[mt][i][r] = fmaf(s, part[i][r], acc[mt][i][r]);
+          }
         }
-        const v4f xsum = *reinterpret_cast<const v4f*>(sums + g * L::kBM + mt * 16 + quarter * 4);
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            acc[mt][i][r] = fmaf(sc[i][g], fmaf(zc[i][g], xsum[r], part[i][r]), acc[mt][i][r]);
       }
     }
-    buf ^= 1;
+    slot += G;
+    if (slot == kSlots || strip + WK >= nstrips) {  // unfilled slots have zs = 0 and finite sums
+      correct(sums);
+      slot = 0;
+      sbuf ^= 1;
+    }
+    if constexpr (WK == 1) buf ^= 1;
   }
 
   if constexpr (WK > 1) {
@@ -386,16 +769,16 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
       for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          store(mt * 16 + quarter * 4 + r, wn * 16 * NT + i * 16 + ln, acc[mt][i][r]);
+          store((wm * MT + mt) * 16 + quarter * 4 + r, wn * 16 * NT + i * 16 + ln, acc[mt][i][r]);
   }
 }
 
-template <int MT, int NT, int WN, int WK, int GS>
-__global__ __launch_bounds__(64 * WN * WK) void int4_gemm_kernel(Int4Args a, const uint16_t* __restrict__ x,
+template <int MT, int NT, int WM, int WN, int WK, int GS>
+__global__ __launch_bounds__(64 * WM * WN * WK) void int4_gemm_kernel(Int4Args a, const uint16_t* __restrict__ x,
                                                                  void* __restrict__ out, int out_bf16, int64_t M,
                                                                  int64_t N, int64_t K, float alpha, Epilogue epi) {
-  using L = Int4Tile<MT, NT, WN, WK>;
-  __shared__ __attribute__((aligned(16))) char lds[L::kLds];
+  using L = Int4Tile<MT, NT, WM, WN, WK>;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
   // Row tiles of one column tile follow each other on one XCD, whose L2 then
   // holds the column tile's weights.
   const int64_t mtiles = (M + L::kBM - 1) / L::kBM, ntiles = (N + L::kBN - 1) / L::kBN, total = mtiles * ntiles;
@@ -403,7 +786,7 @@ __global__ __launch_bounds__(64 * WN * WK) void int4_gemm_kernel(Int4Args a, con
   const int64_t tile = int64_t(blockIdx.x % 8) * per + blockIdx.x / 8;
   if (int64_t(blockIdx.x / 8) >= per || tile >= total) return;  // uniform over the block
   const int64_t m0 = tile % mtiles * L::kBM, n0 = tile / mtiles * L::kBN;
-  int4_tile<MT, NT, WN, WK, GS>(lds, a, x + m0 * K, M - m0, N, K, n0, [&](int m, int n, float v) {
+  int4_tile<MT, NT, WM, WN, WK, GS>(lds, a, x + m0 * K, M - m0, N, K, n0, [&](int m, int n, float v) {
     if (m0 + m < M && n0 + n < N) store_epi(out, m0 + m, n0 + n, N, v, alpha, out_bf16, epi);
   });
 }
@@ -413,12 +796,12 @@ __global__ __launch_bounds__(64 * WN * WK) void int4_gemm_kernel(Int4Args a, con
 // writes zeros, an empty group nothing.  Every block builds the prefix sum of
 // the groups' row tiles in LDS and walks its XCD's contiguous part of the
 // (group, row tile, column tile) list.
-template <int MT, int NT, int WN, int WK, int GS>
-__global__ __launch_bounds__(64 * WN * WK) void int4_grouped_kernel(
+template <int MT, int NT, int WM, int WN, int WK, int GS>
+__global__ __launch_bounds__(64 * WM * WN * WK) void int4_grouped_kernel(
     Int4Args a, const uint16_t* __restrict__ x, const uint32_t* __restrict__ a_offsets,
     const int32_t* __restrict__ expert_ids, void* __restrict__ out, int out_bf16, int64_t groups, int64_t T, int64_t N,
     int64_t K, int64_t E) {
-  using L = Int4Tile<MT, NT, WN, WK>;
+  using L = Int4Tile<MT, NT, WM, WN, WK>;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   int* cum = reinterpret_cast<int*>(lds + L::kLds);  // cum[z] = row tiles of groups 0 .. z - 1
   auto span = [&](int64_t z, int64_t& start, int64_t& rows) {
@@ -479,7 +862,7 @@ __global__ __launch_bounds__(64 * WN * WK) void int4_grouped_kernel(
     b.scale += e * N * a.groups;
     if (b.zero) b.zero += e * N * a.groups;
     __syncthreads();  // the previous tile's buffers are free
-    int4_tile<MT, NT, WN, WK, GS>(lds, b, x + m0 * K, end - m0, N, K, n0, put);
+    int4_tile<MT, NT, WM, WN, WK, GS>(lds, b, x + m0 * K, end - m0, N, K, n0, put);
   }
 }
 
@@ -501,45 +884,67 @@ hipError_t by_group(const Int4Args& a, F&& go) {
   return go(std::integral_constant<int, 4>{});
 }
 
-template <int M>
-hipError_t gemv_m(const Int4Args& a, const uint16_t* x, void* out, int bf16, int64_t N, int64_t K, float alpha,
-                  int num_cus, const Epilogue& epi, hipStream_t s) {
-  const int64_t waves = int64_t(num_cus) * 8;
-  auto go = [&](auto kernel, int rows) {
-    return launch(kernel, dim3(unsigned((N + 4 * rows - 1) / (4 * rows))), dim3(256), 0, s, a, x, out, bf16, N, K,
-                  alpha, epi);
-  };
-  if (N >= waves * 4) return go(int4_gemv_kernel<M, 4, 2>, 4);
-  if (N >= waves * 2) return go(int4_gemv_kernel<M, 2, 2>, 2);
-  return go(int4_gemv_kernel<M, 1, 2>, 1);
+template <typename F>
+hipError_t by_shift(const Int4Args& a, F&& go) {
+  if (a.shift == 5) return go(std::integral_constant<int, 5>{});
+  if (a.shift == 6) return go(std::integral_constant<int, 6>{});
+  if (a.shift == 7) return go(std::integral_constant<int, 7>{});
+  return go(std::integral_constant<int, 8>{});
 }
 
-template <int MT, int NT, int WN, int WK>
-hipError_t gemm_cfg(const Int4Args& a, const uint16_t* x, void* out, int bf16, int64_t M, int64_t N, int64_t K,
-                    float alpha, const Epilogue& epi, hipStream_t s) {
-  using L = Int4Tile<MT, NT, WN, WK>;
-  const int64_t total = ((M + L::kBM - 1) / L::kBM) * ((N + L::kBN - 1) / L::kBN);
-  const int64_t blocks = (total + 7) / 8 * 8;
+template <int M, int NT, int WN, int WK>
+hipError_t stream_cfg(const Int4Args& a, const uint16_t* x, void* out, int bf16, int64_t rows, int64_t N, int64_t K,
+                      float alpha, const Epilogue& epi, hipStream_t s) {
+  using L = StreamLayout<M, NT, WN, WK>;
+  const int64_t blocks = (N + 16 * NT * WN - 1) / (16 * NT * WN);
   if (blocks * L::kThreads >= (int64_t(1) << 32)) return hipErrorInvalidValue;
-  return by_group(a, [&](auto gs) {
-    return launch(int4_gemm_kernel<MT, NT, WN, WK, decltype(gs)::value>, dim3(unsigned(blocks)), dim3(L::kThreads), 0,
-                  s, a, x, out, bf16, M, N, K, alpha, epi);
+  return by_shift(a, [&](auto sh) -> hipError_t {
+    auto kernel = int4_stream_kernel<M, NT, WN, WK, decltype(sh)::value>;
+    static std::atomic<uint64_t> lds_set{0};
+    if (hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(kernel), L::kLds, lds_set)) return e;
+    return launch(kernel, dim3(unsigned(blocks)), dim3(L::kThreads), L::kLds, s, a, x, out, bf16, rows, N, K, alpha, epi);
   });
 }
 
-template <int MT, int NT, int WN, int WK>
+// Waves along K until the card has 8 waves per CU or the steps are used up.
+template <int M>
+hipError_t stream_rows(const Int4Args& a, const uint16_t* x, void* out, int bf16, int64_t rows, int64_t N, int64_t K,
+                       float alpha, int num_cus, const Epilogue& epi, hipStream_t s) {
+  const int64_t tiles = (N + 15) / 16, want = int64_t(num_cus) * 8;
+  if (tiles >= 2 * want) return stream_cfg<M, 2, 4, 1>(a, x, out, bf16, rows, N, K, alpha, epi, s);
+  if (tiles >= want || K < 2 * kStep) return stream_cfg<M, 1, 4, 1>(a, x, out, bf16, rows, N, K, alpha, epi, s);
+  if (tiles * 4 >= want || K < 8 * kStep) return stream_cfg<M, 1, 1, 4>(a, x, out, bf16, rows, N, K, alpha, epi, s);
+  return stream_cfg<M, 1, 1, 8>(a, x, out, bf16, rows, N, K, alpha, epi, s);
+}
+
+template <int MT, int NT, int WM, int WN, int WK>
+hipError_t gemm_cfg(const Int4Args& a, const uint16_t* x, void* out, int bf16, int64_t M, int64_t N, int64_t K,
+                    float alpha, const Epilogue& epi, hipStream_t s) {
+  using L = Int4Tile<MT, NT, WM, WN, WK>;
+  const int64_t total = ((M + L::kBM - 1) / L::kBM) * ((N + L::kBN - 1) / L::kBN);
+  const int64_t blocks = (total + 7) / 8 * 8;
+  if (blocks * L::kThreads >= (int64_t(1) << 32)) return hipErrorInvalidValue;
+  return by_group(a, [&](auto gs) -> hipError_t {
+    auto kernel = int4_gemm_kernel<MT, NT, WM, WN, WK, decltype(gs)::value>;
+    static std::atomic<uint64_t> lds_set{0};
+    if (hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(kernel), L::kLds, lds_set)) return e;
+    return launch(kernel, dim3(unsigned(blocks)), dim3(L::kThreads), L::kLds, s, a, x, out, bf16, M, N, K, alpha, epi);
+  });
+}
+
+template <int MT, int NT, int WM, int WN, int WK>
 hipError_t grouped_cfg(const Int4Args& a, const uint16_t* x, const uint32_t* offsets, const int32_t* ids, void* out,
                        int bf16, int64_t G, int64_t E, int64_t T, int64_t N, int64_t K, int num_cus, hipStream_t s) {
-  using L = Int4Tile<MT, NT, WN, WK>;
+  using L = Int4Tile<MT, NT, WM, WN, WK>;
   const int lds = int(L::kLds + 4 * (G + 1));
   constexpr int kMaxLds = 160 * 1024;
   if (lds > kMaxLds) return hipErrorInvalidValue;
   // At most ceil(T / BM) + min(G, T) row tiles exist.
   const int64_t upper = ((T + L::kBM - 1) / L::kBM + std::min(G, T)) * ((N + L::kBN - 1) / L::kBN);
-  const int64_t per_cu = std::max<int64_t>(1, std::min<int64_t>(kMaxLds / lds, 16 / (WN * WK)));
+  const int64_t per_cu = std::max<int64_t>(1, std::min<int64_t>(kMaxLds / lds, 16 / (WM * WN * WK)));
   const int64_t blocks = (std::min(upper, per_cu * num_cus) + 7) / 8 * 8;
   return by_group(a, [&](auto gs) -> hipError_t {
-    auto kernel = int4_grouped_kernel<MT, NT, WN, WK, decltype(gs)::value>;
+    auto kernel = int4_grouped_kernel<MT, NT, WM, WN, WK, decltype(gs)::value>;
     static std::atomic<uint64_t> lds_set{0};
     if (hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(kernel), kMaxLds, lds_set)) return e;
     return launch(kernel, dim3(unsigned(blocks)), dim3(L::kThreads), lds, s, a, x, offsets, ids, out, bf16, G, T, N, K,
@@ -553,14 +958,16 @@ hipError_t launch_int4_gemm(const uint8_t* w, const uint16_t* scale, const uint8
                             int out_bf16, int64_t M, int64_t N, int64_t K, int64_t group, float alpha, int num_cus,
                             hipStream_t s, const Epilogue& epi) {
   const Int4Args a = make_args(w, scale, zero, K, group);
-  switch (M) {
-    case 1: return gemv_m<1>(a, x, out, out_bf16, N, K, alpha, num_cus, epi, s);
-    case 2: return gemv_m<2>(a, x, out, out_bf16, N, K, alpha, num_cus, epi, s);
-    default: break;
-  }
-  if (M <= 16) return gemm_cfg<1, 1, 1, 4>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
-  if (M <= 64) return gemm_cfg<2, 2, 1, 4>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
-  return gemm_cfg<4, 4, 4, 1>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
+  if (M == 1) return stream_rows<1>(a, x, out, out_bf16, M, N, K, alpha, num_cus, epi, s);
+  if (M == 2) return stream_rows<2>(a, x, out, out_bf16, M, N, K, alpha, num_cus, epi, s);
+  if (M <= 4) return stream_rows<4>(a, x, out, out_bf16, M, N, K, alpha, num_cus, epi, s);
+  if (M <= 16) return stream_rows<16>(a, x, out, out_bf16, M, N, K, alpha, num_cus, epi, s);
+  if (M <= 64) return gemm_cfg<2, 2, 1, 1, 4>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
+  // 128x256 tiles where they give more than half of the CUs one (M = 500, N = 14336,
+  // K = 4096: 95 against 144 us), else 64x128 (M = 500, N = K = 4096: 54 against 90).
+  if (((M + 127) / 128) * ((N + 255) / 256) * 2 > num_cus)
+    return gemm_cfg<8, 2, 1, 8, 1>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
+  return gemm_cfg<4, 2, 1, 4, 1>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
 }
 
 hipError_t launch_int4_grouped(const uint8_t* w, const uint16_t* scale, const uint8_t* zero, const uint16_t* x,
@@ -568,8 +975,15 @@ hipError_t launch_int4_grouped(const uint8_t* w, const uint16_t* scale, const ui
                                int64_t G, int64_t E, int64_t T, int64_t N, int64_t K, int64_t group, int num_cus,
                                hipStream_t s) {
   const Int4Args a = make_args(w, scale, zero, K, group);
-  if (T <= 8 * G) return grouped_cfg<1, 4, 1, 4>(a, x, a_offsets, expert_ids, out, out_bf16, G, E, T, N, K, num_cus, s);
-  return grouped_cfg<4, 4, 4, 1>(a, x, a_offsets, expert_ids, out, out_bf16, G, E, T, N, K, num_cus, s);
+  // Tiles by the rows a group has on average (64 experts, N = 1536, K = 2048, groups
+  // of 128): 16x128 to 4 rows (64 rows: 40 us, 32x128 44), 32x128 to 16 (256 rows: 46,
+  // 16x128 50, 64x256 70), 64x256 to 256 (4096 rows: 108, 32x128 113), 128x256 above
+  // (8 experts, N = K = 4096, 4096 rows: 301 against 357).
+  auto go = [&](auto cfg) { return cfg(a, x, a_offsets, expert_ids, out, out_bf16, G, E, T, N, K, num_cus, s); };
+  if (T <= 4 * G) return go(grouped_cfg<1, 2, 1, 4, 1>);
+  if (T <= 16 * G) return go(grouped_cfg<2, 2, 1, 4, 1>);
+  if (T <= 256 * G) return go(grouped_cfg<4, 2, 1, 8, 1>);
+  return go(grouped_cfg<8, 2, 1, 8, 1>);
 }
 
 }  // namespace qlinear

@@ -281,8 +281,9 @@ int bf16_gemm_impl(const void* w, const void* x, void* out, int out_dtype, int64
                                   size_t(ws_bytes), s, epi));
 }
 
-// int4 groups: a power of two >= 32, or one group per row.
-bool int4_group_ok(int64_t g, int64_t K) { return g >= K || (g >= 32 && (g & (g - 1)) == 0); }
+// int4 groups: a power of two >= 32, or one group per row.  The kernels take
+// 32-bit offsets inside a tile of rows.
+bool int4_group_ok(int64_t g, int64_t K) { return K < (int64_t(1) << 23) && (g >= K || (g >= 32 && (g & (g - 1)) == 0)); }
 
 // Limits of the expert calls: the router keeps a token's logits in one wave's
 // registers and pick j in lane j; slots and rows are int32.
