@@ -522,8 +522,8 @@ int qlinear_moe_route(const void* logits, int logits_dtype, int32_t* expert_ids,
  * the gradient of expert e's weight (0 where e was not chosen),
  *     grad_logits[t, e] = p_e * (a_e - sum_i p_i a_i),
  * 0 for masked experts and, renormalised, for those not chosen.  expert_ids
- * as qlinear_moe_route gave them (ids outside 0 .. E-1 are skipped, and so is
- * their gradient); grad_weights: float32 [T, top_k]; grad_logits: [T, E] of
+ * as qlinear_moe_route gave them, an expert at most once per token (ids outside 0 .. E-1
+ * are skipped, and so is their gradient); grad_weights: float32 [T, top_k]; grad_logits: [T, E] of
  * logits_dtype, written in full.
  */
 int qlinear_moe_route_backward(const void* logits, int logits_dtype, const int32_t* expert_ids,
