@@ -14,6 +14,7 @@ return torch tensors.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -182,6 +183,8 @@ _OUT_CODES = {torch.float32: F32, torch.bfloat16: BF16}
 
 def _out(out, shape, dtype, device):
     if out is None:
+        if len(shape) == 2:  # the same tensor as torch.empty's, in 1.3 us instead of 1.7
+            return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
         return torch.empty(shape, dtype=dtype, device=device)
     _require(out, "out")
     if tuple(out.shape) != tuple(shape) or out.dtype != dtype:
@@ -706,6 +709,14 @@ def moe_route_backward(logits: torch.Tensor, expert_ids: torch.Tensor, grad_weig
     return grad_logits
 
 
+@functools.lru_cache(maxsize=256)
+def _sort_workspace_bytes(slots: int, num_experts: int) -> int:
+    """``qlinear_moe_sort_workspace_size``, a function of the sizes alone."""
+    need = _i64(0)
+    _check(lib.qlinear_moe_sort_workspace_size(slots, num_experts, ctypes.byref(need)), "qlinear_moe_sort_workspace_size")
+    return need.value
+
+
 def moe_sort(expert_ids: torch.Tensor, num_experts: int, workspace: torch.Tensor | None = None):
     """Stable sort of the slots of expert_ids [T, top_k] by expert (``qlinear_moe_sort``)
     -> (a_offsets int32 [num_experts + 1], row_slot int32 [T * top_k], slot_row int32
@@ -717,16 +728,14 @@ def moe_sort(expert_ids: torch.Tensor, num_experts: int, workspace: torch.Tensor
     if expert_ids.dtype != torch.int32 or expert_ids.dim() != 2:
         raise TypeError("expert_ids must be int32 [T, top_k]")
     slots, dev = expert_ids.numel(), expert_ids.device
-    need = _i64(0)
-    _check(lib.qlinear_moe_sort_workspace_size(slots, int(num_experts), ctypes.byref(need)),
-           "qlinear_moe_sort_workspace_size")
-    offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
-    row_slot = torch.empty(slots, dtype=torch.int32, device=dev)
-    slot_row = torch.empty(tuple(expert_ids.shape), dtype=torch.int32, device=dev)
+    need = _sort_workspace_bytes(slots, int(num_experts))
+    offsets = torch.empty_strided((num_experts + 1,), (1,), dtype=torch.int32, device=dev)
+    row_slot = torch.empty_strided((slots,), (1,), dtype=torch.int32, device=dev)
+    slot_row = _out(None, expert_ids.shape, torch.int32, dev)
     if slots == 0:
         return offsets.zero_(), row_slot, slot_row
-    if workspace is None and need.value > 0:
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     nbytes = 0
     if workspace is not None:
         _require(workspace, "workspace")
