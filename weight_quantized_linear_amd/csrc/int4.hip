@@ -83,6 +83,18 @@ __device__ __forceinline__ u32x4 int4x8_to_bf16x8(uint32_t w) {
                __builtin_bit_cast(uint32_t, d)};
 }
 
+// The same in the order 0 .. 7, for two instructions more.
+__device__ __forceinline__ u32x4 int4x8_to_bf16x8_ordered(uint32_t w) {
+  const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
+  const uint32_t lo = __builtin_amdgcn_perm(odd, even, 0x05010400u), hi = __builtin_amdgcn_perm(odd, even, 0x07030602u);
+  const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, false);
+  const v2bf b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, true);
+  const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, false);
+  const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, true);
+  return u32x4{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, c),
+               __builtin_bit_cast(uint32_t, d)};
+}
+
 // Eight consecutive activation values in the decoder's order.
 __device__ __forceinline__ u32x4 decoder_order(u32x4 x) {
   return u32x4{__builtin_amdgcn_perm(x.y, x.x, 0x05040100u), __builtin_amdgcn_perm(x.w, x.z, 0x05040100u),
@@ -123,45 +135,50 @@ __device__ __forceinline__ u32x4 transpose_quarters(u32x4 v) {
 
 // ---------------------------------------------------------------- streaming products of few rows
 
-// 1 <= M <= 16 rows of x: the weight is read once, straight into registers,
+// 1 <= M <= 4 rows of x: the weight is read once, straight into registers,
 // and the matrix cores contract it, so that a code costs its decoding alone
-// (7 vector instructions per 8 codes; the dot products would be 4 more).
+// (7 vector instructions per 8 codes; the dot products would be 4 more per row of x).
 //
 // A wave owns NT tiles of 16 weight rows; lane (n = l % 16, quarter q = l / 16)
 // reads 16-byte chunks (32 codes) of row n, chunk 4 s + q of strip s, four
 // strips (a step of 512 codes) at a time.  The 16x16x32 MFMA takes codes as
 // its column operand: column n, and quarter q's 8 of 32 k slots hold dword t of
 // the lane's chunk.  The slots' order is free as long as x has the same.
+// Row 4 g + m of the other operand is x row m in the slots of quarter g and zero
+// elsewhere.  Four MFMAs then leave in lane (n, g) the sum over that lane's own
+// chunk for each m, to be scaled with the lane's own group, whatever the group
+// size: no lane exchanges, and only M of the 4 results per lane to correct.  The
+// quarters are added at the end.
 //
-// M <= 4 (kMasked): row 4 g + m of the other operand is x row m in the slots of
-// quarter g and zero elsewhere.  Four MFMAs then leave in lane (n, g) the
-// sum over that lane's own chunk for each m, to be scaled with the
-// lane's own group, whatever the group size: no lane exchanges, and only M of the
-// 4 results per lane to correct.  The quarters are added at the end.
+// x (decoder's order) and its sums over 32 values lie in LDS, kChunkK values of k at
+// a time; WK waves split the steps of a chunk and add their sums through LDS at
+// the end, where there are too few rows to fill the card.
 //
-// M <= 16 (!kMasked): row m is x row m; results of a group are complete only
-// over all quarters, so for groups below 128 the four dwords are transposed over
-// the quarters first, which makes MFMA t cover 32 consecutive k.
-//
-// x (decoder's order) and its sums over 32 or a group's values lie in LDS, kChunkK
-// values of k at a time; WK waves split the steps of a chunk and add their
-// sums through LDS at the end, where there are too few rows to fill the card.
+// Bound by HBM where the weight is large (128256 x 4096, one row: 52 us, 5.2 TB/s of
+// 5.7 that loads of 64 bytes from each of 16 rows reach without any work), by the launch
+// and the way to the first weights where it is small (4096 x 4096: 5.5 us).
 
 constexpr int kStep = 512;  // codes per lane quarter set and step: 4 strips
 
 template <int M, int NT, int WN, int WK> struct StreamLayout {
-  static constexpr bool kMasked = M <= 4;
   static constexpr int kWaves = WN * WK, kThreads = 64 * kWaves;
-  static constexpr int kRows = kMasked ? M : 16;
-  static constexpr int kChunkK = kMasked ? 4096 : WK > 2 ? kStep * WK : 1024;
-  static constexpr int kZeros = kMasked ? 1024 : 0;  // what the rows outside a quarter read
+  static constexpr int kChunkK = 4096;
+  static constexpr int kZeros = 1024;  // what the rows outside a quarter read
   static constexpr int kRowBytes = kChunkK * 2 + 16;
-  static constexpr int kSums = kZeros + kRows * kRowBytes;  // float32: masked [M][chunk / 32], else [chunk / 32][16]
-  static constexpr int kReduce = kWaves * NT * (kMasked ? M * 16 : 256) * 4;
-  static constexpr int kUse = kSums + kRows * (kChunkK / 32) * 4;
+  static constexpr int kSums = kZeros + M * kRowBytes;  // float32 [M][kChunkK / 32]
+  static constexpr int kReduce = kWaves * NT * M * 16 * 4;
+  static constexpr int kUse = kSums + M * (kChunkK / 32) * 4;
   static constexpr int kLds = kUse > kReduce ? kUse : kReduce;
-  static constexpr int kAcc = kMasked ? M : 4;
 };
+
+// The thread's index, anew at each call: the tiles' many addresses are made of it, and a
+// kernel that walks tiles would keep them all in registers from one tile to the next
+// (200 bytes a lane went to memory).
+__device__ __forceinline__ int own_thread() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
 
 // What a lane holds of one step of one row tile.  SH = log2(group) for 5, 6, 7;
 // 8 stands for all larger groups.  The scales and zero points of a step's groups
@@ -239,10 +256,8 @@ template <int M, int NT, int WN, int WK, int SH, typename Store>
 __device__ __forceinline__ void int4_stream_tile(char* lds, const Int4Args& a, const uint16_t* __restrict__ x, int rows,
                                                  int64_t N, int64_t K, int64_t n0, Store&& store) {
   using L = StreamLayout<M, NT, WN, WK>;
-  constexpr bool kMasked = L::kMasked;
-  // MFMAs per group inside a strip when the dwords are transposed.
-  constexpr int GS = SH == 5 ? 1 : SH == 6 ? 2 : 4;
-  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int thread = own_thread();
+  const int lane = thread & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(thread / kWave);
   const int ln = lane & 15, quarter = lane >> 4;
   const int wn = wave / WK, wk = wave % WK;
 
@@ -270,64 +285,37 @@ __device__ __forceinline__ void int4_stream_tile(char* lds, const Int4Args& a, c
     }
   };
 
-  float acc[NT][L::kAcc];
+  float acc[NT][M];
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int r = 0; r < L::kAcc; ++r) acc[i][r] = 0.f;
+    for (int m = 0; m < M; ++m) acc[i][m] = 0.f;
 
-  // Where this lane reads x and its sums in the staged chunk.
-  const bool mine = !kMasked || ((ln >> 2) == quarter && (ln & 3) < M);
-  const int xrow = kMasked ? (ln & 3) : ln;
-  const bool swapped = !kMasked && SH < 7;  // transposed dwords: MFMA t covers k = 32 t ..
-  const int xlane = L::kZeros + xrow * L::kRowBytes + (swapped ? 16 : 64) * quarter;
-  const int xt = swapped ? 64 : 16;  // bytes from one MFMA to the next
+  // Where this lane reads x in the staged chunk; lanes of other quarters or past `rows`
+  // read zeros (and a row past `rows` whatever sums: its results are not stored).
+  const bool mine = (ln >> 2) == quarter && (ln & 3) < rows;
+  const int xlane = L::kZeros + (ln & 3) * L::kRowBytes + 64 * quarter;
   const float* sums = reinterpret_cast<const float*>(lds + L::kSums);
 
-  // One strip: k0 = its first value inside the chunk; scale(i, c, s, z) of row tile i, 32-code chunk c.
+  // One strip: its place in the staged x, its first 32-value chunk; scale(i, c, s, z) of row tile i, chunk c.
   auto strip = [&](int xbase, int chunk0, const u32x4 (&w)[NT], auto&& scale) {
     u32x4 xa[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) xa[t] = *reinterpret_cast<const u32x4*>(lds + xbase + t * xt);
-    if constexpr (kMasked) {
-      float xs[M];
+    for (int t = 0; t < 4; ++t) xa[t] = *reinterpret_cast<const u32x4*>(lds + xbase + t * 16);
+    float xs[M];
 #pragma unroll
-      for (int m = 0; m < M; ++m) xs[m] = sums[m * (L::kChunkK / 32) + chunk0 + quarter];
+    for (int m = 0; m < M; ++m) xs[m] = sums[m * (L::kChunkK / 32) + chunk0 + quarter];
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        v4f part{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < NT; ++i) {
+      v4f part{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-          part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, xa[t]),
-                                                         __builtin_bit_cast(v8bf, int4x8_to_bf16x8(w[i][t])), part, 0, 0, 0);
-        float s, z;
-        scale(i, quarter, s, z);
+      for (int t = 0; t < 4; ++t)
+        part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, xa[t]),
+                                                       __builtin_bit_cast(v8bf, int4x8_to_bf16x8(w[i][t])), part, 0, 0, 0);
+      float s, z;
+      scale(i, quarter, s, z);
 #pragma unroll
-        for (int m = 0; m < M; ++m) acc[i][m] = fmaf(s, fmaf(-z, xs[m], part[m]), acc[i][m]);
-      }
-    } else {
-      u32x4 wt[NT];
-#pragma unroll
-      for (int i = 0; i < NT; ++i) wt[i] = swapped ? transpose_quarters(w[i]) : w[i];
-#pragma unroll
-      for (int g = 0; g < 4 / GS; ++g) {
-        v4f xs{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < GS; ++c)
-          xs += *reinterpret_cast<const v4f*>(sums + (chunk0 + g * GS + c) * 16 + quarter * 4);
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          v4f part{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int t = g * GS; t < (g + 1) * GS; ++t)
-            part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, xa[t]),
-                                                           __builtin_bit_cast(v8bf, int4x8_to_bf16x8(wt[i][t])), part, 0, 0, 0);
-          float s, z;
-          scale(i, g * GS, s, z);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[i][r] = fmaf(s, fmaf(-z, xs[r], part[r]), acc[i][r]);
-        }
-      }
+      for (int m = 0; m < M; ++m) acc[i][m] = fmaf(s, fmaf(-z, xs[m], part[m]), acc[i][m]);
     }
   };
 
@@ -341,7 +329,7 @@ __device__ __forceinline__ void int4_stream_tile(char* lds, const Int4Args& a, c
     // x rows in the decoder's order, zeros past K, and the sums of 32 values.
     const int klen = int(K - kc < L::kChunkK ? (K - kc + kStrip - 1) / kStrip * kStrip : L::kChunkK);
     const int per_row = klen / 8;
-    for (int idx = threadIdx.x; idx < rows * per_row; idx += L::kThreads) {  // klen % 32 == 0: quads stay together
+    for (int idx = thread; idx < rows * per_row; idx += L::kThreads) {  // klen % 32 == 0: quads stay together
       const int m = idx / per_row, c = idx % per_row;
       const int64_t k = kc + c * 8;
       const uint16_t* p = x + m * K + k;
@@ -349,27 +337,10 @@ __device__ __forceinline__ void int4_stream_tile(char* lds, const Int4Args& a, c
       *reinterpret_cast<u32x4*>(lds + L::kZeros + m * L::kRowBytes + c * 16) = v;
       float s = dpp_add<0xB1>(sum8(v, 0.f));
       s = dpp_add<0x4E>(s);
-      if ((c & 3) == 0) {
-        float* dst = reinterpret_cast<float*>(lds + L::kSums);
-        if constexpr (kMasked) dst[m * (L::kChunkK / 32) + (c >> 2)] = s;
-        else dst[(c >> 2) * 16 + m] = s;
-      }
+      if ((c & 3) == 0) reinterpret_cast<float*>(lds + L::kSums)[m * (L::kChunkK / 32) + (c >> 2)] = s;
     }
-    if (ch == 0) {  // what rows without x read
-      if constexpr (kMasked) {
-        for (int i = threadIdx.x; i < L::kZeros / 16; i += L::kThreads)
-          *reinterpret_cast<u32x4*>(lds + i * 16) = u32x4{0u, 0u, 0u, 0u};
-      }
-      for (int m = rows; m < L::kRows; ++m) {
-        for (int c = threadIdx.x; c < L::kChunkK / 8; c += L::kThreads)
-          *reinterpret_cast<u32x4*>(lds + L::kZeros + m * L::kRowBytes + c * 16) = u32x4{0u, 0u, 0u, 0u};
-        for (int c = threadIdx.x; c < L::kChunkK / 32; c += L::kThreads) {
-          float* dst = reinterpret_cast<float*>(lds + L::kSums);
-          if constexpr (kMasked) dst[m * (L::kChunkK / 32) + c] = 0.f;
-          else dst[c * 16 + m] = 0.f;
-        }
-      }
-    }
+    if (ch == 0)
+      for (int i = thread; i < L::kZeros / 16; i += L::kThreads) *reinterpret_cast<u32x4*>(lds + i * 16) = u32x4{0u, 0u, 0u, 0u};
     wait_lds();
     block_barrier();
 
@@ -412,33 +383,25 @@ __device__ __forceinline__ void int4_stream_tile(char* lds, const Int4Args& a, c
     block_barrier();  // every wave is done with this chunk of x
   }
 
-  if constexpr (kMasked) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+  for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int m = 0; m < M; ++m) {
-        acc[i][m] += __shfl_xor(acc[i][m], 16, kWave);
-        acc[i][m] += __shfl_xor(acc[i][m], 32, kWave);
-      }
-  }
+    for (int m = 0; m < M; ++m) {
+      acc[i][m] += __shfl_xor(acc[i][m], 16, kWave);
+      acc[i][m] += __shfl_xor(acc[i][m], 32, kWave);
+    }
   if constexpr (WK > 1) {
-    // red[wn][wk][i][value][lane of the value]: the waves' sums are added in wave order.
-    constexpr int kVals = kMasked ? M * 16 : 256;
+    // red[wave][i][m][n]: the waves' sums are added in wave order.
+    constexpr int kVals = M * 16;
     float* red = reinterpret_cast<float*>(lds);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      if constexpr (kMasked) {
-        if (quarter == 0)
+    for (int i = 0; i < NT; ++i)
+      if (quarter == 0)
 #pragma unroll
-          for (int m = 0; m < M; ++m) red[((wave * NT) + i) * kVals + m * 16 + ln] = acc[i][m];
-      } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) red[((wave * NT) + i) * kVals + (quarter * 4 + r) * 16 + ln] = acc[i][r];
-      }
-    }
+        for (int m = 0; m < M; ++m) red[(wave * NT + i) * kVals + m * 16 + ln] = acc[i][m];
     wait_lds();
     block_barrier();
-    for (int idx = threadIdx.x; idx < WN * NT * kVals; idx += L::kThreads) {
+    for (int idx = thread; idx < WN * NT * kVals; idx += L::kThreads) {
       const int w = idx / (NT * kVals), rest = idx % (NT * kVals);
       const int i = rest / kVals, m = rest % kVals / 16, n = rest % 16;
       if (m >= rows) continue;
@@ -449,18 +412,10 @@ __device__ __forceinline__ void int4_stream_tile(char* lds, const Int4Args& a, c
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int n = (wn * NT + i) * 16 + ln;
-      if constexpr (kMasked) {
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int m = 0; m < M; ++m)
-          if (quarter == m && m < rows) store(m, n, acc[i][m]);
-      } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (quarter * 4 + r < rows) store(quarter * 4 + r, n, acc[i][r]);
-      }
-    }
+      for (int m = 0; m < M; ++m)
+        if (quarter == m && m < rows) store(m, (wn * NT + i) * 16 + ln, acc[i][m]);
   }
 }
 
@@ -483,16 +438,18 @@ __global__ __launch_bounds__(64 * WN * WK) void int4_stream_kernel(Int4Args a, c
 //
 // Weights go straight into the registers of the wave that multiplies them: lane
 // (n = l % 16, quarter h = l / 16) reads the 16 bytes k = 32 h .. 32 h + 31 of its
-// row's strip, and two half-wave swap stages transpose the
-// 4x4 dwords over the quarters, after which dword t holds k = 32 t + 8 h ..
-// + 7: MFMA step t covers 32 consecutive k, so a group of 32 is a whole step.
-// Activation: the strip [BM][128] goes through registers into LDS in the
-// decoder's order (16-byte chunks XOR-permuted by row against bank
-// conflicts).
+// row's strip.  For groups of 128 and more MFMA step t takes dword t of every lane, k =
+// 32 h + 8 t ..; for smaller ones two half-wave swap stages first transpose the
+// 4x4 dwords over the quarters, and step t covers k = 32 t + 8 h .., one group's.
+// Activation: the strip [BM][128] goes through registers into LDS as it is, 16-byte
+// chunks XOR-permuted by row against bank conflicts: the vector ALU is what these
+// tiles run out of, so the order of k is mended where a value is decoded once for
+// the whole tile (2 instructions per 8 codes) and not where x is staged.
 //
 // After the last step of a group: acc += scale * group.  The zero points are
 // taken off by the matrix cores too: sum_groups sum_x * (zero * scale) is a
-// product over the groups.  A group's sum of x (float32, 24 bits) is three bfloat16 cut
+// product over the groups.  A group's sum of x (a product with ones) is in float32, 24
+// bits, which are three bfloat16 cut
 // from it, hi + mid + lo, and zero * scale (8 by 8 bits) is two, both exact, so six
 // of a quarter's eight k slots of one MFMA hold all products of one group,
 // and four groups need one instruction per 16x16 tile; on the
@@ -514,16 +471,6 @@ template <int MT, int NT, int WM, int WN, int WK> struct Int4Tile {
   static_assert(WK == 1 || WM * WN == 1, "either the tile or K is split over the waves");
 };
 
-// Sum over groups of 2^LOG neighbouring lanes (LOG = 2, 3, 4), in each lane.
-template <int LOG>
-__device__ __forceinline__ float lanes_sum(float v) {
-  v = dpp_add<0xB1>(v);
-  v = dpp_add<0x4E>(v);
-  if constexpr (LOG >= 3) v = dpp_add<0x141>(v);
-  if constexpr (LOG >= 4) v = dpp_add<0x140>(v);
-  return v;
-}
-
 __device__ __forceinline__ float cut_bf16(float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); }
 
 // -s as (hi, mid, lo, hi, mid, lo, 0, 0), each exact in bfloat16.
@@ -539,6 +486,12 @@ __device__ __forceinline__ u32x4 factor_pieces(float v) {
   return u32x4{h >> 16 | h, h >> 16 | l, l >> 16 | l, 0u};
 }
 
+// Buffer loads take a 32-bit lane offset and a uniform one, without address arithmetic on
+// the vector ALU.  The record count is not used as a bound: every offset lies inside.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, -1, 0x00020000);
+}
+
 // GS: MFMA steps per group inside a strip (1, 2, 4; 4 also for larger groups).
 // store(m, n, value): m relative to the tile's first row.  Every thread of the
 // block calls it; the block's LDS is free when it begins.
@@ -547,6 +500,7 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
                                           int64_t N, int64_t K, int64_t n0, Store&& store) {
   using L = Int4Tile<MT, NT, WM, WN, WK>;
   constexpr int G = 4 / GS;  // groups per strip
+  constexpr int kTiles = MT * WM, kSummers = WM * WN;
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int ln = lane & 15, quarter = lane >> 4;
   const int wn = WK > 1 ? 0 : wave % WN, wm = WK > 1 ? 0 : wave / WN, wk = WK > 1 ? wave : 0;
@@ -559,6 +513,7 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
   const uint16_t* const sbase = a.scale + n0 * a.groups;
   // Without zero points the scales' bytes are read in their place and not used.
   const uint8_t* const zbase = (a.zero ? a.zero : reinterpret_cast<const uint8_t*>(a.scale)) + n0 * a.groups;
+  const __amdgpu_buffer_rsrc_t wbuf = buffer_at(wbase), sbuf_ = buffer_at(sbase), zbuf = buffer_at(zbase), xbuf = buffer_at(x);
   uint32_t woff[NT], soff[NT], xoff[L::kChunks];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
@@ -570,7 +525,7 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
 #pragma unroll
   for (int j = 0; j < L::kChunks; ++j) {
     const int m = (stager + j * L::kStagers) >> 4;
-    xoff[j] = uint32_t(m < rows ? m : rows - 1) * uint32_t(K) + (stager & 15) * 8;  // rows past the end likewise
+    xoff[j] = uint32_t(m < rows ? m : rows - 1) * uint32_t(K) * 2 + (stager & 15) * 16;  // rows past the end likewise
   }
 
   // A strip's G groups of a row are neighbours: their scales come in one load
@@ -583,27 +538,26 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
   // A whole strip: no lane branches, so that nothing waits for a load before
   // the strip after this one is staged.
   auto fetch = [&](int strip) {
-    const int64_t k = int64_t(strip) * kStrip, at = k >> a.shift;
+    const int at = int((int64_t(strip) * kStrip) >> a.shift);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      wreg[i] = ldw16(wbase + (k >> 1) + woff[i]);
-      const uint16_t* sp = sbase + at + soff[i];
-      const uint8_t* zp = zbase + at + soff[i];
+      wreg[i] = __builtin_amdgcn_raw_buffer_load_b128(wbuf, woff[i], strip * (kStrip / 2), 0);
       if constexpr (G == 4) {
-        const u32x2 v = ld_any2<u32x2>(sp);
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(sbuf_, soff[i] * 2, at * 2, 0);
         sreg[i][0] = v.x;
         sreg[i][1] = v.y;
-        zreg[i] = ld_any1<uint32_t>(zp);
+        zreg[i] = __builtin_amdgcn_raw_buffer_load_b32(zbuf, soff[i], at, 0);
       } else if constexpr (G == 2) {
-        sreg[i][0] = ld_any2<uint32_t>(sp);
-        zreg[i] = ld_any1<uint16_t>(zp);
+        sreg[i][0] = __builtin_amdgcn_raw_buffer_load_b32(sbuf_, soff[i] * 2, at * 2, 0);
+        zreg[i] = __builtin_amdgcn_raw_buffer_load_b16(zbuf, soff[i], at, 0);
       } else {
-        shalf[i] = *sp;
-        zreg[i] = *zp;
+        shalf[i] = __builtin_amdgcn_raw_buffer_load_b16(sbuf_, soff[i] * 2, at * 2, 0);
+        zreg[i] = __builtin_amdgcn_raw_buffer_load_b8(zbuf, soff[i], at, 0);
       }
     }
 #pragma unroll
-    for (int j = 0; j < L::kChunks; ++j) xreg[j] = ldx16(x + k + xoff[j]);
+    for (int j = 0; j < L::kChunks; ++j)
+      xreg[j] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, xoff[j], strip * (kStrip * 2), 0);
   };
   // The last, partial strip: zeros behind K, and groups past K are nothing,
   // whatever lies there.
@@ -625,7 +579,7 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
 #pragma unroll
     for (int j = 0; j < L::kChunks; ++j) {
       const int values = left - (stager & 15) * 8;
-      const uint16_t* p = x + k + xoff[j];
+      const uint16_t* p = x + k + (xoff[j] >> 1);
       xreg[j] = values >= 8 ? ldx16(p) : ld_halves(p, values);
     }
   };
@@ -635,9 +589,9 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[mt][i] = v4f{0.f, 0.f, 0.f, 0.f};
-  float zs[NT];  // zero * scale of this quarter's slot
+  float zs[NT], due[NT];  // zero * scale of this quarter's slot: being filled, and of full slots
 #pragma unroll
-  for (int i = 0; i < NT; ++i) zs[i] = 0.f;
+  for (int i = 0; i < NT; ++i) zs[i] = due[i] = 0.f;
   for (int i = stager; i < 2 * L::kSumBytes / 16; i += L::kStagers)
     *reinterpret_cast<u32x4*>(mem + L::kSums + i * 16) = u32x4{0u, 0u, 0u, 0u};
   if constexpr (WK == 1) __syncthreads();  // a slot's first writer need not be its clearer
@@ -645,10 +599,7 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
   auto correct = [&](const char* sums) {
     v8bf zb[NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      zb[i] = __builtin_bit_cast(v8bf, factor_pieces(zs[i]));
-      zs[i] = 0.f;
-    }
+    for (int i = 0; i < NT; ++i) zb[i] = __builtin_bit_cast(v8bf, factor_pieces(due[i]));
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       const v8bf xb = *reinterpret_cast<const v8bf*>(sums + (quarter * L::kBM + (wm * MT + mt) * 16 + ln) * 16);
@@ -656,8 +607,15 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
       for (int i = 0; i < NT; ++i) acc[mt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, zb[i], acc[mt][i], 0, 0, 0);
     }
   };
+  // Where row `row` keeps what a quarter's slots of step t hold.  A read of 64 lanes is free of
+  // bank conflicts if the quarters differ in the low bits of the place, so where quarter q reads chunk
+  // 4 q + t (groups of 128 and more) the two halves of the chunk's number change places.
+  auto place = [&](int row, int t) { return row * (kStrip * 2) + (((t * 4 + quarter) ^ ln) << 4); };
 
-  int buf = 0, slot = 0, sbuf = 0;  // the strip's buffer; its first group's slot and their buffer
+  // buf: the strip's buffer; slot, sbuf: its first group's slot and the slots' buffer.  Sums are
+  // made while their strip is multiplied, so full slots are due one barrier later.
+  int buf = 0, slot = 0, sbuf = 0;
+  bool full = false;
   if (wk < nwhole) fetch(wk);
   for (int strip = wk; strip < nstrips; strip += WK) {
     if (strip >= nwhole) fetch_tail(strip);
@@ -671,15 +629,11 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
       if constexpr (G == 4) asm volatile("" : "+v"(sreg[i][1]));
     }
     char* xs = mem + buf * L::kXBytes;
-    char* sums = mem + L::kSums + sbuf * L::kSumBytes;
 #pragma unroll
     for (int j = 0; j < L::kChunks; ++j) {
       const int idx = stager + j * L::kStagers, m = idx >> 4, c = idx & 15;
-      const u32x4 v = decoder_order(xreg[j]);
-      *reinterpret_cast<u32x4*>(xs + m * (kStrip * 2) + ((c ^ (m & 15)) << 4)) = v;
-      const float s = lanes_sum<(GS == 4 ? 4 : GS == 2 ? 3 : 2)>(sum8(v, 0.f));
-      if ((c & (4 * GS - 1)) == 0)
-        *reinterpret_cast<u32x4*>(sums + ((slot + c / (4 * GS)) * L::kBM + m) * 16) = sum_pieces(s);
+      const int p = GS == 4 ? (c & 3) * 4 + (c >> 2) : c;
+      *reinterpret_cast<u32x4*>(xs + m * (kStrip * 2) + ((p ^ (m & 15)) << 4)) = xreg[j];
     }
     u32x4 w[NT];
     uint32_t sp[NT][2];
@@ -689,11 +643,11 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int t = 0; t < GS; ++t) codes[i][t] = __builtin_bit_cast(v8bf, int4x8_to_bf16x8(w[i][g * GS + t]));
+        for (int t = 0; t < GS; ++t) codes[i][t] = __builtin_bit_cast(v8bf, int4x8_to_bf16x8_ordered(w[i][g * GS + t]));
     };
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      w[i] = transpose_quarters(wreg[i]);
+      w[i] = GS == 4 ? wreg[i] : transpose_quarters(wreg[i]);
       sp[i][0] = G == 1 ? shalf[i] : sreg[i][0];
       if constexpr (G == 4) sp[i][1] = sreg[i][1];
       if (!a.zero) zreg[i] = 0x08080808u;
@@ -704,39 +658,69 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
     if (strip + WK < nwhole) fetch(strip + WK);
     wait_lds();
     if constexpr (WK == 1) block_barrier();
-    {
+    // The sums of x over the strip's groups, row tiles dealt to the waves.
+    char* sums = mem + L::kSums + sbuf * L::kSumBytes;
+    const v8bf ones = __builtin_bit_cast(v8bf, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+#pragma unroll
+    for (int q = 0; q < (kTiles + kSummers - 1) / kSummers; ++q) {
+      const int tile = (WK > 1 ? 0 : wave) + q * kSummers;
+      if (kTiles % kSummers != 0 && tile >= kTiles) break;  // uniform
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        if (g > 0) decode(g);
+        v4f total{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          v4f part[NT];
+        for (int t = g * GS; t < (g + 1) * GS; ++t)
+          total = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              *reinterpret_cast<const v8bf*>(xs + place(tile * 16 + ln, t)), ones, total, 0, 0, 0);
+        const float mine = (ln & 2) ? ((ln & 1) ? total[3] : total[2]) : ((ln & 1) ? total[1] : total[0]);
+        if (ln < 4)
+          *reinterpret_cast<u32x4*>(sums + ((slot + g) * L::kBM + tile * 16 + quarter * 4 + ln) * 16) = sum_pieces(mine);
+      }
+    }
 #pragma unroll
-          for (int t = 0; t < GS; ++t) {
-            const int c = (g * GS + t) * 4 + quarter;
-            const v8bf xa =
-                *reinterpret_cast<const v8bf*>(xs + ((wm * MT + mt) * 16 + ln) * (kStrip * 2) + ((c ^ ln) << 4));
+    for (int g = 0; g < G; ++g) {
+      if (g > 0) decode(g);
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
-              part[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa, codes[i][t], t == 0 ? v4f{0.f, 0.f, 0.f, 0.f} : part[i],
-                                                                0, 0, 0);
-          }
+      for (int mt = 0; mt < MT; ++mt) {
+        v4f part[NT];
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            const float s = scale(i, g);
+        for (int t = 0; t < GS; ++t) {
+          const v8bf xa = *reinterpret_cast<const v8bf*>(xs + place((wm * MT + mt) * 16 + ln, g * GS + t));
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[mt][i][r] = fmaf(s, part[i][r], acc[mt][i][r]);
-          }
+          for (int i = 0; i < NT; ++i)
+            part[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa, codes[i][t], t == 0 ? v4f{0.f, 0.f, 0.f, 0.f} : part[i],
+                                                              0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const float s = scale(i, g);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[mt][i][r] = fmaf(s, part[i][r], acc[mt][i][r]);
         }
       }
     }
+    if (full) correct(mem + L::kSums + (sbuf ^ 1) * L::kSumBytes);
     slot += G;
-    if (slot == kSlots || strip + WK >= nstrips) {  // unfilled slots have zs = 0 and finite sums
-      correct(sums);
+    full = slot == kSlots;
+    if (full) {
       slot = 0;
       sbuf ^= 1;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        due[i] = zs[i];
+        zs[i] = 0.f;
+      }
     }
     if constexpr (WK == 1) buf ^= 1;
+  }
+  wait_lds();
+  if constexpr (WK == 1) block_barrier();
+  if (full) {
+    correct(mem + L::kSums + (sbuf ^ 1) * L::kSumBytes);
+  } else if (slot > 0) {  // unfilled slots have zs = 0 and finite sums
+#pragma unroll
+    for (int i = 0; i < NT; ++i) due[i] = zs[i];
+    correct(mem + L::kSums + sbuf * L::kSumBytes);
   }
 
   if constexpr (WK > 1) {
@@ -773,6 +757,368 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
   }
 }
 
+// A tile's way out: `out` [rows, N] from row 0, column n0 of the tile on.  Plain results
+// leave through a buffer whose record count ends with the last row, so that neither rows nor
+// columns need a branch (a column past N gets an offset past the end), with the row's offset in a
+// scalar register: 3 instructions per value where the general store takes 25, which for
+// 128x256 were 5 us.  With an epilogue, or where a tile spans 2 GiB, values go
+// one by one.
+struct TileOut {
+  void* out;      // row 0, column 0
+  int64_t rows, N, n0;
+  int64_t row0;   // of the epilogue's operands
+  float alpha;
+  int bf16;
+  const Epilogue* epi;  // null: none
+
+  // put(m, n, v): m uniform and the first of 4 rows of quarter 0; n of lane 0.
+  template <int BM, typename F>
+  __device__ __forceinline__ void write(F&& each) const {
+    const int lane = threadIdx.x & (kWave - 1), ln = lane & 15, quarter = lane >> 4;
+    const int64_t es = bf16 ? 2 : 4;
+    const bool plain = !(epi && epi->on) && int64_t(BM) * N * es < (int64_t(1) << 31);
+    if (plain) {
+      const int64_t live = rows < BM ? rows : BM;
+      const uint32_t bytes = uint32_t((live * N - n0) * es);
+      const __amdgpu_buffer_rsrc_t buf =
+          __builtin_amdgcn_make_buffer_rsrc(static_cast<char*>(out) + n0 * es, 0, int(bytes), 0x00020000);
+      const uint32_t line = uint32_t(N * es), lane_at = uint32_t(quarter * 4) * line + uint32_t(ln * es);
+      const int64_t width = N - n0;
+      each([&](int m, int n, v4f v) {
+        const uint32_t at = n + ln < width ? lane_at + uint32_t(n * es) : 0x80000000u;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float f = v[r] * alpha;
+          if (bf16)
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, static_cast<__bf16>(f)), buf, at,
+                                                  uint32_t(m + r) * line, 0);
+          else
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f), buf, at, uint32_t(m + r) * line, 0);
+        }
+      });
+      return;
+    }
+    each([&](int m, int n, v4f v) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int64_t row = m + quarter * 4 + r, col = n0 + n + ln;
+        if (row >= rows || col >= N) continue;
+        float f = v[r] * alpha;
+        if (epi && epi->on) f = epi_apply(*epi, f, row0 + row, col);
+        store_out(out, row * N + col, f, 1.f, bf16);
+      }
+    });
+  }
+};
+
+// The same product with every wave's work in flight at once, for tiles that use all of a
+// CU's registers: while the matrix cores run strip s, the wave decodes the codes of strip
+// s + 1, moves its x from registers to the other LDS buffer, and loads strip s + 2.  WN waves
+// side by side along N, one barrier per strip.  (With these phases one after the other
+// the 128x256 tile took 2.9 us for a strip of which the matrix cores need 1.1.)
+template <int MT, int NT, int WN, int GS>
+__device__ __forceinline__ void int4_pipe_tile(char* lds, const Int4Args& a, const uint16_t* __restrict__ x,
+                                               int64_t rows, int64_t N, int64_t K, int64_t n0, const TileOut& to) {
+  using L = Int4Tile<MT, NT, 1, WN, 1>;
+  constexpr int G = 4 / GS;  // groups per strip
+  const int thread = own_thread();
+  const int lane = thread & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(thread / kWave);
+  const int ln = lane & 15, quarter = lane >> 4;
+  const int nwhole = int(K / kStrip);
+
+  // Uniform bases and 32-bit lane offsets (K < 2^23).
+  const uint8_t* const wbase = a.w + n0 * a.row_bytes;
+  const uint16_t* const sbase = a.scale + n0 * a.groups;
+  // Without zero points the scales' bytes are read in their place and not used.
+  const uint8_t* const zbase = (a.zero ? a.zero : reinterpret_cast<const uint8_t*>(a.scale)) + n0 * a.groups;
+  const __amdgpu_buffer_rsrc_t wbuf = buffer_at(wbase), scbuf = buffer_at(sbase), zbuf = buffer_at(zbase), xbuf = buffer_at(x);
+  uint32_t woff[NT], soff[NT], xoff[L::kChunks];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int n = wave * 16 * NT + i * 16 + ln;
+    const uint32_t row = n0 + n < N ? n : uint32_t(N - 1 - n0);  // columns past N re-read the last row, never stored
+    woff[i] = row * uint32_t(a.row_bytes) + quarter * 16;
+    soff[i] = row * uint32_t(a.groups);
+  }
+#pragma unroll
+  for (int j = 0; j < L::kChunks; ++j) {
+    const int m = (thread + j * L::kThreads) >> 4;
+    xoff[j] = uint32_t(m < rows ? m : rows - 1) * uint32_t(K) * 2 + (thread & 15) * 16;  // rows past the end likewise
+  }
+
+  // A strip's weights as they come; its G groups' scales and zero points stay packed.
+  struct Raw {
+    u32x4 w[NT];
+    uint32_t s[NT][2];
+    uint32_t z[NT];
+    uint16_t half[NT], zhalf[NT];  // in place of s where G = 1, of z where G < 4
+  };
+  // Decoded: MFMA operands and packed scales.
+  struct Codes {
+    v8bf b[NT][4];
+    uint32_t s[NT][2];
+    __device__ __forceinline__ float scale(int i, int g) const {
+      if constexpr (G == 1) return __uint_as_float(s[i][0]);
+      else return __uint_as_float((g & 1) ? s[i][g >> 1] & 0xFFFF0000u : s[i][g >> 1] << 16);
+    }
+  };
+  u32x4 xreg[L::kChunks];
+  auto fetch_w = [&](Raw& f, int strip) {
+    const int at = int((int64_t(strip) * kStrip) >> a.shift);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      f.w[i] = __builtin_amdgcn_raw_buffer_load_b128(wbuf, woff[i], strip * (kStrip / 2), 0);
+      if constexpr (G == 4) {
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(scbuf, soff[i] * 2, at * 2, 0);
+        f.s[i][0] = v.x;
+        f.s[i][1] = v.y;
+        f.z[i] = __builtin_amdgcn_raw_buffer_load_b32(zbuf, soff[i], at, 0);
+      } else if constexpr (G == 2) {
+        f.s[i][0] = __builtin_amdgcn_raw_buffer_load_b32(scbuf, soff[i] * 2, at * 2, 0);
+        f.zhalf[i] = __builtin_amdgcn_raw_buffer_load_b16(zbuf, soff[i], at, 0);
+      } else {
+        f.half[i] = __builtin_amdgcn_raw_buffer_load_b16(scbuf, soff[i] * 2, at * 2, 0);
+        f.zhalf[i] = __builtin_amdgcn_raw_buffer_load_b8(zbuf, soff[i], at, 0);
+      }
+    }
+  };
+  auto fetch_x = [&](int strip) {
+#pragma unroll
+    for (int j = 0; j < L::kChunks; ++j)
+      xreg[j] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, xoff[j], strip * (kStrip * 2), 0);
+  };
+  // The last, partial strip: zeros behind K, and groups past K are nothing,
+  // whatever lies there.
+  auto fetch_tail = [&](Raw& f, int strip) {
+    const int64_t k = int64_t(strip) * kStrip, at = k >> a.shift;
+    const int left = int(K - k);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int codes = left - quarter * 32;
+      const uint8_t* p = wbase + (k >> 1) + woff[i];
+      f.w[i] = codes >= 31 ? ldw16(p) : ld_bytes(p, (codes + 1) >> 1);
+      const int groups = int(a.groups - at < G ? a.groups - at : G);
+      const u32x4 v = ld_halves(sbase + at + soff[i], groups);
+      f.s[i][0] = v.x;
+      f.s[i][1] = v.y;
+      f.half[i] = uint16_t(v.x);
+      f.z[i] = ld_bytes(zbase + at + soff[i], groups).x;
+      f.zhalf[i] = uint16_t(f.z[i]);
+    }
+#pragma unroll
+    for (int j = 0; j < L::kChunks; ++j) {
+      const int values = left - (thread & 15) * 8;
+      const uint16_t* p = x + k + (xoff[j] >> 1);
+      xreg[j] = values >= 8 ? ldx16(p) : ld_halves(p, values);
+    }
+  };
+  auto stage_x = [&](int buf) {
+#pragma unroll
+    for (int j = 0; j < L::kChunks; ++j) {
+      const int idx = thread + j * L::kThreads, m = idx >> 4, c = idx & 15;
+      const int p = GS == 4 ? (c & 3) * 4 + (c >> 2) : c;
+      *reinterpret_cast<u32x4*>(lds + buf * L::kXBytes + m * (kStrip * 2) + ((p ^ (m & 15)) << 4)) = xreg[j];
+    }
+  };
+
+  v4f acc[MT][NT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[mt][i] = v4f{0.f, 0.f, 0.f, 0.f};
+  // zero * scale of this quarter's slot: of the slots being filled, and of full ones.  The
+  // sums of a strip are made while it is multiplied, so full slots are due in the next strip.
+  float zs[NT], due[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) zs[i] = due[i] = 0.f;
+  for (int i = thread; i < 2 * L::kSumBytes / 16; i += L::kThreads)
+    *reinterpret_cast<u32x4*>(lds + L::kSums + i * 16) = u32x4{0u, 0u, 0u, 0u};
+  auto correct = [&](const char* sums) {
+    v8bf zb[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) zb[i] = __builtin_bit_cast(v8bf, factor_pieces(due[i]));
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const v8bf xb = *reinterpret_cast<const v8bf*>(sums + (quarter * L::kBM + mt * 16 + ln) * 16);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[mt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, zb[i], acc[mt][i], 0, 0, 0);
+    }
+  };
+  // Where row `row` keeps what a quarter's slots of step t hold.  A read of 64 lanes is free of
+  // bank conflicts if the quarters differ in the low bits of the place, so where quarter q reads chunk
+  // 4 q + t (groups of 128 and more) the two halves of the chunk's number change places.
+  auto place = [&](int row, int t) { return row * (kStrip * 2) + (((t * 4 + quarter) ^ ln) << 4); };
+
+  // Before a strip's codes: `slot` its first group's; live: the strip exists (else nothing is noted).
+  const uint32_t zkeep = a.zero ? 0xFFFFFFFFu : 0u, zset = a.zero ? 0u : 0x08080808u;
+  auto begin = [&](Raw& f, Codes& c, int slot, bool live) {
+    const int first = live ? slot : kSlots;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      // What is made of the loaded values is made from here on: the compiler would
+      // widen a scale or a zero point behind its load, where it waits for memory.
+      uint32_t z;
+      if constexpr (G == 1) {
+        asm volatile("v_lshlrev_b32 %0, 16, %1" : "=v"(c.s[i][0]) : "v"(f.half[i]));
+      } else {
+        asm volatile("" : "+v"(f.s[i][0]));
+        c.s[i][0] = f.s[i][0];
+      }
+      if constexpr (G == 4) {
+        asm volatile("" : "+v"(f.s[i][1]), "+v"(f.z[i]));
+        c.s[i][1] = f.s[i][1];
+        z = f.z[i];
+      } else {
+        asm volatile("v_mov_b32 %0, %1" : "=v"(z) : "v"(f.zhalf[i]));  // only its first G bytes are used
+      }
+      if constexpr (GS < 4) f.w[i] = transpose_quarters(f.w[i]);
+      z = (z & zkeep) | zset;
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        zs[i] = quarter == first + g ? c.scale(i, g) * float((z >> (8 * g)) & 255u) : zs[i];
+    }
+  };
+  auto decode = [&](const Raw& f, Codes& c, int d) {
+    c.b[d / 4][d % 4] = __builtin_bit_cast(v8bf, int4x8_to_bf16x8_ordered(f.w[d / 4][d % 4]));
+  };
+  // Sums of x over the groups of the strip in buffer `buf`, row tiles dealt to the waves.
+  auto sum_x = [&](int buf, int set, int slot) {
+    const char* xs = lds + buf * L::kXBytes;
+    char* sums = lds + L::kSums + set * L::kSumBytes;
+    const v8bf ones = __builtin_bit_cast(v8bf, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+#pragma unroll
+    for (int q = 0; q < (MT + WN - 1) / WN; ++q) {
+      const int tile = wave + q * WN;
+      if (MT % WN != 0 && tile >= MT) break;  // uniform
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        v4f total{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int t = g * GS; t < (g + 1) * GS; ++t)
+          total = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              *reinterpret_cast<const v8bf*>(xs + place(tile * 16 + ln, t)), ones, total, 0, 0, 0);
+        const float mine = (ln & 2) ? ((ln & 1) ? total[3] : total[2]) : ((ln & 1) ? total[1] : total[0]);
+        if (ln < 4)
+          *reinterpret_cast<u32x4*>(sums + ((slot + g) * L::kBM + tile * 16 + quarter * 4 + ln) * 16) = sum_pieces(mine);
+      }
+    }
+  };
+  // A row tile's x is read while the one before it is multiplied; between(mt) runs after each.
+  auto multiply = [&](int buf, const Codes& c, auto&& between) {
+    const char* xs = lds + buf * L::kXBytes;
+    v8bf xa[2][4];
+    auto read = [&](int mt) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) xa[mt & 1][t] = *reinterpret_cast<const v8bf*>(xs + place(mt * 16 + ln, t));
+    };
+    read(0);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      if (mt + 1 < MT) read(mt + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        v4f part[NT];
+#pragma unroll
+        for (int t = 0; t < GS; ++t)
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+            part[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa[mt & 1][g * GS + t], c.b[i][g * GS + t],
+                                                              t == 0 ? v4f{0.f, 0.f, 0.f, 0.f} : part[i], 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const float s = c.scale(i, g);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[mt][i][r] = fmaf(s, part[i][r], acc[mt][i][r]);
+        }
+      }
+      between(mt);
+    }
+  };
+
+  int slot = 0, set = 0;  // of the strip being multiplied
+  bool ready = false;     // the other set's slots are due
+  constexpr int D = NT * 4;
+  auto advance = [&]() {
+    slot += G;
+    ready = slot == kSlots;
+    if (ready) {
+      slot = 0;
+      set ^= 1;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        due[i] = zs[i];
+        zs[i] = 0.f;
+      }
+    }
+  };
+  // One strip: r0 receives strip s + 2, r1 holds s + 1, c the codes of s; n gets those of s + 1.
+  auto step = [&](int s, Raw& r0, Raw& r1, const Codes& c, Codes& n) {
+    const int buf = s & 1;
+    stage_x(buf ^ 1);
+    const int next2 = s + 2 < nwhole ? s + 2 : nwhole - 1;  // past the end: the last one again, not used
+    fetch_x(next2);
+    fetch_w(r0, next2);
+    if (ready) correct(lds + L::kSums + (set ^ 1) * L::kSumBytes);
+    sum_x(buf, set, slot);
+    advance();
+    begin(r1, n, slot, s + 1 < nwhole);
+    multiply(buf, c, [&](int mt) {
+#pragma unroll
+      for (int d = mt * D / MT; d < (mt + 1) * D / MT; ++d) decode(r1, n, d);
+    });
+    wait_lds();
+    block_barrier();
+  };
+  Raw r0, r1;
+  Codes c0, c1;
+  if (nwhole > 0) {
+    fetch_x(0);
+    fetch_w(r0, 0);
+    stage_x(0);
+    fetch_x(nwhole > 1 ? 1 : 0);
+    fetch_w(r1, nwhole > 1 ? 1 : 0);
+    begin(r0, c0, 0, true);
+#pragma unroll
+    for (int d = 0; d < D; ++d) decode(r0, c0, d);
+  }
+  wait_lds();
+  block_barrier();
+  for (int s = 0; s < nwhole; s += 2) {
+    step(s, r0, r1, c0, c1);
+    if (s + 1 < nwhole) step(s + 1, r1, r0, c1, c0);
+  }
+  if (K % kStrip != 0) {
+    if (ready) correct(lds + L::kSums + (set ^ 1) * L::kSumBytes);
+    const int buf = nwhole & 1;
+    fetch_tail(r0, nwhole);
+    stage_x(buf);  // every wave is done with the strips before it
+    begin(r0, c0, slot, true);
+#pragma unroll
+    for (int d = 0; d < D; ++d) decode(r0, c0, d);
+    wait_lds();
+    block_barrier();
+    sum_x(buf, set, slot);
+    advance();
+    multiply(buf, c0, [](int) {});
+    wait_lds();
+    block_barrier();
+  }
+  if (ready) {
+    correct(lds + L::kSums + (set ^ 1) * L::kSumBytes);
+  } else if (slot > 0) {  // unfilled slots have zs = 0 and finite sums
+#pragma unroll
+    for (int i = 0; i < NT; ++i) due[i] = zs[i];
+    correct(lds + L::kSums + set * L::kSumBytes);
+  }
+  to.write<16 * MT>([&](auto&& put) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) put(mt * 16, wave * 16 * NT + i * 16, acc[mt][i]);
+  });
+}
+
 template <int MT, int NT, int WM, int WN, int WK, int GS>
 __global__ __launch_bounds__(64 * WM * WN * WK) void int4_gemm_kernel(Int4Args a, const uint16_t* __restrict__ x,
                                                                  void* __restrict__ out, int out_bf16, int64_t M,
@@ -786,24 +1132,26 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void int4_gemm_kernel(Int4Args a
   const int64_t tile = int64_t(blockIdx.x % 8) * per + blockIdx.x / 8;
   if (int64_t(blockIdx.x / 8) >= per || tile >= total) return;  // uniform over the block
   const int64_t m0 = tile % mtiles * L::kBM, n0 = tile / mtiles * L::kBN;
-  int4_tile<MT, NT, WM, WN, WK, GS>(lds, a, x + m0 * K, M - m0, N, K, n0, [&](int m, int n, float v) {
+  auto put = [&](int m, int n, float v) {
     if (m0 + m < M && n0 + n < N) store_epi(out, m0 + m, n0 + n, N, v, alpha, out_bf16, epi);
-  });
+  };
+  if constexpr (WK == 1) {
+    const TileOut to{static_cast<char*>(out) + m0 * N * (out_bf16 ? 2 : 4), M - m0, N, n0, m0, alpha, out_bf16, &epi};
+    int4_pipe_tile<MT, NT, WN, GS>(lds, a, x + m0 * K, M - m0, N, K, n0, to);
+  }
+  else int4_tile<MT, NT, WM, WN, WK, GS>(lds, a, x + m0 * K, M - m0, N, K, n0, put);
 }
 
 // Grouped: group z owns rows a_offsets[z] .. a_offsets[z + 1] - 1 (clipped to
 // T) and multiplies them by expert expert_ids[z]; an id outside 0 .. E - 1
 // writes zeros, an empty group nothing.  Every block builds the prefix sum of
-// the groups' row tiles in LDS and walks its XCD's contiguous part of the
-// (group, row tile, column tile) list.
-template <int MT, int NT, int WM, int WN, int WK, int GS>
-__global__ __launch_bounds__(64 * WM * WN * WK) void int4_grouped_kernel(
-    Int4Args a, const uint16_t* __restrict__ x, const uint32_t* __restrict__ a_offsets,
-    const int32_t* __restrict__ expert_ids, void* __restrict__ out, int out_bf16, int64_t groups, int64_t T, int64_t N,
-    int64_t K, int64_t E) {
-  using L = Int4Tile<MT, NT, WM, WN, WK>;
-  extern __shared__ __attribute__((aligned(16))) char lds[];
-  int* cum = reinterpret_cast<int*>(lds + L::kLds);  // cum[z] = row tiles of groups 0 .. z - 1
+// the groups' row tiles in LDS (cum[z] = row tiles of groups 0 .. z - 1) and walks its XCD's
+// contiguous part of the (group, row tile, column tile) list.
+// f(expert's operands, m0, rows from m0 to the group's end, n0).
+template <int BM, int BN, int THREADS, typename F>
+__device__ __forceinline__ void walk_groups(int* cum, const Int4Args& a, const uint32_t* __restrict__ a_offsets,
+                                            const int32_t* __restrict__ expert_ids, void* __restrict__ out, int out_bf16,
+                                            int64_t groups, int64_t T, int64_t N, int64_t E, F&& f) {
   auto span = [&](int64_t z, int64_t& start, int64_t& rows) {
     int64_t b = a_offsets[z], e = a_offsets[z + 1];
     b = b < T ? b : T;
@@ -820,7 +1168,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void int4_grouped_kernel(
       if (z < groups) {
         int64_t start, rows;
         span(z, start, rows);
-        t = int((rows + L::kBM - 1) / L::kBM);
+        t = int((rows + BM - 1) / BM);
       }
       int incl = t;
 #pragma unroll
@@ -833,28 +1181,28 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void int4_grouped_kernel(
     }
   }
   __syncthreads();
-  const int64_t ntiles = (N + L::kBN - 1) / L::kBN, work = int64_t(cum[groups]) * ntiles;
+  const int64_t ntiles = (N + BN - 1) / BN, work = int64_t(__builtin_amdgcn_readfirstlane(cum[groups])) * ntiles;
   const int64_t xcd = blockIdx.x % 8, per_xcd = gridDim.x / 8;  // gridDim.x is a multiple of 8
   const int64_t first = xcd * work / 8, last = (xcd + 1) * work / 8;
   for (int64_t i = first + blockIdx.x / 8; i < last; i += per_xcd) {
     const int mt = int(i / ntiles);
-    const int64_t n0 = i % ntiles * L::kBN;
+    const int64_t n0 = i % ntiles * BN;
     int64_t lo = 0, hi = groups;  // cum[lo] <= mt < cum[hi]
     while (hi - lo > 1) {
       const int64_t mid = (lo + hi) / 2;
       if (cum[mid] <= mt) lo = mid;
       else hi = mid;
     }
+    // What was read from LDS is uniform, which the tile's scalar bases rest on.
+    lo = __builtin_amdgcn_readfirstlane(int(lo));
+    const int before = __builtin_amdgcn_readfirstlane(cum[lo]);
     int64_t start, rows;
     span(lo, start, rows);
-    const int64_t m0 = start + int64_t(mt - cum[lo]) * L::kBM, end = start + rows;
+    const int64_t m0 = start + int64_t(mt - before) * BM, left = start + rows - m0;
     const int64_t e = expert_ids[lo];
-    auto put = [&](int m, int n, float v) {
-      if (m0 + m >= end || n0 + n >= N) return;
-      store_out(out, (m0 + m) * N + n0 + n, v, 1.f, out_bf16);
-    };
     if (e < 0 || e >= E) {
-      for (int idx = threadIdx.x; idx < L::kBM * L::kBN; idx += L::kThreads) put(idx / L::kBN, idx % L::kBN, 0.f);
+      for (int idx = threadIdx.x; idx < BM * BN; idx += THREADS)
+        if (idx / BN < left && n0 + idx % BN < N) store_out(out, (m0 + idx / BN) * N + n0 + idx % BN, 0.f, 1.f, out_bf16);
       continue;
     }
     Int4Args b = a;
@@ -862,8 +1210,43 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void int4_grouped_kernel(
     b.scale += e * N * a.groups;
     if (b.zero) b.zero += e * N * a.groups;
     __syncthreads();  // the previous tile's buffers are free
-    int4_tile<MT, NT, WM, WN, WK, GS>(lds, b, x + m0 * K, end - m0, N, K, n0, put);
+    f(b, m0, left, n0);
   }
+}
+
+template <int MT, int NT, int WN, int GS>
+__global__ __launch_bounds__(64 * WN) void int4_grouped_kernel(Int4Args a, const uint16_t* __restrict__ x,
+                                                               const uint32_t* __restrict__ a_offsets,
+                                                               const int32_t* __restrict__ expert_ids,
+                                                               void* __restrict__ out, int out_bf16, int64_t groups,
+                                                               int64_t T, int64_t N, int64_t K, int64_t E) {
+  using L = Int4Tile<MT, NT, 1, WN, 1>;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  walk_groups<L::kBM, L::kBN, L::kThreads>(
+      reinterpret_cast<int*>(lds + L::kLds), a, a_offsets, expert_ids, out, out_bf16, groups, T, N, E,
+      [&](const Int4Args& b, int64_t m0, int64_t left, int64_t n0) {
+        const TileOut to{static_cast<char*>(out) + m0 * N * (out_bf16 ? 2 : 4), left, N, n0, m0, 1.f, out_bf16, nullptr};
+        int4_pipe_tile<MT, NT, WN, GS>(lds, b, x + m0 * K, left, N, K, n0, to);
+      });
+}
+
+// Groups of few rows: tiles of 4 rows through the streaming form.
+template <int NT, int WN, int SH>
+__global__ __launch_bounds__(64 * WN, 4) void int4_grouped_stream_kernel(Int4Args a, const uint16_t* __restrict__ x,
+                                                                         const uint32_t* __restrict__ a_offsets,
+                                                                         const int32_t* __restrict__ expert_ids,
+                                                                         void* __restrict__ out, int out_bf16,
+                                                                         int64_t groups, int64_t T, int64_t N, int64_t K,
+                                                                         int64_t E) {
+  using L = StreamLayout<4, NT, WN, 1>;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  walk_groups<4, 16 * NT * WN, 64 * WN>(
+      reinterpret_cast<int*>(lds + L::kLds), a, a_offsets, expert_ids, out, out_bf16, groups, T, N, E,
+      [&](const Int4Args& b, int64_t m0, int64_t left, int64_t n0) {
+        int4_stream_tile<4, NT, WN, 1, SH>(lds, b, x + m0 * K, int(left < 4 ? left : 4), N, K, n0, [&](int m, int n, float v) {
+          if (n0 + n < N) store_out(out, (m0 + m) * N + n0 + n, v, 1.f, out_bf16);
+        });
+      });
 }
 
 // ---------------------------------------------------------------- launch
@@ -932,23 +1315,53 @@ hipError_t gemm_cfg(const Int4Args& a, const uint16_t* x, void* out, int bf16, i
   });
 }
 
-template <int MT, int NT, int WM, int WN, int WK>
-hipError_t grouped_cfg(const Int4Args& a, const uint16_t* x, const uint32_t* offsets, const int32_t* ids, void* out,
-                       int bf16, int64_t G, int64_t E, int64_t T, int64_t N, int64_t K, int num_cus, hipStream_t s) {
-  using L = Int4Tile<MT, NT, WM, WN, WK>;
-  const int lds = int(L::kLds + 4 * (G + 1));
-  constexpr int kMaxLds = 160 * 1024;
-  if (lds > kMaxLds) return hipErrorInvalidValue;
-  // At most ceil(T / BM) + min(G, T) row tiles exist.
-  const int64_t upper = ((T + L::kBM - 1) / L::kBM + std::min(G, T)) * ((N + L::kBN - 1) / L::kBN);
-  const int64_t per_cu = std::max<int64_t>(1, std::min<int64_t>(kMaxLds / lds, 16 / (WM * WN * WK)));
-  const int64_t blocks = (std::min(upper, per_cu * num_cus) + 7) / 8 * 8;
-  return by_group(a, [&](auto gs) -> hipError_t {
-    auto kernel = int4_grouped_kernel<MT, NT, WM, WN, WK, decltype(gs)::value>;
-    static std::atomic<uint64_t> lds_set{0};
+constexpr int kMaxLds = 160 * 1024;
+
+// Blocks for a walk of tiles BM x BN: as many as fit, if there are so many tiles (at
+// most ceil(T / BM) + min(G, T) row tiles exist), a multiple of 8.
+int64_t walk_blocks(int64_t BM, int64_t BN, int waves, int lds, int64_t G, int64_t T, int64_t N, int num_cus) {
+  const int64_t upper = ((T + BM - 1) / BM + std::min(G, T)) * ((N + BN - 1) / BN);
+  const int64_t per_cu = std::max<int64_t>(1, std::min<int64_t>(kMaxLds / lds, 16 / waves));
+  return (std::min(upper, per_cu * num_cus) + 7) / 8 * 8;
+}
+
+struct GroupedCall {
+  const Int4Args& a;
+  const uint16_t* x;
+  const uint32_t* offsets;
+  const int32_t* ids;
+  void* out;
+  int bf16;
+  int64_t G, E, T, N, K;
+  int num_cus;
+  hipStream_t s;
+
+  template <typename Kernel> hipError_t go(Kernel kernel, std::atomic<uint64_t>& lds_set, int lds, int64_t BM, int64_t BN,
+                                           int waves) const {
+    if (lds > kMaxLds) return hipErrorInvalidValue;
     if (hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(kernel), kMaxLds, lds_set)) return e;
-    return launch(kernel, dim3(unsigned(blocks)), dim3(L::kThreads), lds, s, a, x, offsets, ids, out, bf16, G, T, N, K,
-                  E);
+    const int64_t blocks = walk_blocks(BM, BN, waves, lds, G, T, N, num_cus);
+    return launch(kernel, dim3(unsigned(blocks)), dim3(64 * waves), lds, s, a, x, offsets, ids, out, bf16, G, T, N, K, E);
+  }
+};
+
+template <int MT, int NT, int WN>
+hipError_t grouped_cfg(const GroupedCall& c) {
+  using L = Int4Tile<MT, NT, 1, WN, 1>;
+  return by_group(c.a, [&](auto gs) -> hipError_t {
+    static std::atomic<uint64_t> lds_set{0};
+    return c.go(int4_grouped_kernel<MT, NT, WN, decltype(gs)::value>, lds_set, int(L::kLds + 4 * (c.G + 1)), L::kBM, L::kBN,
+                WN);
+  });
+}
+
+template <int NT, int WN>
+hipError_t grouped_stream(const GroupedCall& c) {
+  constexpr int kLds = StreamLayout<4, NT, WN, 1>::kLds;
+  return by_shift(c.a, [&](auto sh) -> hipError_t {
+    static std::atomic<uint64_t> lds_set{0};
+    return c.go(int4_grouped_stream_kernel<NT, WN, decltype(sh)::value>, lds_set, int(kLds + 4 * (c.G + 1)), 4, 16 * NT * WN,
+                WN);
   });
 }
 
@@ -961,12 +1374,26 @@ hipError_t launch_int4_gemm(const uint8_t* w, const uint16_t* scale, const uint8
   if (M == 1) return stream_rows<1>(a, x, out, out_bf16, M, N, K, alpha, num_cus, epi, s);
   if (M == 2) return stream_rows<2>(a, x, out, out_bf16, M, N, K, alpha, num_cus, epi, s);
   if (M <= 4) return stream_rows<4>(a, x, out, out_bf16, M, N, K, alpha, num_cus, epi, s);
-  if (M <= 16) return stream_rows<16>(a, x, out, out_bf16, M, N, K, alpha, num_cus, epi, s);
-  if (M <= 64) return gemm_cfg<2, 2, 1, 1, 4>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
-  // 128x256 tiles where they give more than half of the CUs one (M = 500, N = 14336,
-  // K = 4096: 95 against 144 us), else 64x128 (M = 500, N = K = 4096: 54 against 90).
-  if (((M + 127) / 128) * ((N + 255) / 256) * 2 > num_cus)
-    return gemm_cfg<8, 2, 1, 8, 1>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
+  // Small tiles whose waves split K, while a CU gets at most 4 of 32x32: M = 100, N = K =
+  // 4096: 22 us, 64x128 44; M = 64, N = 14336, K = 4096: 40 and 51; M = 100 there (7 of them per
+  // CU): 63 and 47.  Half their width or height where one would leave CUs without any:
+  // M = 16, N = K = 4096: 16x16 7.9 us, 16x32 10.3; N = 14336: 21.1 and 18.7.
+  auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  const bool narrow = N <= int64_t(num_cus) * 32;
+  if (M <= 16) {
+    if (narrow) return gemm_cfg<1, 1, 1, 1, 4>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
+    return gemm_cfg<1, 2, 1, 1, 4>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
+  }
+  if (tiles(32, 32) <= 4 * int64_t(num_cus)) {
+    if (M <= 32 && narrow) return gemm_cfg<2, 1, 1, 1, 4>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
+    return gemm_cfg<2, 2, 1, 1, 4>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
+  }
+  // Tiles of 256 columns as high as M (M = 64, N = 60000, K = 2048: 64x256 36 us, 32x32 71),
+  // of 128 rows where they give more than half of the CUs one (M = 500, N = 14336, K = 4096:
+  // 90 us, 64x128 144), else 64x128 (M = 500, N = K = 4096: 47 against 90).
+  if (M <= 32) return gemm_cfg<2, 2, 1, 8, 1>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
+  if (M <= 64) return gemm_cfg<4, 2, 1, 8, 1>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
+  if (tiles(128, 256) * 2 > num_cus) return gemm_cfg<8, 2, 1, 8, 1>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
   return gemm_cfg<4, 2, 1, 4, 1>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
 }
 
@@ -979,11 +1406,16 @@ hipError_t launch_int4_grouped(const uint8_t* w, const uint16_t* scale, const ui
   // of 128): 16x128 to 4 rows (64 rows: 40 us, 32x128 44), 32x128 to 16 (256 rows: 46,
   // 16x128 50, 64x256 70), 64x256 to 256 (4096 rows: 108, 32x128 113), 128x256 above
   // (8 experts, N = K = 4096, 4096 rows: 301 against 357).
-  auto go = [&](auto cfg) { return cfg(a, x, a_offsets, expert_ids, out, out_bf16, G, E, T, N, K, num_cus, s); };
-  if (T <= 4 * G) return go(grouped_cfg<1, 2, 1, 4, 1>);
-  if (T <= 16 * G) return go(grouped_cfg<2, 2, 1, 4, 1>);
-  if (T <= 256 * G) return go(grouped_cfg<4, 2, 1, 8, 1>);
-  return go(grouped_cfg<8, 2, 1, 8, 1>);
+  // By the rows a group has on average (64 experts, N = 1536, K = 2048, groups of
+  // 128, unless said): to 4 the streaming form (64 rows: 37 us, 32x256 56; 256 rows: 46 and 56),
+  // to 32 tiles of 32x256 (1024 rows: 57, 64x256 68), to 256 of 64x256 (4096 rows: 101, 32x256
+  // 109; 8 experts, N = K = 4096, 512 rows: 86, 128x256 131), above of 128x256 (those
+  // with 4096 rows: 363, 64x256 385).
+  const GroupedCall c{a, x, a_offsets, expert_ids, out, out_bf16, G, E, T, N, K, num_cus, s};
+  if (T <= 4 * G) return grouped_stream<1, 4>(c);
+  if (T <= 32 * G) return grouped_cfg<2, 2, 8>(c);
+  if (T <= 256 * G) return grouped_cfg<4, 2, 8>(c);
+  return grouped_cfg<8, 2, 8>(c);
 }
 
 }  // namespace qlinear
