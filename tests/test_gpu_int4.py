@@ -202,6 +202,88 @@ def test_weight_beyond_4_gib(q, m):
     assert not out[:, :-3].any()
 
 
+def plain64(packed, scale, zero, x, group):
+    """x @ D^T by the definition in float64 torch on the device: for sizes the numpy oracle is slow at."""
+    k = x.shape[1]
+    codes = torch.stack([packed & 15, packed >> 4], -1).reshape(packed.shape[0], -1)[:, :k].double()
+    g = torch.arange(k, device=DEV) // group
+    z = 8.0 if zero is None else zero.double()[:, g]
+    return x.double() @ ((codes - z) * scale.double()[:, g]).t().contiguous()
+
+
+def random_operands(seed, m, n, k, group, zeros, exact):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    groups = -(-k // group)
+    w = torch.randint(0, 256, (n, (k + 1) // 2), generator=g, device=DEV, dtype=torch.uint8)
+    z = torch.randint(0, 16, (n, groups), generator=g, device=DEV, dtype=torch.uint8) if zeros else None
+    if exact:
+        s = torch.exp2(torch.randint(-3, 1, (n, groups), generator=g, device=DEV).float()).bfloat16()
+        x = torch.randint(-4, 5, (m, k), generator=g, device=DEV).bfloat16()
+    else:
+        s = (torch.rand((n, groups), generator=g, device=DEV) * 0.01 + 0.005).bfloat16()
+        x = torch.randn((m, k), generator=g, device=DEV).bfloat16()
+    return w, s, z, x
+
+
+# wide enough for the tiles of 256 columns and 32, 64 and 128 rows, and for 64x128; K of one strip, of a few and of many,
+# whole and partial, so that every phase of the pipeline and every number of filled correction slots comes up
+@pytest.mark.parametrize("m,n", [(20, 33000), (40, 20000), (100, 33000), (100, 20001)])
+@pytest.mark.parametrize("k,group", [(96, 32), (128, 128), (129, 64), (256, 32), (385, 128), (640, 64), (1000, 32), (1152, 128),
+                                     (2050, 256), (1023, 64), (700, 700)])
+def test_exact_big_tiles(q, m, n, k, group):
+    for zeros, dt in ((True, torch.float32), (False, torch.bfloat16)):
+        show("int4 big tiles", m, n, k, group, zeros)
+        w, s, z, x = random_operands(m * n + k, m, n, k, group, zeros, True)
+        out = q.int4_gemm(w, s, x, w_zero=z, group_size=group, out_dtype=dt)
+        assert torch.equal(out, plain64(w, s, z, x, group).to(dt))
+
+
+@pytest.mark.parametrize("m,n,k,group", [(24, 33000, 1536, 128), (300, 20000, 1500, 64), (128, 33100, 640, 32)])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_random_big_tiles(q, m, n, k, group, dt):
+    w, s, z, x = random_operands(m + n, m, n, k, group, True, False)
+    show("int4 random big tiles", m, n, k, group, dt)
+    out = q.int4_gemm(w, s, x, w_zero=z, group_size=group, out_dtype=dt).double()
+    ref = plain64(w, s, z, x, group)
+    size = plain64(w, s, torch.zeros_like(z), x.abs(), group) + plain64(torch.zeros_like(w), s, z, x.abs(), group).abs()
+    tau = (k + 8) * U * size
+    assert bool(((out - ref).abs() <= tau + HALF[dt] * (ref.abs() + tau)).all())
+
+
+@pytest.mark.parametrize("m,n", [(20, 33000), (40, 20000), (100, 33000), (70, 20001)])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_big_tiles_write_inside_out_and_take_the_epilogue(q, m, n, dt):
+    k = 256
+    w, s, z, x = random_operands(n, m, n, k, 64, True, True)
+    ref = plain64(w, s, z, x, 64)
+    buf = torch.full((m * n + 4096,), 7.0, dtype=dt, device=DEV)
+    show("int4 big tiles bounds", m, n, dt)
+    q.int4_gemm(w, s, x, w_zero=z, group_size=64, out=buf[2048:2048 + m * n].view(m, n), out_dtype=dt)
+    assert torch.equal(buf[2048:2048 + m * n].view(m, n), ref.to(dt))
+    assert torch.all(buf[:2048] == 7.0) and torch.all(buf[2048 + m * n:] == 7.0)
+    bias = torch.randint(-8, 9, (n,), device=DEV).bfloat16()
+    res = torch.randint(-8, 9, (m, n), device=DEV).float()
+    out = q.int4_gemm(w, s, x, w_zero=z, group_size=64, out_dtype=dt, alpha=0.5, bias=bias, residual=res, activation="relu")
+    assert torch.equal(out, (torch.relu(0.5 * ref + bias.double()) + res.double()).to(dt))
+
+
+def test_big_tile_keeps_nonfinite_values_in_their_place(q):
+    """A NaN scale stays in its column; infinities and NaN of x in their rows, also where the row's group follows others."""
+    m, n, k = 100, 33000, 512
+    w, s, z, x = random_operands(5, m, n, k, 64, True, True)
+    ref = plain64(w, s, z, x, 64).float()
+    s[777, 3] = float("nan")
+    x[5, 70], x[63, 200], x[99, 511] = float("inf"), float("nan"), float("-inf")
+    show("int4 big tiles non-finite")
+    out = q.int4_gemm(w, s, x, w_zero=z, group_size=64, out_dtype=torch.float32)
+    rows = torch.ones(m, dtype=torch.bool, device=DEV)
+    rows[[5, 63, 99]] = False
+    cols = torch.ones(n, dtype=torch.bool, device=DEV)
+    cols[777] = False
+    assert torch.equal(out[rows][:, cols], ref[rows][:, cols])
+    assert torch.isnan(out[:, 777]).all() and not torch.isfinite(out[~rows]).any()
+
+
 def test_no_rows(q):
     w, s = torch.zeros((8, 32), dtype=torch.uint8, device=DEV), torch.ones((8, 2), dtype=torch.bfloat16, device=DEV)
     x = torch.empty((0, 64), dtype=torch.bfloat16, device=DEV)
@@ -266,6 +348,47 @@ def test_grouped_many_groups(q, groups, t):
     show("int4 grouped many", groups, t)
     out = q.int4_grouped_gemm(w, s, xd, dev(offs.astype(np.int32)), dev(ids), w_zero=z, group_size=32, out_dtype=torch.float32)
     assert written.all() and same(out, ref)
+
+
+# one to four rows a group, about 16, about 64, over 256: each form of the walk; K long, odd and short
+@pytest.mark.parametrize("rows", [1, 3, 16, 70, 300])
+@pytest.mark.parametrize("k,group", [(1100, 32), (1024, 64), (897, 128), (2000, 512), (33, 32)])
+def test_grouped_forms(q, rows, k, group):
+    e, n, groups = 5, 272, 7
+    rng = np.random.default_rng([23, rows, k])
+    counts = rng.integers(0, 2 * rows + 1, groups)
+    counts[0], counts[3] = rows, 0
+    offs = torch.from_numpy(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)).to(DEV)
+    ids = torch.tensor([4, 0, -1, 2, 1, 3, 4], dtype=torch.int32, device=DEV)
+    t = int(counts.sum())
+    w, s, z, x = random_operands(rows + k, t, e * n, k, group, True, True)
+    w, s, z = w.view(e, n, -1), s.view(e, n, -1), z.view(e, n, -1)
+    for dt in (torch.float32, torch.bfloat16):
+        show("int4 grouped forms", rows, k, group, dt)
+        out = torch.full((t + 2, n), 3.0, dtype=dt, device=DEV)
+        q.int4_grouped_gemm(w, s, x, offs, ids, w_zero=z, group_size=group, out=out[:t], out_dtype=dt)
+        assert torch.all(out[t:] == 3.0)
+        for i, (b, c) in enumerate(zip(offs[:-1].tolist(), offs[1:].tolist())):
+            x_i, e_i = x[b:c], int(ids[i])
+            want = plain64(w[e_i], s[e_i], z[e_i], x_i, group) if e_i >= 0 else torch.zeros((c - b, n), device=DEV)
+            assert torch.equal(out[b:c], want.to(dt))
+
+
+def test_grouped_more_groups_than_a_block_counts(q):
+    """Most of 40000 groups are empty; the rows' groups lie before and behind each launch's last group."""
+    groups, e, n, k = 40000, 3, 48, 64
+    at = [0, 1, 16383, 16384, 20000, 32767, 32768, 39999]
+    counts = torch.zeros(groups, dtype=torch.int64)
+    counts[at] = torch.tensor([2, 1, 5, 1, 3, 4, 1, 2])
+    offs = torch.cat([torch.zeros(1, dtype=torch.int64), counts.cumsum(0)])
+    ids = torch.arange(groups) % e
+    w, s, z, x = random_operands(9, int(counts.sum()), e * n, k, 32, True, True)
+    w, s, z = w.view(e, n, -1), s.view(e, n, -1), z.view(e, n, -1)
+    show("int4 grouped 40000")
+    out = q.int4_grouped_gemm(w, s, x, offs.int().to(DEV), ids.int().to(DEV), w_zero=z, group_size=32, out_dtype=torch.float32)
+    for i in at:
+        b, c = int(offs[i]), int(offs[i + 1])
+        assert torch.equal(out[b:c], plain64(w[i % e], s[i % e], z[i % e], x[b:c], 32).float())
 
 
 def test_other_stream_and_same_bits_again(q):

@@ -242,7 +242,54 @@ def test_rows_beyond_4_gib(q):
     assert torch.equal(back, (x.float() * top_k).bfloat16())
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_calls_larger_than_the_caches(q, dtype):
+    """The forms that stream past the caches, against float64 on the device."""
+    t, top_k, h = 2700, 6, 4100
+    g = torch.Generator(device=DEV).manual_seed(11)
+    ids = torch.randint(-1, 40, (t, top_k), generator=g, device=DEV, dtype=torch.int32)
+    sr = q.moe_sort(ids, 40)[2]
+    x = torch.randn((t, h), generator=g, device=DEV).to(dtype)
+    rows = torch.randn((t * top_k, h), generator=g, device=DEV).to(dtype)
+    w = torch.rand((t, top_k), generator=g, device=DEV)
+    on, place = sr >= 0, torch.where(sr < 0, ~sr, sr).long()
+    show("moe large", dtype)
+    xs = q.moe_gather(x, sr)
+    want = torch.zeros_like(rows)
+    want[place[on]] = x.repeat_interleave(top_k, 0).view(t, top_k, h)[on]
+    assert torch.equal(xs, want)
+    part = rows.double()[place] * torch.where(on, w, 0.0).double()[:, :, None]
+    tau = (top_k + 1) * U * part.abs().sum(1)
+    ref = part.sum(1)
+    assert bool(((q.moe_combine(rows, sr, w).double() - ref).abs() <= tau + HALF[dtype] * (ref.abs() + tau)).all())
+    gr, gw = q.moe_combine_backward(x, rows, sr, w)
+    ref = torch.zeros_like(rows, dtype=torch.float64)
+    ref[place[on]] = (x.double()[:, None, :] * w.double()[:, :, None])[on]
+    assert bool(((gr.double() - ref).abs() <= U * ref.abs() + HALF[dtype] * ref.abs() * (1 + U)).all())
+    prod = x.double()[:, None, :] * rows.double()[place] * on[:, :, None]
+    assert bool(((gw.double() - prod.sum(2)).abs() <= (h + 1) * U * prod.abs().sum(2)).all())
+
+
 # ---------------------------------------------------------------- gated activation
+
+
+def test_swiglu_larger_than_the_caches(q):
+    m, f = 20000, 1537
+    g = torch.Generator(device=DEV).manual_seed(12)
+    x = (torch.randn((m, 2 * f), generator=g, device=DEV) * 3).bfloat16()
+    dy = torch.randn((m, f), generator=g, device=DEV).bfloat16()
+    show("swiglu large")
+    gate, up = x.double().split(f, 1)
+    sig, rest = torch.sigmoid(gate), torch.sigmoid(-gate)
+    ref = gate * sig * up
+    tau = 16 * U * ref.abs()
+    assert bool(((q.swiglu(x).double() - ref).abs() <= tau + HALF[torch.bfloat16] * (ref.abs() + tau)).all())
+    out = q.swiglu_backward(dy, x).double()
+    first = dy.double() * up * sig
+    for got, ref, size in ((out[:, :f], first * (1 + gate * rest), first.abs() * (1 + gate.abs() * rest)),
+                           (out[:, f:], dy.double() * gate * sig, (dy.double() * gate * sig).abs())):
+        tau = 16 * U * size
+        assert bool(((got - ref).abs() <= tau + HALF[torch.bfloat16] * (ref.abs() + tau)).all())
 
 
 @pytest.mark.parametrize("dtype", DTYPES)

@@ -1411,11 +1411,18 @@ hipError_t launch_int4_grouped(const uint8_t* w, const uint16_t* scale, const ui
   // to 32 tiles of 32x256 (1024 rows: 57, 64x256 68), to 256 of 64x256 (4096 rows: 101, 32x256
   // 109; 8 experts, N = K = 4096, 512 rows: 86, 128x256 131), above of 128x256 (those
   // with 4096 rows: 363, 64x256 385).
-  const GroupedCall c{a, x, a_offsets, expert_ids, out, out_bf16, G, E, T, N, K, num_cus, s};
-  if (T <= 4 * G) return grouped_stream<1, 4>(c);
-  if (T <= 32 * G) return grouped_cfg<2, 2, 8>(c);
-  if (T <= 256 * G) return grouped_cfg<4, 2, 8>(c);
-  return grouped_cfg<8, 2, 8>(c);
+  // A block keeps the groups' prefix sums in LDS beside its tile: more groups take more launches.
+  constexpr int64_t kMost = 16384;
+  for (int64_t z = 0; z < G; z += kMost) {
+    const int64_t groups = std::min(kMost, G - z);
+    const GroupedCall c{a, x, a_offsets + z, expert_ids + z, out, out_bf16, groups, E, T, N, K, num_cus, s};
+    const hipError_t e = T <= 4 * G     ? grouped_stream<1, 4>(c)
+                         : T <= 32 * G  ? grouped_cfg<2, 2, 8>(c)
+                         : T <= 256 * G ? grouped_cfg<4, 2, 8>(c)
+                                        : grouped_cfg<8, 2, 8>(c);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace qlinear
