@@ -225,9 +225,9 @@ def random_operands(seed, m, n, k, group, zeros, exact):
     return w, s, z, x
 
 
-# wide enough for the tiles of 256 columns and 32, 64 and 128 rows, and for 64x128; K of one strip, of a few and of many,
+# sizes for the tiles of 32x32, 64x128, 128x256, 128x128, 32x128 and 64x256; K of one strip, of a few and of many,
 # whole and partial, so that every phase of the pipeline and every number of filled correction slots comes up
-@pytest.mark.parametrize("m,n", [(20, 33000), (40, 20000), (100, 33000), (100, 20001)])
+@pytest.mark.parametrize("m,n", [(20, 33000), (40, 20000), (100, 33000), (100, 20001), (250, 4096), (40, 40000)])
 @pytest.mark.parametrize("k,group", [(96, 32), (128, 128), (129, 64), (256, 32), (385, 128), (640, 64), (1000, 32), (1152, 128),
                                      (2050, 256), (1023, 64), (700, 700)])
 def test_exact_big_tiles(q, m, n, k, group):

@@ -432,9 +432,9 @@ __global__ __launch_bounds__(64 * WN * WK) void int4_stream_kernel(Int4Args a, c
 
 // ---------------------------------------------------------------- matrix-core tile
 
-// A block computes BM = 16 MT WM rows by BN = 16 NT WN columns with 16x16x32
-// MFMA.  WM x WN waves share each 128-value strip of x, or WK waves split the
-// strips between them and add their tiles at the end.
+// A block computes BM = 16 MT rows by BN = 16 NT WN columns with 16x16x32
+// MFMA.  WN waves side by side share each 128-value strip of x (int4_pipe_tile), or WK
+// waves split the strips between them and add their tiles at the end (int4_tile).
 //
 // Weights go straight into the registers of the wave that multiplies them: lane
 // (n = l % 16, quarter h = l / 16) reads the 16 bytes k = 32 h .. 32 h + 31 of its
@@ -456,19 +456,19 @@ __global__ __launch_bounds__(64 * WN * WK) void int4_stream_kernel(Int4Args a, c
 // vector ALU, which the decoding and the scaling fill already, they would be 16.
 constexpr int kSlots = 4;  // groups per correction
 
-template <int MT, int NT, int WM, int WN, int WK> struct Int4Tile {
-  static constexpr int kBM = 16 * MT * WM, kBN = 16 * NT * WN, kThreads = 64 * WM * WN * WK;
-  static constexpr int kStagers = WK > 1 ? 64 : kThreads;  // threads that fill one activation buffer
+template <int MT, int NT, int WN, int WK> struct Int4Tile {
+  static constexpr int kBM = 16 * MT, kBN = 16 * NT * WN, kThreads = 64 * WN * WK;
+  static constexpr int kStagers = 64 * WN;                 // threads that fill one activation buffer
   static constexpr int kChunks = kBM * 16 / kStagers;      // 16-byte chunks per staging thread
   static constexpr int kXBytes = kBM * kStrip * 2;
-  static constexpr int kBufs = WK > 1 ? 1 : 2;             // private buffers need no second one
+  static constexpr int kBufs = WK > 1 ? 1 : 2;             // a wave's own buffer needs no second one
   static constexpr int kSumBytes = kSlots * kBM * 16;      // [slot][BM] pieces of the sums
   static constexpr int kSums = kXBytes * kBufs;
   static constexpr int kOne = kSums + 2 * kSumBytes;
   static constexpr int kRing = kOne * WK;
   static constexpr int kReduce = WK > 1 ? WK * 64 * MT * NT * 16 : 0;
   static constexpr int kLds = kRing > kReduce ? kRing : kReduce;
-  static_assert(WK == 1 || WM * WN == 1, "either the tile or K is split over the waves");
+  static_assert(WK == 1 || WN == 1, "either the tile or K is split over the waves");
 };
 
 __device__ __forceinline__ float cut_bf16(float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); }
@@ -493,18 +493,17 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p) {
 }
 
 // GS: MFMA steps per group inside a strip (1, 2, 4; 4 also for larger groups).
+// The waves share nothing until they add their tiles, so that none waits for another: this is
+// the form for few rows, where a tile's time is the memory's answer.
 // store(m, n, value): m relative to the tile's first row.  Every thread of the
 // block calls it; the block's LDS is free when it begins.
-template <int MT, int NT, int WM, int WN, int WK, int GS, typename Store>
+template <int MT, int NT, int WK, int GS, typename Store>
 __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const uint16_t* __restrict__ x, int64_t rows,
                                           int64_t N, int64_t K, int64_t n0, Store&& store) {
-  using L = Int4Tile<MT, NT, WM, WN, WK>;
+  using L = Int4Tile<MT, NT, 1, WK>;
   constexpr int G = 4 / GS;  // groups per strip
-  constexpr int kTiles = MT * WM, kSummers = WM * WN;
-  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int lane = threadIdx.x & (kWave - 1), wk = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int ln = lane & 15, quarter = lane >> 4;
-  const int wn = WK > 1 ? 0 : wave % WN, wm = WK > 1 ? 0 : wave / WN, wk = WK > 1 ? wave : 0;
-  const int stager = WK > 1 ? lane : threadIdx.x;
   const int nstrips = int((K + kStrip - 1) / kStrip), nwhole = int(K / kStrip);
   char* const mem = lds + wk * L::kOne;
 
@@ -517,15 +516,15 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
   uint32_t woff[NT], soff[NT], xoff[L::kChunks];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    const int n = wn * 16 * NT + i * 16 + ln;
+    const int n = i * 16 + ln;
     const uint32_t row = n0 + n < N ? n : uint32_t(N - 1 - n0);  // columns past N re-read the last row, never stored
     woff[i] = row * uint32_t(a.row_bytes) + quarter * 16;
     soff[i] = row * uint32_t(a.groups);
   }
 #pragma unroll
   for (int j = 0; j < L::kChunks; ++j) {
-    const int m = (stager + j * L::kStagers) >> 4;
-    xoff[j] = uint32_t(m < rows ? m : rows - 1) * uint32_t(K) * 2 + (stager & 15) * 16;  // rows past the end likewise
+    const int m = (lane + j * kWave) >> 4;
+    xoff[j] = uint32_t(m < rows ? m : rows - 1) * uint32_t(K) * 2 + (lane & 15) * 16;  // rows past the end likewise
   }
 
   // A strip's G groups of a row are neighbours: their scales come in one load
@@ -578,7 +577,7 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
     }
 #pragma unroll
     for (int j = 0; j < L::kChunks; ++j) {
-      const int values = left - (stager & 15) * 8;
+      const int values = left - (lane & 15) * 8;
       const uint16_t* p = x + k + (xoff[j] >> 1);
       xreg[j] = values >= 8 ? ldx16(p) : ld_halves(p, values);
     }
@@ -592,9 +591,8 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
   float zs[NT], due[NT];  // zero * scale of this quarter's slot: being filled, and of full slots
 #pragma unroll
   for (int i = 0; i < NT; ++i) zs[i] = due[i] = 0.f;
-  for (int i = stager; i < 2 * L::kSumBytes / 16; i += L::kStagers)
+  for (int i = lane; i < 2 * L::kSumBytes / 16; i += kWave)
     *reinterpret_cast<u32x4*>(mem + L::kSums + i * 16) = u32x4{0u, 0u, 0u, 0u};
-  if constexpr (WK == 1) __syncthreads();  // a slot's first writer need not be its clearer
 
   auto correct = [&](const char* sums) {
     v8bf zb[NT];
@@ -602,7 +600,7 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
     for (int i = 0; i < NT; ++i) zb[i] = __builtin_bit_cast(v8bf, factor_pieces(due[i]));
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const v8bf xb = *reinterpret_cast<const v8bf*>(sums + (quarter * L::kBM + (wm * MT + mt) * 16 + ln) * 16);
+      const v8bf xb = *reinterpret_cast<const v8bf*>(sums + (quarter * L::kBM + mt * 16 + ln) * 16);
 #pragma unroll
       for (int i = 0; i < NT; ++i) acc[mt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb, zb[i], acc[mt][i], 0, 0, 0);
     }
@@ -612,9 +610,9 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
   // 4 q + t (groups of 128 and more) the two halves of the chunk's number change places.
   auto place = [&](int row, int t) { return row * (kStrip * 2) + (((t * 4 + quarter) ^ ln) << 4); };
 
-  // buf: the strip's buffer; slot, sbuf: its first group's slot and the slots' buffer.  Sums are
-  // made while their strip is multiplied, so full slots are due one barrier later.
-  int buf = 0, slot = 0, sbuf = 0;
+  // slot, sbuf: the strip's first group's slot and the slots' buffer.  Sums are made while
+  // their strip is multiplied, and full slots are due in the next.
+  int slot = 0, sbuf = 0;
   bool full = false;
   if (wk < nwhole) fetch(wk);
   for (int strip = wk; strip < nstrips; strip += WK) {
@@ -628,10 +626,10 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
       else asm volatile("" : "+v"(sreg[i][0]), "+v"(zreg[i]));
       if constexpr (G == 4) asm volatile("" : "+v"(sreg[i][1]));
     }
-    char* xs = mem + buf * L::kXBytes;
+    char* const xs = mem;
 #pragma unroll
     for (int j = 0; j < L::kChunks; ++j) {
-      const int idx = stager + j * L::kStagers, m = idx >> 4, c = idx & 15;
+      const int idx = lane + j * kWave, m = idx >> 4, c = idx & 15;
       const int p = GS == 4 ? (c & 3) * 4 + (c >> 2) : c;
       *reinterpret_cast<u32x4*>(xs + m * (kStrip * 2) + ((p ^ (m & 15)) << 4)) = xreg[j];
     }
@@ -657,14 +655,11 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
     decode(0);
     if (strip + WK < nwhole) fetch(strip + WK);
     wait_lds();
-    if constexpr (WK == 1) block_barrier();
-    // The sums of x over the strip's groups, row tiles dealt to the waves.
+    // The sums of x over the strip's groups.
     char* sums = mem + L::kSums + sbuf * L::kSumBytes;
     const v8bf ones = __builtin_bit_cast(v8bf, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
 #pragma unroll
-    for (int q = 0; q < (kTiles + kSummers - 1) / kSummers; ++q) {
-      const int tile = (WK > 1 ? 0 : wave) + q * kSummers;
-      if (kTiles % kSummers != 0 && tile >= kTiles) break;  // uniform
+    for (int tile = 0; tile < MT; ++tile) {
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         v4f total{0.f, 0.f, 0.f, 0.f};
@@ -685,7 +680,7 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
         v4f part[NT];
 #pragma unroll
         for (int t = 0; t < GS; ++t) {
-          const v8bf xa = *reinterpret_cast<const v8bf*>(xs + place((wm * MT + mt) * 16 + ln, g * GS + t));
+          const v8bf xa = *reinterpret_cast<const v8bf*>(xs + place(mt * 16 + ln, g * GS + t));
 #pragma unroll
           for (int i = 0; i < NT; ++i)
             part[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa, codes[i][t], t == 0 ? v4f{0.f, 0.f, 0.f, 0.f} : part[i],
@@ -711,10 +706,8 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
         zs[i] = 0.f;
       }
     }
-    if constexpr (WK == 1) buf ^= 1;
   }
   wait_lds();
-  if constexpr (WK == 1) block_barrier();
   if (full) {
     correct(mem + L::kSums + (sbuf ^ 1) * L::kSumBytes);
   } else if (slot > 0) {  // unfilled slots have zs = 0 and finite sums
@@ -723,37 +716,27 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
     correct(mem + L::kSums + sbuf * L::kSumBytes);
   }
 
-  if constexpr (WK > 1) {
-    // Add the waves' tiles in wave order: each wave leaves its tile in LDS
-    // (one 16-byte store per lane and 16x16 tile) and takes every WK-th one.
-    __syncthreads();
-    v4f* red = reinterpret_cast<v4f*>(lds);
+  // Add the waves' tiles in wave order: each wave leaves its tile in LDS
+  // (one 16-byte store per lane and 16x16 tile) and takes every WK-th one.
+  __syncthreads();
+  v4f* red = reinterpret_cast<v4f*>(lds);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+  for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int i = 0; i < NT; ++i) red[((wk * MT + mt) * NT + i) * 64 + lane] = acc[mt][i];
-    __syncthreads();
+    for (int i = 0; i < NT; ++i) red[((wk * MT + mt) * NT + i) * 64 + lane] = acc[mt][i];
+  __syncthreads();
 #pragma unroll
-    for (int q = 0; q < MT * NT; ++q) {
-      if (q % WK != wk) continue;
-      v4f v = red[q * 64 + lane];
+  for (int q = 0; q < MT * NT; ++q) {
+    if (q % WK != wk) continue;
+    v4f v = red[q * 64 + lane];
 #pragma unroll
-      for (int o = 1; o < WK; ++o) {
-        const v4f b = red[(o * MT * NT + q) * 64 + lane];
+    for (int o = 1; o < WK; ++o) {
+      const v4f b = red[(o * MT * NT + q) * 64 + lane];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] += b[r];
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) store((q / NT) * 16 + quarter * 4 + r, (q % NT) * 16 + ln, v[r]);
+      for (int r = 0; r < 4; ++r) v[r] += b[r];
     }
-  } else {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          store((wm * MT + mt) * 16 + quarter * 4 + r, wn * 16 * NT + i * 16 + ln, acc[mt][i][r]);
+    for (int r = 0; r < 4; ++r) store((q / NT) * 16 + quarter * 4 + r, (q % NT) * 16 + ln, v[r]);
   }
 }
 
@@ -819,7 +802,7 @@ struct TileOut {
 template <int MT, int NT, int WN, int GS>
 __device__ __forceinline__ void int4_pipe_tile(char* lds, const Int4Args& a, const uint16_t* __restrict__ x,
                                                int64_t rows, int64_t N, int64_t K, int64_t n0, const TileOut& to) {
-  using L = Int4Tile<MT, NT, 1, WN, 1>;
+  using L = Int4Tile<MT, NT, WN, 1>;
   constexpr int G = 4 / GS;  // groups per strip
   const int thread = own_thread();
   const int lane = thread & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(thread / kWave);
@@ -1119,11 +1102,11 @@ __device__ __forceinline__ void int4_pipe_tile(char* lds, const Int4Args& a, con
   });
 }
 
-template <int MT, int NT, int WM, int WN, int WK, int GS>
-__global__ __launch_bounds__(64 * WM * WN * WK) void int4_gemm_kernel(Int4Args a, const uint16_t* __restrict__ x,
+template <int MT, int NT, int WN, int WK, int GS>
+__global__ __launch_bounds__(64 * WN * WK) void int4_gemm_kernel(Int4Args a, const uint16_t* __restrict__ x,
                                                                  void* __restrict__ out, int out_bf16, int64_t M,
                                                                  int64_t N, int64_t K, float alpha, Epilogue epi) {
-  using L = Int4Tile<MT, NT, WM, WN, WK>;
+  using L = Int4Tile<MT, NT, WN, WK>;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   // Row tiles of one column tile follow each other on one XCD, whose L2 then
   // holds the column tile's weights.
@@ -1132,14 +1115,14 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void int4_gemm_kernel(Int4Args a
   const int64_t tile = int64_t(blockIdx.x % 8) * per + blockIdx.x / 8;
   if (int64_t(blockIdx.x / 8) >= per || tile >= total) return;  // uniform over the block
   const int64_t m0 = tile % mtiles * L::kBM, n0 = tile / mtiles * L::kBN;
-  auto put = [&](int m, int n, float v) {
-    if (m0 + m < M && n0 + n < N) store_epi(out, m0 + m, n0 + n, N, v, alpha, out_bf16, epi);
-  };
   if constexpr (WK == 1) {
     const TileOut to{static_cast<char*>(out) + m0 * N * (out_bf16 ? 2 : 4), M - m0, N, n0, m0, alpha, out_bf16, &epi};
     int4_pipe_tile<MT, NT, WN, GS>(lds, a, x + m0 * K, M - m0, N, K, n0, to);
+  } else {
+    int4_tile<MT, NT, WK, GS>(lds, a, x + m0 * K, M - m0, N, K, n0, [&](int m, int n, float v) {
+      if (m0 + m < M && n0 + n < N) store_epi(out, m0 + m, n0 + n, N, v, alpha, out_bf16, epi);
+    });
   }
-  else int4_tile<MT, NT, WM, WN, WK, GS>(lds, a, x + m0 * K, M - m0, N, K, n0, put);
 }
 
 // Grouped: group z owns rows a_offsets[z] .. a_offsets[z + 1] - 1 (clipped to
@@ -1220,7 +1203,7 @@ __global__ __launch_bounds__(64 * WN) void int4_grouped_kernel(Int4Args a, const
                                                                const int32_t* __restrict__ expert_ids,
                                                                void* __restrict__ out, int out_bf16, int64_t groups,
                                                                int64_t T, int64_t N, int64_t K, int64_t E) {
-  using L = Int4Tile<MT, NT, 1, WN, 1>;
+  using L = Int4Tile<MT, NT, WN, 1>;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   walk_groups<L::kBM, L::kBN, L::kThreads>(
       reinterpret_cast<int*>(lds + L::kLds), a, a_offsets, expert_ids, out, out_bf16, groups, T, N, E,
@@ -1300,15 +1283,15 @@ hipError_t stream_rows(const Int4Args& a, const uint16_t* x, void* out, int bf16
   return stream_cfg<M, 1, 1, 8>(a, x, out, bf16, rows, N, K, alpha, epi, s);
 }
 
-template <int MT, int NT, int WM, int WN, int WK>
+template <int MT, int NT, int WN, int WK>
 hipError_t gemm_cfg(const Int4Args& a, const uint16_t* x, void* out, int bf16, int64_t M, int64_t N, int64_t K,
                     float alpha, const Epilogue& epi, hipStream_t s) {
-  using L = Int4Tile<MT, NT, WM, WN, WK>;
+  using L = Int4Tile<MT, NT, WN, WK>;
   const int64_t total = ((M + L::kBM - 1) / L::kBM) * ((N + L::kBN - 1) / L::kBN);
   const int64_t blocks = (total + 7) / 8 * 8;
   if (blocks * L::kThreads >= (int64_t(1) << 32)) return hipErrorInvalidValue;
   return by_group(a, [&](auto gs) -> hipError_t {
-    auto kernel = int4_gemm_kernel<MT, NT, WM, WN, WK, decltype(gs)::value>;
+    auto kernel = int4_gemm_kernel<MT, NT, WN, WK, decltype(gs)::value>;
     static std::atomic<uint64_t> lds_set{0};
     if (hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(kernel), L::kLds, lds_set)) return e;
     return launch(kernel, dim3(unsigned(blocks)), dim3(L::kThreads), L::kLds, s, a, x, out, bf16, M, N, K, alpha, epi);
@@ -1347,7 +1330,7 @@ struct GroupedCall {
 
 template <int MT, int NT, int WN>
 hipError_t grouped_cfg(const GroupedCall& c) {
-  using L = Int4Tile<MT, NT, 1, WN, 1>;
+  using L = Int4Tile<MT, NT, WN, 1>;
   return by_group(c.a, [&](auto gs) -> hipError_t {
     static std::atomic<uint64_t> lds_set{0};
     return c.go(int4_grouped_kernel<MT, NT, WN, decltype(gs)::value>, lds_set, int(L::kLds + 4 * (c.G + 1)), L::kBM, L::kBN,
@@ -1374,27 +1357,45 @@ hipError_t launch_int4_gemm(const uint8_t* w, const uint16_t* scale, const uint8
   if (M == 1) return stream_rows<1>(a, x, out, out_bf16, M, N, K, alpha, num_cus, epi, s);
   if (M == 2) return stream_rows<2>(a, x, out, out_bf16, M, N, K, alpha, num_cus, epi, s);
   if (M <= 4) return stream_rows<4>(a, x, out, out_bf16, M, N, K, alpha, num_cus, epi, s);
-  // Small tiles whose waves split K, while a CU gets at most 4 of 32x32: M = 100, N = K =
-  // 4096: 22 us, 64x128 44; M = 64, N = 14336, K = 4096: 40 and 51; M = 100 there (7 of them per
-  // CU): 63 and 47.  Half their width or height where one would leave CUs without any:
-  // M = 16, N = K = 4096: 16x16 7.9 us, 16x32 10.3; N = 14336: 21.1 and 18.7.
-  auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  const bool narrow = N <= int64_t(num_cus) * 32;
+  // Up to 16 rows: tiles whose 4 waves split K, narrower where wide ones would leave CUs without any
+  // (N = K = 4096: 16x16 7.9 us, 16x32 10.3; N = 14336: 21.1 and 18.7).
   if (M <= 16) {
-    if (narrow) return gemm_cfg<1, 1, 1, 1, 4>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
-    return gemm_cfg<1, 2, 1, 1, 4>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
+    if (N <= int64_t(num_cus) * 32) return gemm_cfg<1, 1, 1, 4>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
+    return gemm_cfg<1, 2, 1, 4>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
   }
-  if (tiles(32, 32) <= 4 * int64_t(num_cus)) {
-    if (M <= 32 && narrow) return gemm_cfg<2, 1, 1, 1, 4>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
-    return gemm_cfg<2, 2, 1, 1, 4>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
+  // Above, the tile with the least time for the CU that gets most of them.  A tile's time
+  // hardly depends on how many other CUs have one: for K = 4096, groups of 64, in us,
+  //   64x128 38 (M = 500, N = 4096: 256 tiles 39; M = 200, N = 14336: 448 of them 74)
+  //   32x128 28 (M = 250, N = 4096: 29; M = 500: 55), 64x256 64, 128x128 62, 128x256 112
+  //   (M = 500, N = 14336: 112; with 128x128 tiles 124, 64x256 128, 64x128 150).
+  // Those of 32x32 and 32x16 split K over their waves and share a CU: 11 (9) for the first, and
+  // as much for each more on average (M = 64, N = 4096: 13; M = 64, N = 14336: 40).
+  struct Tile {
+    int bm, bn, us;
+    bool shared;
+  };
+  constexpr Tile kTiles[] = {{32, 16, 9, true},    {32, 32, 11, true},    {32, 128, 28, false}, {64, 128, 38, false},
+                             {64, 256, 64, false}, {128, 128, 62, false}, {128, 256, 112, false}};
+  int best = 0;
+  double least = 0.0;
+  for (int i = 0; i < int(sizeof(kTiles) / sizeof(Tile)); ++i) {
+    const Tile& t = kTiles[i];
+    const int64_t tiles = ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
+    const double per_cu = t.shared ? std::max(1.0, double(tiles) / num_cus) : double((tiles + num_cus - 1) / num_cus);
+    if (i == 0 || per_cu * t.us < least) {
+      best = i;
+      least = per_cu * t.us;
+    }
   }
-  // Tiles of 256 columns as high as M (M = 64, N = 60000, K = 2048: 64x256 36 us, 32x32 71),
-  // of 128 rows where they give more than half of the CUs one (M = 500, N = 14336, K = 4096:
-  // 90 us, 64x128 144), else 64x128 (M = 500, N = K = 4096: 47 against 90).
-  if (M <= 32) return gemm_cfg<2, 2, 1, 8, 1>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
-  if (M <= 64) return gemm_cfg<4, 2, 1, 8, 1>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
-  if (tiles(128, 256) * 2 > num_cus) return gemm_cfg<8, 2, 1, 8, 1>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
-  return gemm_cfg<4, 2, 1, 4, 1>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
+  switch (best) {
+    case 0: return gemm_cfg<2, 1, 1, 4>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
+    case 1: return gemm_cfg<2, 2, 1, 4>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
+    case 2: return gemm_cfg<2, 1, 8, 1>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
+    case 3: return gemm_cfg<4, 1, 8, 1>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
+    case 4: return gemm_cfg<4, 2, 8, 1>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
+    case 5: return gemm_cfg<8, 1, 8, 1>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
+    default: return gemm_cfg<8, 2, 8, 1>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
+  }
 }
 
 hipError_t launch_int4_grouped(const uint8_t* w, const uint16_t* scale, const uint8_t* zero, const uint16_t* x,
@@ -1402,24 +1403,18 @@ hipError_t launch_int4_grouped(const uint8_t* w, const uint16_t* scale, const ui
                                int64_t G, int64_t E, int64_t T, int64_t N, int64_t K, int64_t group, int num_cus,
                                hipStream_t s) {
   const Int4Args a = make_args(w, scale, zero, K, group);
-  // Tiles by the rows a group has on average (64 experts, N = 1536, K = 2048, groups
-  // of 128): 16x128 to 4 rows (64 rows: 40 us, 32x128 44), 32x128 to 16 (256 rows: 46,
-  // 16x128 50, 64x256 70), 64x256 to 256 (4096 rows: 108, 32x128 113), 128x256 above
-  // (8 experts, N = K = 4096, 4096 rows: 301 against 357).
-  // By the rows a group has on average (64 experts, N = 1536, K = 2048, groups of
-  // 128, unless said): to 4 the streaming form (64 rows: 37 us, 32x256 56; 256 rows: 46 and 56),
-  // to 32 tiles of 32x256 (1024 rows: 57, 64x256 68), to 256 of 64x256 (4096 rows: 101, 32x256
-  // 109; 8 experts, N = K = 4096, 512 rows: 86, 128x256 131), above of 128x256 (those
-  // with 4096 rows: 363, 64x256 385).
+  // By the rows a group has on average (64 experts, N = 1536, K = 2048, groups of 128, unless
+  // said), in us: to 4 the streaming form (64 rows: 35, 32x256 54; 256 rows: 44 and 54), to 32 tiles of
+  // 32x256 (1024 rows: 57, 64x256 68), above of 64x256 (4096 rows: 102, 32x256 109, 128x256 128;
+  // 8 experts, N = K = 4096, groups of 64, 512 rows: 74, 128x256 128; 4096 rows: 338 and 348).
   // A block keeps the groups' prefix sums in LDS beside its tile: more groups take more launches.
   constexpr int64_t kMost = 16384;
   for (int64_t z = 0; z < G; z += kMost) {
     const int64_t groups = std::min(kMost, G - z);
     const GroupedCall c{a, x, a_offsets + z, expert_ids + z, out, out_bf16, groups, E, T, N, K, num_cus, s};
-    const hipError_t e = T <= 4 * G     ? grouped_stream<1, 4>(c)
-                         : T <= 32 * G  ? grouped_cfg<2, 2, 8>(c)
-                         : T <= 256 * G ? grouped_cfg<4, 2, 8>(c)
-                                        : grouped_cfg<8, 2, 8>(c);
+    const hipError_t e = T <= 4 * G    ? grouped_stream<1, 4>(c)
+                         : T <= 32 * G ? grouped_cfg<2, 2, 8>(c)
+                                       : grouped_cfg<4, 2, 8>(c);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
