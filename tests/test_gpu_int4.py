@@ -350,11 +350,11 @@ def test_grouped_many_groups(q, groups, t):
     assert written.all() and same(out, ref)
 
 
-# one to four rows a group, about 16, about 64, over 256: each form of the walk; K long, odd and short
-@pytest.mark.parametrize("rows", [1, 3, 16, 70, 300])
+# one to six rows a group, about 16 in few columns and in many, over 32: each form of the walk; K long, odd and short
+@pytest.mark.parametrize("rows,n", [(1, 272), (3, 272), (16, 272), (16, 9000), (70, 272), (300, 272)])
 @pytest.mark.parametrize("k,group", [(1100, 32), (1024, 64), (897, 128), (2000, 512), (33, 32)])
-def test_grouped_forms(q, rows, k, group):
-    e, n, groups = 5, 272, 7
+def test_grouped_forms(q, rows, n, k, group):
+    e, groups = 5, 7
     rng = np.random.default_rng([23, rows, k])
     counts = rng.integers(0, 2 * rows + 1, groups)
     counts[0], counts[3] = rows, 0

@@ -1213,9 +1213,13 @@ __global__ __launch_bounds__(64 * WN) void int4_grouped_kernel(Int4Args a, const
       });
 }
 
-// Groups of few rows: tiles of 4 rows through the streaming form.
+// Groups of few rows: tiles of 4 rows through the streaming form, 3 waves per SIMD: with 4, 50 to
+// 150 bytes of a lane's step went to memory (64 experts, N = 1536, K = 2048, groups of 128:
+// 64 rows 35 us, with 3 29; 256 rows 44 and 40; with 3 and a fourth block per CU 30 and 48).
+constexpr int kStreamWaves = 3;
+
 template <int NT, int WN, int SH>
-__global__ __launch_bounds__(64 * WN, 4) void int4_grouped_stream_kernel(Int4Args a, const uint16_t* __restrict__ x,
+__global__ __launch_bounds__(64 * WN, kStreamWaves) void int4_grouped_stream_kernel(Int4Args a, const uint16_t* __restrict__ x,
                                                                          const uint32_t* __restrict__ a_offsets,
                                                                          const int32_t* __restrict__ expert_ids,
                                                                          void* __restrict__ out, int out_bf16,
@@ -1300,11 +1304,12 @@ hipError_t gemm_cfg(const Int4Args& a, const uint16_t* x, void* out, int bf16, i
 
 constexpr int kMaxLds = 160 * 1024;
 
-// Blocks for a walk of tiles BM x BN: as many as fit, if there are so many tiles (at
+// Blocks for a walk of tiles BM x BN: as many as fit by LDS and registers (`waves` per block of
+// cu_waves per CU), if there are so many tiles (at
 // most ceil(T / BM) + min(G, T) row tiles exist), a multiple of 8.
-int64_t walk_blocks(int64_t BM, int64_t BN, int waves, int lds, int64_t G, int64_t T, int64_t N, int num_cus) {
+int64_t walk_blocks(int64_t BM, int64_t BN, int waves, int cu_waves, int lds, int64_t G, int64_t T, int64_t N, int num_cus) {
   const int64_t upper = ((T + BM - 1) / BM + std::min(G, T)) * ((N + BN - 1) / BN);
-  const int64_t per_cu = std::max<int64_t>(1, std::min<int64_t>(kMaxLds / lds, 16 / waves));
+  const int64_t per_cu = std::max<int64_t>(1, std::min<int64_t>(kMaxLds / lds, cu_waves / waves));
   return (std::min(upper, per_cu * num_cus) + 7) / 8 * 8;
 }
 
@@ -1320,10 +1325,10 @@ struct GroupedCall {
   hipStream_t s;
 
   template <typename Kernel> hipError_t go(Kernel kernel, std::atomic<uint64_t>& lds_set, int lds, int64_t BM, int64_t BN,
-                                           int waves) const {
+                                           int waves, int cu_waves) const {
     if (lds > kMaxLds) return hipErrorInvalidValue;
     if (hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(kernel), kMaxLds, lds_set)) return e;
-    const int64_t blocks = walk_blocks(BM, BN, waves, lds, G, T, N, num_cus);
+    const int64_t blocks = walk_blocks(BM, BN, waves, cu_waves, lds, G, T, N, num_cus);
     return launch(kernel, dim3(unsigned(blocks)), dim3(64 * waves), lds, s, a, x, offsets, ids, out, bf16, G, T, N, K, E);
   }
 };
@@ -1334,7 +1339,7 @@ hipError_t grouped_cfg(const GroupedCall& c) {
   return by_group(c.a, [&](auto gs) -> hipError_t {
     static std::atomic<uint64_t> lds_set{0};
     return c.go(int4_grouped_kernel<MT, NT, WN, decltype(gs)::value>, lds_set, int(L::kLds + 4 * (c.G + 1)), L::kBM, L::kBN,
-                WN);
+                WN, 16);
   });
 }
 
@@ -1344,7 +1349,7 @@ hipError_t grouped_stream(const GroupedCall& c) {
   return by_shift(c.a, [&](auto sh) -> hipError_t {
     static std::atomic<uint64_t> lds_set{0};
     return c.go(int4_grouped_stream_kernel<NT, WN, decltype(sh)::value>, lds_set, int(kLds + 4 * (c.G + 1)), 4, 16 * NT * WN,
-                WN);
+                WN, 4 * kStreamWaves);
   });
 }
 
@@ -1404,16 +1409,19 @@ hipError_t launch_int4_grouped(const uint8_t* w, const uint16_t* scale, const ui
                                hipStream_t s) {
   const Int4Args a = make_args(w, scale, zero, K, group);
   // By the rows a group has on average (64 experts, N = 1536, K = 2048, groups of 128, unless
-  // said), in us: to 4 the streaming form (64 rows: 35, 32x256 54; 256 rows: 44 and 54), to 32 tiles of
-  // 32x256 (1024 rows: 57, 64x256 68), above of 64x256 (4096 rows: 102, 32x256 109, 128x256 128;
-  // 8 experts, N = K = 4096, groups of 64, 512 rows: 74, 128x256 128; 4096 rows: 338 and 348).
+  // said), in us: to 6 the streaming form (64 rows: 29, 32x256 54; 384 rows: 50 and 58; 768 rows: 85
+  // and 57), to 32 tiles of 32x256 (1024 rows: 57, 32x128 66, 64x256 68), or of 32x128 where 32x256 would
+  // leave CUs without any (8 experts, N = K = 4096, groups of 64, 96 rows: 37 and 60), above of
+  // 64x256 (4096 rows: 102, 32x256 109, 128x256 128; those 8 experts, 512 rows: 74, 64x128 83,
+  // 128x256 128; 4096 rows: 338, 128x256 348).
+  const bool few = ((T + 31) / 32 + std::min(G, T)) * ((N + 255) / 256) <= num_cus;
   // A block keeps the groups' prefix sums in LDS beside its tile: more groups take more launches.
   constexpr int64_t kMost = 16384;
   for (int64_t z = 0; z < G; z += kMost) {
     const int64_t groups = std::min(kMost, G - z);
     const GroupedCall c{a, x, a_offsets + z, expert_ids + z, out, out_bf16, groups, E, T, N, K, num_cus, s};
-    const hipError_t e = T <= 4 * G    ? grouped_stream<1, 4>(c)
-                         : T <= 32 * G ? grouped_cfg<2, 2, 8>(c)
+    const hipError_t e = T <= 6 * G    ? grouped_stream<1, 4>(c)
+                         : T <= 32 * G ? few ? grouped_cfg<2, 1, 8>(c) : grouped_cfg<2, 2, 8>(c)
                                        : grouped_cfg<4, 2, 8>(c);
     if (e != hipSuccess) return e;
   }
