@@ -86,7 +86,7 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 // most 16 each), so a wave takes up to 4 tokens; lane l of a token holds the R
 // logits e = l R .. l R + R - 1.  The kernel is bound by its vector instructions, and
 // a pick costs the same ones however many tokens the wave holds: T = 16384, E = 256,
-// top 8, bfloat16 took 15.8 us with one token per wave.
+// top 8, bfloat16 takes 9.0 us, 15.8 with one token per wave.
 
 // Reductions over the L lanes of a token; every lane gets the result.
 template <int L, typename F>
@@ -239,7 +239,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const void* __rest
 // With renormalised weights the softmax runs over the chosen ones only, so only their logits
 // are read, and every other gradient is 0.  Lane layout of the router; a row (the
 // chosen experts' gradients, or with renormalised weights the result) lies in LDS,
-// where the chosen lanes put what belongs to their experts.
+// where the chosen lanes put what belongs to their experts.  T = 16384, E = 256, bfloat16:
+// 7.8 us, 2.2 TB/s; bound by the vector instructions of the softmax as the router is.
 template <int BF16, int L, int R>
 __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const void* __restrict__ logits,
                                                                        const int32_t* __restrict__ ids,
@@ -341,7 +342,9 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const voi
 //   start of its bin + the bin's slots in earlier pieces + its rank in the
 //   wave's piece,
 // with no atomic whose order could matter: counts come from LDS atomics
-// (sums only), ranks from ballots.
+// (sums only), ranks from ballots.  Bound by latency, the way from the ids over the counts to
+// the places: 64 slots 4.7 us (one launch), 131072 slots of 256 experts 4.8 to count
+// and 9.7 to place.
 constexpr int kSortWaves = 8;
 constexpr int kSortThreads = kSortWaves * kWave;
 constexpr int kSortMaxBins = 1025;
@@ -501,7 +504,8 @@ __device__ __forceinline__ Slots load_slots(const int32_t* p, const float* w, in
 }
 
 // The token's bytes are read once and stored to each of its top_k rows; a
-// dropped slot (~row) clears the row it pads.
+// dropped slot (~row) clears the row it pads.  16384 tokens of 2048 bfloat16, top 8: 120 us, 5.0 TB/s
+// read and written, the rate of a copy.
 template <int BF16, bool NT>
 __global__ __launch_bounds__(256) void gather_kernel(const void* __restrict__ x, const int32_t* __restrict__ slot_row,
                                                      void* __restrict__ out, int64_t T, int top_k, int64_t H,
@@ -532,7 +536,7 @@ __global__ __launch_bounds__(256) void gather_kernel(const void* __restrict__ x,
 }
 
 // out[t] = sum over the token's live slots, in slot order, of weight x row,
-// in float32, rounded once.
+// in float32, rounded once.  The same sizes: 114 us, 5.3 TB/s.
 template <int BF16, int OBF16, bool NT>
 __global__ __launch_bounds__(256, 6) void combine_kernel(const void* __restrict__ rows,
                                                          const int32_t* __restrict__ slot_row,
@@ -593,7 +597,7 @@ __global__ __launch_bounds__(256, 6) void combine_kernel(const void* __restrict_
 // Gradients of the weighted sum: grad_rows[row] = w dy[t] and
 // grad_weights[t, j] = <dy[t], rows[row]>.  One wave per slot, four pieces of the row
 // in flight; the slots of a token run next to each other, so dy comes from the
-// caches after the first.
+// caches after the first.  4099 tokens of 4096 bfloat16, top 6: 86 us for 437 MB, 5.1 TB/s.
 template <int BF16, bool NT>
 __global__ __launch_bounds__(256) void combine_backward_kernel(
     const void* __restrict__ dy, const void* __restrict__ rows, const int32_t* __restrict__ slot_row,
@@ -703,7 +707,8 @@ struct Divisor {
   }
 };
 
-// x: [M, 2F], gate columns first.  Thread item = 16 bytes of one row's half.
+// x: [M, 2F], gate columns first.  Thread item = 16 bytes of one row's half.  Bound by HBM: 32768 x 1536,
+// bfloat16, 47 us, 6.4 TB/s; the gradient of 4100 x 1535 in float32 22 us, 5.7 TB/s.
 template <int BF16, bool BACK, bool NT>
 __global__ __launch_bounds__(256) void swiglu_kernel(const void* __restrict__ x, const void* __restrict__ dy,
                                                      void* __restrict__ out, uint32_t items, int64_t F,
