@@ -578,8 +578,9 @@ def int8_grouped_gemm(a: torch.Tensor, b: torch.Tensor, a_scale: torch.Tensor | 
 
 
 def _int4_operands(w_packed, w_scale, w_zero, x, group_size: int, lead: str):
-    """The checked int4 operands (w, scale, zero pointer, x, K, groups); ``lead`` names
-    the leading dimension of an expert stack ("" for one matrix)."""
+    """The checked int4 operands (w, scale, zero pointer, x, K, group size); ``lead`` names
+    the leading dimension of an expert stack ("" for one matrix).  The group size comes
+    back as at most K, which means the same and fits the call's 64-bit argument."""
     w = _as_u8(w_packed, "w_packed")
     sc = _as_bf16(w_scale, "w_scale")
     x = _as_bf16(x, "x")
@@ -600,7 +601,7 @@ def _int4_operands(w_packed, w_scale, w_zero, x, group_size: int, lead: str):
         if w_zero.dtype != torch.uint8 or w_zero.shape != sc.shape:
             raise ValueError("w_zero must be uint8 of w_scale's shape")
         zero = _ptr(w_zero)
-    return w, sc, zero, x, k
+    return w, sc, zero, x, k, min(int(group_size), k)
 
 
 def int4_gemm(w_packed: torch.Tensor, w_scale: torch.Tensor, x: torch.Tensor, w_zero: torch.Tensor | None = None,
@@ -612,14 +613,14 @@ def int4_gemm(w_packed: torch.Tensor, w_scale: torch.Tensor, x: torch.Tensor, w_
     packed [N, (K + 1) / 2] (even k in the low nibble), one bfloat16 scale and one uint8
     zero point (None: 8) per ``group_size`` consecutive k (``qlinear_int4_gemm``);
     epilogue as ``fp8_gemm``."""
-    w, sc, zero, x, k = _int4_operands(w_packed, w_scale, w_zero, x, group_size, "")
+    w, sc, zero, x, k, group = _int4_operands(w_packed, w_scale, w_zero, x, group_size, "")
     m, n = x.shape[0], w.shape[0]
     out = _out(out, (m, n), out_dtype, x.device)
     d = _epilogue(m, n, row_scale, col_scale, bias, residual, activation) if m else None
     if m == 0:
         return out
     st = lib.qlinear_int4_gemm(_ptr(w), _ptr(sc), zero, _ptr(x), _ptr(out), _OUT_CODES[out_dtype], m, n, k,
-                               int(group_size), float(alpha), _epi_ref(d), _stream(x))
+                               group, float(alpha), _epi_ref(d), _stream(x))
     _check(st, "qlinear_int4_gemm")
     return out
 
@@ -633,7 +634,7 @@ def int4_grouped_gemm(w_packed: torch.Tensor, w_scale: torch.Tensor, x: torch.Te
     ``int4_gemm`` from the expert stack w_packed [E, N, (K + 1) / 2], w_scale and w_zero
     [E, N, ceil(K / group_size)].  Rows outside every group keep whatever ``out`` held
     (a new ``out`` starts uninitialised)."""
-    w, sc, zero, x, k = _int4_operands(w_packed, w_scale, w_zero, x, group_size, "E, ")
+    w, sc, zero, x, k, group = _int4_operands(w_packed, w_scale, w_zero, x, group_size, "E, ")
     _require(a_offsets, "a_offsets")
     _require(expert_ids, "expert_ids")
     if a_offsets.dtype not in (torch.int32, torch.uint32) or expert_ids.dtype != torch.int32:
@@ -650,7 +651,7 @@ def int4_grouped_gemm(w_packed: torch.Tensor, w_scale: torch.Tensor, x: torch.Te
         return out
     st = lib.qlinear_int4_grouped_gemm(_ptr(w), _ptr(sc), zero, _ptr(x), _ptr(a_offsets), _ptr(expert_ids), _ptr(out),
                                        _OUT_CODES[out_dtype], g, int(max_tokens_per_group), e, t, n, k,
-                                       int(group_size), _stream(x))
+                                       group, _stream(x))
     _check(st, "qlinear_int4_grouped_gemm")
     return out
 

@@ -1243,6 +1243,7 @@ __global__ __launch_bounds__(64 * WN, kStreamWaves) void int4_grouped_stream_ker
 // ---------------------------------------------------------------- launch
 
 Int4Args make_args(const uint8_t* w, const uint16_t* scale, const uint8_t* zero, int64_t K, int64_t group) {
+  group = std::min(group, K);  // one group per row may be asked for with any larger value: K + group could overflow
   Int4Args a{w, scale, zero, (K + 1) / 2, (K + group - 1) / group, 62};
   if (group < K) {
     a.shift = 0;
