@@ -659,38 +659,43 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(
 
 // ---------------------------------------------------------------- gated activation
 
-// sigmoid(g) and sigmoid(-g) from e = exp(-|g|), as 1 / (1 + e) and e / (1 + e): neither
-// overflows nor cancels.  Good to a few float32 roundings (u = 2^-24):
-// |g| log2(e) is taken with the rounding error of its product, so the
-// exponential is off by 3 u (the instruction itself by 2), 1 + e adds one, and a Newton step
-// leaves one of the reciprocal.  Beyond |g| = 256 nothing changes (e = 0).
+// What sigmoid(g) and sigmoid(-g) are made of, from h = exp(-|g| / 2): near = 1 / (1 + h^2) =
+// sigmoid(|g|); half = 1 for g >= 0, else h, so that sigmoid(g) = half^2 near; rest = sigmoid(-g).  Nothing
+// overflows or cancels.  A negative gate's two halves go to different factors of a
+// product: h^2 leaves float32's normal range below g = -87 (and the exponential instruction gives 0
+// there), where its product with u or dy need not, and h only below g = -174.
+// Good to a few float32 roundings (u = 2^-24): |g| log2(e) / 2 is taken with the
+// rounding error of its product, so h is off by 3 u (the instruction itself by 2) and h^2 by 7, 1 + h^2
+// adds one, and a Newton step leaves one of the reciprocal.  Beyond |g| = 256 nothing changes (h = 0).
 // The library's expf and division would be twice the instructions, and the forward pass over
 // bfloat16 was bound by them.
-__device__ __forceinline__ void sigmoids(float g, float& sig, float& rest) {
-  constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;  // log2(e)
+__device__ __forceinline__ void sigmoids(float g, float& near, float& half, float& rest) {
+  constexpr float kHi = 0.5f * 1.44269502f, kLo = 0.5f * 1.92596299e-8f;  // log2(e) / 2
   const float a = fminf(fabsf(g), 256.f);
   const float t = -a * kHi;
   const float r = fmaf(-a, kLo, fmaf(-a, kHi, -t));
-  float e = __builtin_amdgcn_exp2f(t);
-  e = fmaf(e, r * 0.693147182f, e);
-  const float d = 1.f + e, y = __builtin_amdgcn_rcpf(d);
-  const float near = fmaf(y, fmaf(-d, y, 1.f), y), far = e * near;
-  sig = g >= 0.f ? near : far;
-  rest = g >= 0.f ? far : near;
+  float h = __builtin_amdgcn_exp2f(t);
+  h = fmaf(h, r * 0.693147182f, h);
+  const float d = fmaf(h, h, 1.f), y = __builtin_amdgcn_rcpf(d);
+  near = fmaf(y, fmaf(-d, y, 1.f), y);
+  half = g >= 0.f ? 1.f : h;
+  rest = g >= 0.f ? h * h * near : near;
 }
 
 __device__ __forceinline__ float swiglu_one(float g, float u) {
-  float sig, rest;
-  sigmoids(g, sig, rest);
-  return g * sig * u;
+  float near, half, rest;
+  sigmoids(g, near, half, rest);
+  return (g * near * half) * (u * half);
 }
 
-// dgate = dy u sig (1 + g (1 - sig)), dup = dy g sig, with sigmoid(-g) for 1 - sig.
+// dgate = dy u sig (1 + g (1 - sig)), dup = dy g sig, with sigmoid(-g) for 1 - sig.  dy u alone
+// could overflow where the gradient does not.
 __device__ __forceinline__ void swiglu_grad(float g, float u, float dy, float& dg, float& du) {
-  float sig, rest;
-  sigmoids(g, sig, rest);
-  dg = dy * u * sig * fmaf(g, rest, 1.f);
-  du = dy * (g * sig);
+  float near, half, rest;
+  sigmoids(g, near, half, rest);
+  const float dh = dy * half;
+  dg = dh * (u * half) * (near * fmaf(g, rest, 1.f));
+  du = dh * (g * near * half);
 }
 
 // n / d for n < 2^31 as a product: m = floor(2^(31 + l) / d) + 1 with l = ceil(log2 d) is
