@@ -10,7 +10,7 @@ import torch
 
 from oracle import moe as O
 from gpu_util import DEV, show
-from test_gpu_int4 import dev, exact_weight, operands, same
+from test_gpu_int4 import dev, exact_weight, operands, plain64, random_operands, same
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,18 @@ def test_any_group_size_from_k_on_is_one_group(q, m, k, group_size):
     assert st == q.OK
     ref, _, _ = O.int4_grouped(packed, scale, zero, x, k, offs.cpu().numpy(), ids.cpu().numpy())
     assert same(out, ref)
+
+
+# rows that end in every 16 rows of a tile, in tiles of several shapes, first and last column tile
+@pytest.mark.parametrize("m", [18, 31, 33, 47, 48, 49, 63, 65, 80, 81, 95, 97, 112, 113, 127, 129])
+@pytest.mark.parametrize("n", [20001, 33000])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_rows_behind_the_last_one_stay(q, m, n, dt):
+    k = 128
+    w, s, z, x = random_operands(m + n, m, n, k, 64, True, True)
+    rows = 200
+    buf = torch.full((m + 2 * rows, n), 7.0, dtype=dt, device=DEV)
+    show("int4 rows behind", m, n, dt)
+    q.int4_gemm(w, s, x, w_zero=z, group_size=64, out=buf[rows:rows + m], out_dtype=dt)
+    assert torch.equal(buf[rows:rows + m], plain64(w, s, z, x, 64).to(dt))
+    assert torch.all(buf[:rows] == 7.0) and torch.all(buf[rows + m:] == 7.0)

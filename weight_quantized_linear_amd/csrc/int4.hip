@@ -741,10 +741,12 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
 }
 
 // A tile's way out: `out` [rows, N] from row 0, column n0 of the tile on.  Plain results
-// leave through a buffer whose record count ends with the last row, so that neither rows nor
-// columns need a branch (a column past N gets an offset past the end), with the row's offset in a
-// scalar register: 3 instructions per value where the general store takes 25, which for
-// 128x256 were 5 us.  With an epilogue, or where a tile spans 2 GiB, values go
+// leave through buffers whose record count ends with the last row, so that neither rows nor
+// columns need a branch: a column past N gets an offset past the end, and a row past the last one has
+// it.  Each 16 rows have a buffer of their own, beginning at their first row: the hardware's check takes the lane's
+// offset against the count less the scalar offset, so a row in the scalar offset would be past the count
+// itself, where the difference is no longer a bound.  3 instructions per value where the general
+// store takes 25, which for 128x256 were 5 us.  With an epilogue, or where a tile spans 2 GiB, values go
 // one by one.
 struct TileOut {
   void* out;      // row 0, column 0
@@ -761,22 +763,23 @@ struct TileOut {
     const int64_t es = bf16 ? 2 : 4;
     const bool plain = !(epi && epi->on) && int64_t(BM) * N * es < (int64_t(1) << 31);
     if (plain) {
-      const int64_t live = rows < BM ? rows : BM;
-      const uint32_t bytes = uint32_t((live * N - n0) * es);
-      const __amdgpu_buffer_rsrc_t buf =
-          __builtin_amdgcn_make_buffer_rsrc(static_cast<char*>(out) + n0 * es, 0, int(bytes), 0x00020000);
+      const int live = int(rows < BM ? rows : BM);
+      char* const first = static_cast<char*>(out) + n0 * es;
       const uint32_t line = uint32_t(N * es), lane_at = uint32_t(quarter * 4) * line + uint32_t(ln * es);
       const int64_t width = N - n0;
       each([&](int m, int n, v4f v) {
+        const uint32_t bytes = m < live ? uint32_t(live - m) * line - uint32_t(n0 * es) : 0u;
+        const __amdgpu_buffer_rsrc_t buf =
+            __builtin_amdgcn_make_buffer_rsrc(first + int64_t(m) * line, 0, int(bytes), 0x00020000);
         const uint32_t at = n + ln < width ? lane_at + uint32_t(n * es) : 0x80000000u;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float f = v[r] * alpha;
           if (bf16)
-            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, static_cast<__bf16>(f)), buf, at,
-                                                  uint32_t(m + r) * line, 0);
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, static_cast<__bf16>(f)), buf,
+                                                  at + uint32_t(r) * line, 0, 0);
           else
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f), buf, at, uint32_t(m + r) * line, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f), buf, at + uint32_t(r) * line, 0, 0);
         }
       });
       return;
