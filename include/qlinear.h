@@ -474,7 +474,9 @@ int qlinear_int8_grouped_gemm(const void* a, const void* b, const float* a_scale
  * [M, K]; out: [M, N] of out_dtype (F32 or BF16); 1 <= K < 2^23.  w_packed and
  * w_zero need no alignment, the others that of their type.  Each group is
  * summed in float32 over exact products and scaled then, so no weight is
- * rounded.  alpha and `epilogue` (NULL = none) as in qlinear_fp8_gemm_ws.
+ * rounded.  A sum that is not finite that way (infinite or NaN activations or
+ * scales, partial sums beyond float32) is taken by the formula in float64, so
+ * infinities and NaN are the formula's, and finite results stay so.  alpha and `epilogue` (NULL = none) as in qlinear_fp8_gemm_ws.
  * M = 0 is allowed and does nothing.
  */
 int qlinear_int4_gemm(const void* w_packed, const void* w_scale, const void* w_zero, const void* x,

@@ -64,3 +64,99 @@ def test_rows_behind_the_last_one_stay(q, m, n, dt):
     q.int4_gemm(w, s, x, w_zero=z, group_size=64, out=buf[rows:rows + m], out_dtype=dt)
     assert torch.equal(buf[rows:rows + m], plain64(w, s, z, x, 64).to(dt))
     assert torch.all(buf[:rows] == 7.0) and torch.all(buf[rows + m:] == 7.0)
+
+
+def equal_or_nan(out, ref):
+    """Bit for bit the float64 reference rounded to the output's type; NaN where it is NaN."""
+    return torch.equal(torch.nan_to_num(out, nan=0.125, posinf=float("inf"), neginf=float("-inf")),
+                       torch.nan_to_num(ref.to(out.dtype), nan=0.125, posinf=float("inf"), neginf=float("-inf")))
+
+
+def defined64(w, s, z, x, group):
+    """x @ D^T elementwise in float64, so that infinities meet exactly the weights of their k."""
+    k = x.shape[1]
+    codes = torch.stack([w & 15, w >> 4], -1).reshape(w.shape[0], -1)[:, :k].double()
+    g = torch.arange(k, device=DEV) // group
+    d = (codes - (8.0 if z is None else z.double()[:, g])) * s.double()[:, g]
+    return torch.stack([(row[None, :] * d).sum(1) for row in x.double()])
+
+
+# rows for each form: streaming with K over the waves and not, the tiles that split K, the pipelined ones
+FORMS = [(1, 300), (2, 40), (4, 300), (1, 70000), (3, 70000), (9, 300), (12, 9000), (30, 300), (64, 20000), (100, 33000)]
+
+
+@pytest.mark.parametrize("m,n", FORMS)
+@pytest.mark.parametrize("k,group", [(96, 32), (301, 64), (1100, 128), (640, 640)])
+def test_infinite_activations_have_the_value_of_the_definition(q, m, n, k, group):
+    """inf (code - zero) scale is inf, -inf, or NaN where code = zero; opposite infinities and NaN are NaN; the other rows
+    stay exact."""
+    w, s, z, x = random_operands(m + n + k, m, n, k, group, k != 301, True)
+    inf = float("inf")
+    x[0, k // 2] = inf
+    if m > 2:
+        x[1, 0], x[2, k - 1] = -inf, float("nan")
+    if m > 8:
+        x[8, 3], x[8, k - 2] = inf, -inf
+        x[m - 1, k - 1] = -inf
+    show("int4 infinite", m, n, k, group)
+    for dt in (torch.float32, torch.bfloat16):
+        out = q.int4_gemm(w, s, x, w_zero=z, group_size=group, out_dtype=dt)
+        rows = [i for i in (0, 1, 2, 3, 8, m - 1) if i < m]
+        assert equal_or_nan(out[rows], defined64(w, s, z, x[rows], group))
+
+
+@pytest.mark.parametrize("m,n", FORMS)
+@pytest.mark.parametrize("k,group", [(96, 32), (301, 64), (1100, 128)])
+def test_sums_beyond_float32_in_between(q, m, n, k, group):
+    """Activations of up to 2^126 and scales of 2^-23 .. 2^-20: sum x code leaves float32's range, the result does not."""
+    w, s, z, x = random_operands(m + n + k + 1, m, n, k, group, True, True)
+    x, s = x * 2.0 ** 124, s * 2.0 ** -20
+    show("int4 large activations", m, n, k, group)
+    ref = plain64(w, s, z, x, group)
+    assert bool((x.double().abs().sum(1) * 15 > 3.5e38).all()) and bool((ref.abs() < 3e38).all())
+    for dt in (torch.float32, torch.bfloat16):
+        assert torch.equal(q.int4_gemm(w, s, x, w_zero=z, group_size=group, out_dtype=dt), ref.to(dt))
+
+
+@pytest.mark.parametrize("m,n", [(1, 300), (3, 70000), (12, 300), (100, 33000)])
+def test_infinite_activations_through_the_epilogue(q, m, n):
+    """The residual is the output itself: each of its elements is read before it is written."""
+    k, group = 256, 64
+    w, s, z, x = random_operands(m + n + 2, m, n, k, group, True, True)
+    if m > 1:
+        x[0] *= 2.0 ** 124  # sums beyond float32 in between, all partial results exact
+    x[m - 1, 7] = float("inf")
+    s *= 2.0 ** -20
+    bias = torch.randint(-8, 9, (n,), device=DEV).bfloat16()
+    out = torch.randint(-8, 9, (m, n), device=DEV).float()
+    rows = sorted({0, m // 2, m - 1})
+    want = 0.5 * defined64(w, s, z, x[rows], group).float() + bias.float() + out[rows]
+    show("int4 infinite epilogue", m, n)
+    q.int4_gemm(w, s, x, w_zero=z, group_size=group, out=out, out_dtype=torch.float32, alpha=0.5, bias=bias, residual=out)
+    near = torch.isfinite(want)
+    assert equal_or_nan(torch.where(near, 0.0, out[rows]), torch.where(near, 0.0, want))
+    # three roundings of float32 in 0.5 v + bias + residual, each of values below |v| + 16
+    assert bool(((out[rows] - want)[near].abs() <= 4 * 2.0 ** -24 * (want[near].abs() + 32)).all())
+
+
+@pytest.mark.parametrize("rows,n", [(2, 272), (16, 272), (16, 9000), (70, 272)])
+@pytest.mark.parametrize("k,group", [(96, 32), (301, 64), (1100, 128), (640, 640)])
+def test_grouped_infinite_and_large_activations(q, rows, n, k, group):
+    e, counts = 4, [rows, 0, rows + 1, 1, 2 * rows, rows]
+    ids = [3, 0, 1, 2, -1, 0]
+    offs = np.concatenate([[0], np.cumsum(counts)])
+    t = int(offs[-1])
+    w, s, z, x = random_operands(rows + n + k, t, e * n, k, group, True, True)
+    w, s, z = w.view(e, n, -1), s.view(e, n, -1) * 2.0 ** -20, z.view(e, n, -1)
+    x[::3] *= 2.0 ** 124
+    x[1::5, k // 3] = float("inf")
+    x[t - 1, k - 1] = float("-inf")
+    show("int4 grouped infinite", rows, n, k, group)
+    for dt in (torch.float32, torch.bfloat16):
+        out = q.int4_grouped_gemm(w, s, x, dev(offs.astype(np.int32)), dev(np.asarray(ids, np.int32)), w_zero=z,
+                                  group_size=group, out_dtype=dt)
+        for i, (b, c) in enumerate(zip(offs[:-1], offs[1:])):
+            if c > b:
+                want = defined64(w[ids[i]], s[ids[i]], z[ids[i]], x[b:c], group) if ids[i] >= 0 else \
+                    torch.zeros((c - b, n), device=DEV)
+                assert equal_or_nan(out[b:c], want)

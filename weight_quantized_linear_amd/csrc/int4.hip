@@ -122,6 +122,53 @@ struct Int4Args {
 
 __device__ __forceinline__ float zero_at(const Int4Args& a, int64_t i) { return a.zero ? float(a.zero[i]) : 8.f; }
 
+// How the arguments of every kernel here begin.
+struct Int4Head {
+  Int4Args a;
+  const uint16_t* x;
+};
+
+// One output by the definition, sum_k x[k] (code - zero) scale, in float64: what a result that is not finite is
+// replaced with.  The factored sum has no finite value where sum x code or zero sum x passes float32's range,
+// and is inf - inf = NaN wherever an activation is infinite; here only the result's own value counts.
+// m: row of x, n: row of the weights (of all experts).  One lane walks K, which costs nothing where all results
+// are finite, and it stops at the first NaN (M = 500, N = 14336, K = 4096: 108 us a call of its own, 188 if all x is
+// NaN, 363 with one infinity, 8 ms with one in every row).  The operands are
+// read from the kernel's arguments anew: kept for this from the start, they took 13 scalar
+// registers from the tiles that have none to spare.
+__device__ __forceinline__ float int4_defined(int64_t m, int64_t n, int64_t K) {
+  uint64_t args = reinterpret_cast<uint64_t>(__builtin_amdgcn_kernarg_segment_ptr());
+  asm volatile("" : "+s"(args));
+  const auto* const head = reinterpret_cast<const __attribute__((address_space(4))) Int4Head*>(args);
+  const int64_t row_bytes = head->a.row_bytes, groups = head->a.groups;
+  const int shift = head->a.shift;
+  const uint8_t* const w = head->a.w + n * row_bytes;
+  const uint16_t* const scale = head->a.scale + n * groups;
+  const uint8_t* const zeros = head->a.zero ? head->a.zero + n * groups : nullptr;
+  const uint16_t* const x = head->x + m * K;
+  double sum = 0.0;
+  for (int64_t k = 0; k < K && sum == sum; k += 32) {  // 32 values lie in one group
+    const int64_t g = k >> shift;
+    const int left = int(K - k);
+    const u32x4 c = left >= 31 ? ldw16(w + (k >> 1)) : ld_bytes(w + (k >> 1), (left + 1) >> 1);
+    const float zero = zeros ? float(zeros[g]) : 8.f;
+    double part = 0.0;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const uint16_t* const p = x + k + 8 * t;
+      const u32x4 v = left >= 8 * t + 8 ? ldx16(p) : ld_halves(p, left - 8 * t);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float xi = (i & 1) ? bf16hi(v[i / 2]) : bf16lo(v[i / 2]);
+        part = fma(double(xi), double(float((c[t] >> (4 * i)) & 15u) - zero), part);
+      }
+    }
+    sum = fma(part, double(bf16_to_f32(scale[g])), sum);
+  }
+  return float(sum);
+}
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) < INFINITY; }
+
 constexpr int kStrip = 128;  // values of k that the four quarters of a wave take with one 16-byte load each
 
 // 4x4 transpose of dwords between register index and lane quarter.
@@ -251,10 +298,11 @@ __device__ __forceinline__ void pick_scale(const StreamScales<SH>& o, int u, int
   }
 }
 
-// store(m, n, value): m < rows, n relative to the block's first row of weights.
-template <int M, int NT, int WN, int WK, int SH, typename Store>
+// store(m, n, value): m < rows, n relative to the block's first row of weights; defined(m, n): the value of a result
+// that is not finite.
+template <int M, int NT, int WN, int WK, int SH, typename Store, typename Defined>
 __device__ __forceinline__ void int4_stream_tile(char* lds, const Int4Args& a, const uint16_t* __restrict__ x, int rows,
-                                                 int64_t N, int64_t K, int64_t n0, Store&& store) {
+                                                 int64_t N, int64_t K, int64_t n0, Store&& store, Defined&& defined) {
   using L = StreamLayout<M, NT, WN, WK>;
   const int thread = own_thread();
   const int lane = thread & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(thread / kWave);
@@ -408,14 +456,34 @@ __device__ __forceinline__ void int4_stream_tile(char* lds, const Int4Args& a, c
       float v = red[(w * WK * NT + i) * kVals + m * 16 + n];
 #pragma unroll
       for (int o = 1; o < WK; ++o) v += red[((w * WK + o) * NT + i) * kVals + m * 16 + n];
-      store(m, (w * NT + i) * 16 + n, v);
+      const int at = (w * NT + i) * 16 + n;
+      if (!finite(v) && n0 + at < N) v = defined(m, at);
+      store(m, at, v);
     }
   } else {
+    float mine[NT], sum = 0.f;  // quarter m takes row m
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < NT; ++i) {
+      mine[i] = acc[i][0];
 #pragma unroll
-      for (int m = 0; m < M; ++m)
-        if (quarter == m && m < rows) store(m, (wn * NT + i) * 16 + ln, acc[i][m]);
+      for (int m = 1; m < M; ++m) mine[i] = quarter == m ? acc[i][m] : mine[i];
+      sum = fmaf(mine[i], 0.f, sum);
+    }
+    if (quarter >= rows) return;
+    const int n = wn * NT * 16 + ln;
+    if (__ballot(sum != sum) == 0) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) store(quarter, n + i * 16, mine[i]);
+      return;
+    }
+#pragma unroll 1
+    for (int i = 0; i < NT; ++i) {  // results that are not finite among them
+      float v = mine[0];
+#pragma unroll
+      for (int j = 1; j < NT; ++j) v = i == j ? mine[j] : v;
+      if (!finite(v) && n0 + n + i * 16 < N) v = defined(quarter, n + i * 16);
+      store(quarter, n + i * 16, v);
+    }
   }
 }
 
@@ -427,7 +495,7 @@ __global__ __launch_bounds__(64 * WN * WK) void int4_stream_kernel(Int4Args a, c
   const int64_t n0 = int64_t(blockIdx.x) * (16 * NT * WN);
   int4_stream_tile<M, NT, WN, WK, SH>(lds, a, x, int(rows), N, K, n0, [&](int m, int n, float v) {
     if (n0 + n < N) store_epi(out, m, n0 + n, N, v, alpha, out_bf16, epi);
-  });
+  }, [&](int m, int n) { return int4_defined(m, n0 + n, K); });
 }
 
 // ---------------------------------------------------------------- matrix-core tile
@@ -495,11 +563,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p) {
 // GS: MFMA steps per group inside a strip (1, 2, 4; 4 also for larger groups).
 // The waves share nothing until they add their tiles, so that none waits for another: this is
 // the form for few rows, where a tile's time is the memory's answer.
-// store(m, n, value): m relative to the tile's first row.  Every thread of the
-// block calls it; the block's LDS is free when it begins.
-template <int MT, int NT, int WK, int GS, typename Store>
+// store(m, n, value): m and n relative to the tile; defined(m, n): the value of a result that is not finite.  Every
+// thread of the block calls it; the block's LDS is free when it begins.
+template <int MT, int NT, int WK, int GS, typename Store, typename Defined>
 __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const uint16_t* __restrict__ x, int64_t rows,
-                                          int64_t N, int64_t K, int64_t n0, Store&& store) {
+                                          int64_t N, int64_t K, int64_t n0, Store&& store, Defined&& defined) {
   using L = Int4Tile<MT, NT, 1, WK>;
   constexpr int G = 4 / GS;  // groups per strip
   const int lane = threadIdx.x & (kWave - 1), wk = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -717,7 +785,7 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
   }
 
   // Add the waves' tiles in wave order: each wave leaves its tile in LDS
-  // (one 16-byte store per lane and 16x16 tile) and takes every WK-th one.
+  // (one 16-byte store per lane and 16x16 tile) and takes one.
   __syncthreads();
   v4f* red = reinterpret_cast<v4f*>(lds);
 #pragma unroll
@@ -725,18 +793,27 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
 #pragma unroll
     for (int i = 0; i < NT; ++i) red[((wk * MT + mt) * NT + i) * 64 + lane] = acc[mt][i];
   __syncthreads();
+  static_assert(MT * NT <= WK, "a 16x16 tile per wave at most");
+  if (wk >= MT * NT) return;
+  v4f v = red[wk * 64 + lane];
 #pragma unroll
-  for (int q = 0; q < MT * NT; ++q) {
-    if (q % WK != wk) continue;
-    v4f v = red[q * 64 + lane];
+  for (int o = 1; o < WK; ++o) {
+    const v4f b = red[(o * MT * NT + wk) * 64 + lane];
 #pragma unroll
-    for (int o = 1; o < WK; ++o) {
-      const v4f b = red[(o * MT * NT + q) * 64 + lane];
+    for (int r = 0; r < 4; ++r) v[r] += b[r];
+  }
+  const int m = (wk / NT) * 16 + quarter * 4, n = (wk % NT) * 16 + ln;
+  const float sum = fmaf(v[0], 0.f, fmaf(v[1], 0.f, fmaf(v[2], 0.f, v[3] * 0.f)));
+  if (__ballot(sum != sum) == 0) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] += b[r];
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) store((q / NT) * 16 + quarter * 4 + r, (q % NT) * 16 + ln, v[r]);
+    for (int r = 0; r < 4; ++r) store(m + r, n, v[r]);
+    return;
+  }
+#pragma unroll 1
+  for (int r = 0; r < 4; ++r) {  // results that are not finite among them
+    float f = r == 0 ? v[0] : r == 1 ? v[1] : r == 2 ? v[2] : v[3];
+    if (!finite(f) && m + r < rows && n0 + n < N) f = defined(m + r, n);
+    store(m + r, n, f);
   }
 }
 
@@ -751,49 +828,84 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
 struct TileOut {
   void* out;      // row 0, column 0
   int64_t rows, N, n0;
-  int64_t row0;   // of the epilogue's operands
+  int64_t row0;   // of the epilogue's operands and of x
+  int64_t wrow0;  // of the expert among the weights
   float alpha;
   int bf16;
-  const Epilogue* epi;  // null: none
+  Epilogue epi;
 
-  // put(m, n, v): m uniform and the first of 4 rows of quarter 0; n of lane 0.
-  template <int BM, typename F>
-  __device__ __forceinline__ void write(F&& each) const {
+  // acc[mt][i]: rows 16 mt .., columns wave_n + 16 i ..; K for the results that are not finite.
+  template <int MT, int NT>
+  __device__ __forceinline__ void write(const v4f (&acc)[MT][NT], int wave_n, int64_t K) const {
+    constexpr int BM = 16 * MT;
+    static_assert(MT * NT * 4 <= 64, "a bit per result of a lane");
     const int lane = threadIdx.x & (kWave - 1), ln = lane & 15, quarter = lane >> 4;
     const int64_t es = bf16 ? 2 : 4;
-    const bool plain = !(epi && epi->on) && int64_t(BM) * N * es < (int64_t(1) << 31);
+    const bool plain = !epi.on && int64_t(BM) * N * es < (int64_t(1) << 31);
+    float sum = 0.f;  // NaN if a result is not finite
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sum = fmaf(acc[mt][i][r], 0.f, sum);
     if (plain) {
       const int live = int(rows < BM ? rows : BM);
       char* const first = static_cast<char*>(out) + n0 * es;
-      const uint32_t line = uint32_t(N * es), lane_at = uint32_t(quarter * 4) * line + uint32_t(ln * es);
-      const int64_t width = N - n0;
-      each([&](int m, int n, v4f v) {
+      const uint32_t line = uint32_t(N * es), lane_at = uint32_t(quarter * 4) * line + uint32_t((wave_n + ln) * es);
+      const int64_t width = N - n0 - wave_n - ln;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int m = 16 * mt;
         const uint32_t bytes = m < live ? uint32_t(live - m) * line - uint32_t(n0 * es) : 0u;
         const __amdgpu_buffer_rsrc_t buf =
             __builtin_amdgcn_make_buffer_rsrc(first + int64_t(m) * line, 0, int(bytes), 0x00020000);
-        const uint32_t at = n + ln < width ? lane_at + uint32_t(n * es) : 0x80000000u;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float f = v[r] * alpha;
-          if (bf16)
-            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, static_cast<__bf16>(f)), buf,
-                                                  at + uint32_t(r) * line, 0, 0);
-          else
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f), buf, at + uint32_t(r) * line, 0, 0);
+        for (int i = 0; i < NT; ++i) {
+          const uint32_t at = 16 * i < width ? lane_at + uint32_t(16 * i * es) : 0x80000000u;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float f = acc[mt][i][r] * alpha;
+            if (bf16)
+              __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, static_cast<__bf16>(f)), buf,
+                                                    at + uint32_t(r) * line, 0, 0);
+            else
+              __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f), buf, at + uint32_t(r) * line, 0, 0);
+          }
         }
-      });
-      return;
-    }
-    each([&](int m, int n, v4f v) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t row = m + quarter * 4 + r, col = n0 + n + ln;
-        if (row >= rows || col >= N) continue;
-        float f = v[r] * alpha;
-        if (epi && epi->on) f = epi_apply(*epi, f, row0 + row, col);
-        store_out(out, row * N + col, f, 1.f, bf16);
       }
-    });
+    } else {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int64_t row = mt * 16 + quarter * 4 + r, col = n0 + wave_n + i * 16 + ln;
+            // The residual may be the output: a result that follows below is not stored before.
+            if (row < rows && col < N && finite(acc[mt][i][r])) put(row, col, acc[mt][i][r]);
+          }
+    }
+    if (__ballot(sum != sum) == 0) return;
+    uint64_t lost = 0;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) lost |= uint64_t(!finite(acc[mt][i][r])) << ((mt * NT + i) * 4 + r);
+    const int again = own_thread();
+    for (; lost; lost &= lost - 1) {
+      const int b = __builtin_ctzll(lost), tile = b >> 2;
+      const int64_t row = tile / NT * 16 + (again & 63) / 16 * 4 + (b & 3), col = n0 + wave_n + tile % NT * 16 + (again & 15);
+      if (row < rows && col < N) put(row, col, int4_defined(row0 + row, wrow0 + col, K));
+    }
+  }
+
+  __device__ __forceinline__ void put(int64_t row, int64_t col, float v) const {
+    float f = v * alpha;
+    if (epi.on) f = epi_apply(epi, f, row0 + row, col);
+    store_out(out, row * N + col, f, 1.f, bf16);
   }
 };
 
@@ -1101,12 +1213,7 @@ __device__ __forceinline__ void int4_pipe_tile(char* lds, const Int4Args& a, con
     for (int i = 0; i < NT; ++i) due[i] = zs[i];
     correct(lds + L::kSums + set * L::kSumBytes);
   }
-  to.write<16 * MT>([&](auto&& put) {
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int i = 0; i < NT; ++i) put(mt * 16, wave * 16 * NT + i * 16, acc[mt][i]);
-  });
+  to.write(acc, wave * 16 * NT, K);
 }
 
 template <int MT, int NT, int WN, int WK, int GS>
@@ -1123,12 +1230,12 @@ __global__ __launch_bounds__(64 * WN * WK) void int4_gemm_kernel(Int4Args a, con
   if (int64_t(blockIdx.x / 8) >= per || tile >= total) return;  // uniform over the block
   const int64_t m0 = tile % mtiles * L::kBM, n0 = tile / mtiles * L::kBN;
   if constexpr (WK == 1) {
-    const TileOut to{static_cast<char*>(out) + m0 * N * (out_bf16 ? 2 : 4), M - m0, N, n0, m0, alpha, out_bf16, &epi};
+    const TileOut to{static_cast<char*>(out) + m0 * N * (out_bf16 ? 2 : 4), M - m0, N, n0, m0, 0, alpha, out_bf16, epi};
     int4_pipe_tile<MT, NT, WN, GS>(lds, a, x + m0 * K, M - m0, N, K, n0, to);
   } else {
     int4_tile<MT, NT, WK, GS>(lds, a, x + m0 * K, M - m0, N, K, n0, [&](int m, int n, float v) {
       if (m0 + m < M && n0 + n < N) store_epi(out, m0 + m, n0 + n, N, v, alpha, out_bf16, epi);
-    });
+    }, [&](int m, int n) { return int4_defined(m0 + m, n0 + n, K); });
   }
 }
 
@@ -1137,7 +1244,7 @@ __global__ __launch_bounds__(64 * WN * WK) void int4_gemm_kernel(Int4Args a, con
 // writes zeros, an empty group nothing.  Every block builds the prefix sum of
 // the groups' row tiles in LDS (cum[z] = row tiles of groups 0 .. z - 1) and walks its XCD's
 // contiguous part of the (group, row tile, column tile) list.
-// f(expert's operands, m0, rows from m0 to the group's end, n0).
+// f(expert's operands, the expert, m0, rows from m0 to the group's end, n0).
 template <int BM, int BN, int THREADS, typename F>
 __device__ __forceinline__ void walk_groups(int* cum, const Int4Args& a, const uint32_t* __restrict__ a_offsets,
                                             const int32_t* __restrict__ expert_ids, void* __restrict__ out, int out_bf16,
@@ -1200,7 +1307,7 @@ __device__ __forceinline__ void walk_groups(int* cum, const Int4Args& a, const u
     b.scale += e * N * a.groups;
     if (b.zero) b.zero += e * N * a.groups;
     __syncthreads();  // the previous tile's buffers are free
-    f(b, m0, left, n0);
+    f(b, e, m0, left, n0);
   }
 }
 
@@ -1214,8 +1321,8 @@ __global__ __launch_bounds__(64 * WN) void int4_grouped_kernel(Int4Args a, const
   extern __shared__ __attribute__((aligned(16))) char lds[];
   walk_groups<L::kBM, L::kBN, L::kThreads>(
       reinterpret_cast<int*>(lds + L::kLds), a, a_offsets, expert_ids, out, out_bf16, groups, T, N, E,
-      [&](const Int4Args& b, int64_t m0, int64_t left, int64_t n0) {
-        const TileOut to{static_cast<char*>(out) + m0 * N * (out_bf16 ? 2 : 4), left, N, n0, m0, 1.f, out_bf16, nullptr};
+      [&](const Int4Args& b, int64_t e, int64_t m0, int64_t left, int64_t n0) {
+        const TileOut to{static_cast<char*>(out) + m0 * N * (out_bf16 ? 2 : 4), left, N, n0, m0, e * N, 1.f, out_bf16, Epilogue{}};
         int4_pipe_tile<MT, NT, WN, GS>(lds, b, x + m0 * K, left, N, K, n0, to);
       });
 }
@@ -1236,10 +1343,10 @@ __global__ __launch_bounds__(64 * WN, kStreamWaves) void int4_grouped_stream_ker
   extern __shared__ __attribute__((aligned(16))) char lds[];
   walk_groups<4, 16 * NT * WN, 64 * WN>(
       reinterpret_cast<int*>(lds + L::kLds), a, a_offsets, expert_ids, out, out_bf16, groups, T, N, E,
-      [&](const Int4Args& b, int64_t m0, int64_t left, int64_t n0) {
+      [&](const Int4Args& b, int64_t e, int64_t m0, int64_t left, int64_t n0) {
         int4_stream_tile<4, NT, WN, 1, SH>(lds, b, x + m0 * K, int(left < 4 ? left : 4), N, K, n0, [&](int m, int n, float v) {
           if (n0 + n < N) store_out(out, (m0 + m) * N + n0 + n, v, 1.f, out_bf16);
-        });
+        }, [&](int m, int n) { return int4_defined(m0 + m, e * N + n0 + n, K); });
       });
 }
 
