@@ -160,3 +160,47 @@ def test_grouped_infinite_and_large_activations(q, rows, n, k, group):
                 want = defined64(w[ids[i]], s[ids[i]], z[ids[i]], x[b:c], group) if ids[i] >= 0 else \
                     torch.zeros((c - b, n), device=DEV)
                 assert equal_or_nan(out[b:c], want)
+
+
+def test_offsets_that_fall_count_every_row_once(q):
+    """Offsets that fall and rise again: 8192 groups would cover all 17 million rows each.  Only the first does; the result of
+    the others is undefined, the reads and writes are not."""
+    t, groups, e, n, k = 2 ** 24 + 300000, 16384, 3, 4, 2
+    w, s, z, x = random_operands(77, 1000, e * n, k, 32, True, True)
+    w, s, z = w.view(e, n, -1), s.view(e, n, -1), z.view(e, n, -1)
+    x = x.repeat(t // 1000 + 1, 1)[:t].contiguous()
+    offs = torch.tensor([0, -1], dtype=torch.int32, device=DEV).repeat(groups // 2 + 1)[:groups + 1].contiguous()
+    ids = torch.full((groups,), 1, dtype=torch.int32, device=DEV)
+    buf = torch.full((t + 2000, n), 7.0, dtype=torch.bfloat16, device=DEV)
+    show("int4 falling offsets", t, groups)
+    q.int4_grouped_gemm(w, s, x, offs, ids, w_zero=z, group_size=32, out=buf[1000:1000 + t])
+    assert torch.all(buf[:1000] == 7.0) and torch.all(buf[1000 + t:] == 7.0)
+    want = plain64(w[1], s[1], z[1], x[:1000], 32).bfloat16()
+    assert torch.equal(buf[1000:1000 + t], want.repeat(t // 1000 + 1, 1)[:t])
+
+
+@pytest.mark.parametrize("t,groups", [(40, 9), (300, 130), (3000, 200), (9000, 70)])
+def test_offsets_in_any_order_stay_inside(q, t, groups):
+    """Groups that begin behind every earlier end are computed, whatever the other offsets hold; rows behind T stay."""
+    rng = np.random.default_rng([31, t, groups])
+    e, n, k = 4, 80, 130
+    w, s, z, x = random_operands(t + groups, t, e * n, k, 64, True, True)
+    w, s, z = w.view(e, n, -1), s.view(e, n, -1), z.view(e, n, -1)
+    offs = np.sort(rng.integers(0, t + 1, groups + 1))
+    offs[groups // 2] = 2 ** 32 - 1
+    offs[[1, groups // 3]] = offs[[groups // 3, 1]]
+    ids = rng.integers(-1, e, groups).astype(np.int32)
+    buf = torch.full((t + 600, n), 7.0, device=DEV)
+    show("int4 offsets in any order", t, groups)
+    q.int4_grouped_gemm(w, s, x, dev(offs.astype(np.uint32).view(np.int32)), dev(ids), w_zero=z, group_size=64,
+                        out=buf[300:300 + t], out_dtype=torch.float32)
+    assert torch.all(buf[:300] == 7.0) and torch.all(buf[300 + t:] == 7.0)
+    top, covered = 0, np.zeros(t, int)
+    spans = [(min(int(a), t), min(int(b), t)) for a, b in zip(offs[:-1], offs[1:])]
+    for b, c in spans:
+        covered[b:c] += 1
+    for i, (b, c) in enumerate(spans):
+        if c > b and b >= top and covered[b:c].max() == 1:
+            want = plain64(w[ids[i]], s[ids[i]], z[ids[i]], x[b:c], 64).float() if ids[i] >= 0 else torch.zeros((c - b, n), device=DEV)
+            assert torch.equal(buf[300 + b:300 + c], want)
+        top = max(top, c)

@@ -261,4 +261,54 @@ __device__ __forceinline__ float wave_sum(float v) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
+// ---------------------------------------------------------------- ragged groups
+
+// Row tiles of BM rows in front of every group, cum[0 .. groups], made by the block's first
+// wave: group z owns the rows a_offsets[z] .. a_offsets[z + 1] - 1, clipped to T.  A group that begins
+// before the end of an earlier one gets no tile.  Offsets that never decrease leave no such group; where they
+// do, groups could cover the same rows thousands of times, and the count of their tiles pass
+// 32 bits and with it every bound that the walk over the tiles keeps.  So the tiles are at most
+// T / BM + groups, whatever the offsets hold.
+template <int BM>
+__device__ __forceinline__ void count_group_tiles(int* cum, const uint32_t* __restrict__ a_offsets, int64_t groups,
+                                                  int64_t T) {
+  const int lane = threadIdx.x;
+  const uint32_t limit = uint32_t(T < 0xFFFFFFFFll ? T : 0xFFFFFFFFll);
+  int carry = 0;
+  uint32_t top = 0;  // the highest end so far
+  for (int64_t z0 = 0; z0 <= groups; z0 += kWave) {
+    const int64_t z = z0 + lane;
+    uint32_t b = 0, e = 0;
+    if (z < groups) {
+      b = a_offsets[z];
+      e = a_offsets[z + 1];
+      b = b < limit ? b : limit;
+      e = e < limit ? e : limit;
+    }
+    uint32_t before = top, ends = e;
+    int last = int(groups - 1 - z0 < kWave - 1 ? groups - 1 - z0 : kWave - 1);
+    if (__ballot(e < b) != 0) {  // running maximum of the ends; rising ends are their own
+#pragma unroll
+      for (int d = 1; d < kWave; d <<= 1) {
+        const uint32_t o = __shfl_up(ends, d, kWave);
+        if (lane >= d) ends = ends > o ? ends : o;
+      }
+      const uint32_t o = __shfl_up(ends, 1, kWave);
+      if (lane > 0) before = before > o ? before : o;
+      last = kWave - 1;
+    }
+    const uint32_t highest = last >= 0 ? __builtin_amdgcn_readlane(ends, last) : 0u;
+    top = top > highest ? top : highest;
+    const int t = e > b && b >= before ? int((int64_t(e - b) + BM - 1) / BM) : 0;
+    int incl = t;  // inclusive prefix sum over the wave
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+      const int o = __shfl_up(incl, d, kWave);
+      if (lane >= d) incl += o;
+    }
+    if (z <= groups) cum[z] = carry + incl - t;
+    carry += __shfl(incl, kWave - 1, kWave);
+  }
+}
+
 }  // namespace qlinear

@@ -1256,27 +1256,7 @@ __device__ __forceinline__ void walk_groups(int* cum, const Int4Args& a, const u
     start = b;
     rows = e > b ? e - b : 0;
   };
-  if (threadIdx.x < kWave) {
-    const int lane = threadIdx.x;
-    int carry = 0;
-    for (int64_t z0 = 0; z0 <= groups; z0 += kWave) {
-      const int64_t z = z0 + lane;
-      int t = 0;
-      if (z < groups) {
-        int64_t start, rows;
-        span(z, start, rows);
-        t = int((rows + BM - 1) / BM);
-      }
-      int incl = t;
-#pragma unroll
-      for (int d = 1; d < kWave; d <<= 1) {
-        const int o = __shfl_up(incl, d, kWave);
-        if (lane >= d) incl += o;
-      }
-      if (z <= groups) cum[z] = carry + incl - t;
-      carry += __shfl(incl, kWave - 1, kWave);
-    }
-  }
+  if (threadIdx.x < kWave) count_group_tiles<BM>(cum, a_offsets, groups, T);
   __syncthreads();
   const int64_t ntiles = (N + BN - 1) / BN, work = int64_t(__builtin_amdgcn_readfirstlane(cum[groups])) * ntiles;
   const int64_t xcd = blockIdx.x % 8, per_xcd = gridDim.x / 8;  // gridDim.x is a multiple of 8
