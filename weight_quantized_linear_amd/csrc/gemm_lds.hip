@@ -796,27 +796,7 @@ __global__ __launch_bounds__(64 * NW) void grouped_gemm_kernel(const uint16_t* _
     start = b;
     rows = e > b ? e - b : 0;
   };
-  if (threadIdx.x < 64) {
-    const int lane = threadIdx.x;
-    int carry = 0;
-    for (int64_t z0 = 0; z0 <= G; z0 += 64) {
-      const int64_t z = z0 + lane;
-      int t = 0;
-      if (z < G) {
-        int64_t st, rows;
-        group_span(z, st, rows);
-        t = int((rows + BM - 1) / BM);
-      }
-      int incl = t;  // inclusive prefix sum over the wave
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(incl, d, 64);
-        if (lane >= d) incl += o;
-      }
-      if (z <= G) cum[z] = carry + incl - t;
-      carry += __shfl(incl, 63, 64);
-    }
-  }
+  if (threadIdx.x < 64) count_group_tiles<BM>(cum, a_offsets, G, T);
   __syncthreads();
   const int64_t n_tiles = (N + BN - 1) / BN;
   const int64_t work = int64_t(cum[G]) * n_tiles;
@@ -1164,27 +1144,7 @@ __global__ __launch_bounds__(64 * NW) void int8_grouped_kernel(
     start = lo;
     rows = hi > lo ? hi - lo : 0;
   };
-  if (threadIdx.x < 64) {
-    const int lane = threadIdx.x;
-    int carry = 0;
-    for (int64_t z0 = 0; z0 <= G; z0 += 64) {
-      const int64_t z = z0 + lane;
-      int t = 0;
-      if (z < G) {
-        int64_t st, rows;
-        group_span(z, st, rows);
-        t = int((rows + BM - 1) / BM);
-      }
-      int incl = t;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(incl, d, 64);
-        if (lane >= d) incl += o;
-      }
-      if (z <= G) cum[z] = carry + incl - t;
-      carry += __shfl(incl, 63, 64);
-    }
-  }
+  if (threadIdx.x < 64) count_group_tiles<BM>(cum, a_offsets, G, T);
   __syncthreads();
   const int64_t n_tiles = (N + BN - 1) / BN;
   const int64_t work = int64_t(cum[G]) * n_tiles;
