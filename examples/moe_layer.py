@@ -23,10 +23,11 @@ import weight_quantized_linear_amd as q  # noqa: E402
 
 
 def quantize_int4(w: torch.Tensor, group: int):
-    """Codes, scales and zero points of [..., N, K] weights, one pair per `group` values of k."""
+    """Codes, scales and zero points of [..., N, K] weights, one pair per `group` values of k.
+    A group's range takes in 0, which the zero point 0 .. 15 has to stand for."""
     k = w.shape[-1]
     g = w.float().unflatten(-1, (k // group, group))
-    low, high = g.amin(-1), g.amax(-1)
+    low, high = g.amin(-1).clamp(max=0.0), g.amax(-1).clamp(min=0.0)
     scale = ((high - low) / 15.0).clamp(min=1e-8).bfloat16()
     zero = (-low / scale.float()).round().clamp(0, 15)
     codes = (g / scale.float()[..., None] + zero[..., None]).round().clamp(0, 15).flatten(-2).to(torch.uint8)
