@@ -490,8 +490,9 @@ int qlinear_int4_gemm(const void* w_packed, const void* w_scale, const void* w_z
  * w_scale: bfloat16 and w_zero: uint8 [num_experts, N, G]), and the groups of
  * rows of qlinear_fp8_grouped_gemm.  a_offsets, expert_ids, num_groups,
  * max_tokens_per_group, inactive / empty groups (zeros / nothing), untouched
- * rows, preconditions and bounds behaviour: exactly as there.  T = 0 is
- * allowed and does nothing.
+ * rows, preconditions and bounds behaviour: as there (the launch is sized by T
+ * and num_groups, so max_tokens_per_group is checked and not used further).
+ * T = 0 is allowed and does nothing.
  */
 int qlinear_int4_grouped_gemm(const void* w_packed, const void* w_scale, const void* w_zero,
                               const void* x, const uint32_t* a_offsets,

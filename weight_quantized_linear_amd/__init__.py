@@ -633,7 +633,8 @@ def int4_grouped_gemm(w_packed: torch.Tensor, w_scale: torch.Tensor, x: torch.Te
     a_offsets[z] .. a_offsets[z+1]-1 of x times D_e^T, e = expert_ids[z], D_e as in
     ``int4_gemm`` from the expert stack w_packed [E, N, (K + 1) / 2], w_scale and w_zero
     [E, N, ceil(K / group_size)].  Rows outside every group keep whatever ``out`` held
-    (a new ``out`` starts uninitialised)."""
+    (a new ``out`` starts uninitialised).  ``max_tokens_per_group`` is accepted as by the
+    other grouped calls and does not change the launch."""
     w, sc, zero, x, k, group = _int4_operands(w_packed, w_scale, w_zero, x, group_size, "E, ")
     _require(a_offsets, "a_offsets")
     _require(expert_ids, "expert_ids")

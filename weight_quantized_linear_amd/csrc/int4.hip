@@ -914,9 +914,11 @@ struct TileOut {
 // s + 1, moves its x from registers to the other LDS buffer, and loads strip s + 2.  WN waves
 // side by side along N, one barrier per strip.  (With these phases one after the other
 // the 128x256 tile took 2.9 us for a strip of which the matrix cores need 1.1.)
-// Bound by the latency of the LDS reads between two barriers, at 2 waves per SIMD: 128x256,
-// groups of 128, keeps the matrix cores busy for 30 % of the time and the vector ALU for 24 %.
-// M = 500, N = 14336, K = 4096: 104 us with groups of 64 (563 TFLOP/s), 90 with 128, 146 with 32.
+// Bound by what the 2 waves of a SIMD issue in turn: the vector ALU (decoding, and scaling, which
+// grows with the groups of a strip) and the matrix cores overlap little.  128x256 with groups of 128, 64, 32: ALU
+// busy for 38, 46, 56 % of the SIMDs' cycles, matrix cores for 39, 35, 31, LDS reads waited for by under 4 % of the
+// waves' cycles.  M = 500, N = 14336, K = 4096: 82, 98 (599 TFLOP/s), 121 us, calls behind each other
+// with the weights in the 256 MB cache.
 // With four strips' loads under way the smaller tiles gained nothing (64x256 58 us for 54).
 template <int MT, int NT, int WN, int GS>
 __device__ __forceinline__ void int4_pipe_tile(char* lds, const Int4Args& a, const uint16_t* __restrict__ x,
@@ -1308,7 +1310,7 @@ __global__ __launch_bounds__(64 * WN) void int4_grouped_kernel(Int4Args a, const
 }
 
 // Groups of few rows: tiles of 4 rows through the streaming form, 3 waves per SIMD: with 4, 50 to
-// 150 bytes of a lane's step went to memory (64 experts, N = 1536, K = 2048, groups of 128:
+// 150 bytes of a lane's step went to memory (64 experts, N = 1536, K = 2048, groups of 128, no weights in the caches:
 // 64 rows 35 us, with 3 29; 256 rows 44 and 40; with 3 and a fourth block per CU 30 and 48).
 constexpr int kStreamWaves = 3;
 
@@ -1464,18 +1466,21 @@ hipError_t launch_int4_gemm(const uint8_t* w, const uint16_t* scale, const uint8
     return gemm_cfg<1, 2, 1, 4>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
   }
   // Above, the tile with the least time for the CU that gets most of them.  A tile's time
-  // hardly depends on how many other CUs have one: for K = 4096, groups of 64, in us,
-  //   64x128 38 (M = 500, N = 4096: 256 tiles 39; M = 200, N = 14336: 448 of them 74)
-  //   32x128 28 (M = 250, N = 4096: 29; M = 500: 55), 64x256 64, 128x128 62, 128x256 112
-  //   (M = 500, N = 14336: 112; with 128x128 tiles 124, 64x256 128, 64x128 150).
+  // hardly depends on how many other CUs have one: for K = 4096, groups of 64, calls behind each other, in us,
+  //   64x128 36 (M = 500, N = 4096: 256 tiles 36; M = 200, N = 14336: 448 of them 70)
+  //   32x128 28 (M = 250, N = 4096: 28; M = 500: 51), 64x256 62, 128x128 60, 128x256 97
+  //   (M = 500, N = 14336: 98; with 128x128 tiles 120, 64x256 123, 64x128 138;
+  //   M = 2048, N = 14336: 381, 420, 430, 503).
   // Those of 32x32 and 32x16 split K over their waves and share a CU: 11 (9) for the first, and
-  // as much for each more on average (M = 64, N = 4096: 13; M = 64, N = 14336: 40).
+  // as much for each more on average (M = 64, N = 4096: 15; M = 64, N = 14336: 38).
+  // Groups of 128 take 0.82 to 0.96 of these times, groups of 32 1.18 to 1.36, and K = 1024 and 14336 a third and 3.3 times:
+  // the same tile is the fastest for each of them at M = 500, N = 4096 and 14336.
   struct Tile {
     int bm, bn, us;
     bool shared;
   };
-  constexpr Tile kTiles[] = {{32, 16, 9, true},    {32, 32, 11, true},    {32, 128, 28, false}, {64, 128, 38, false},
-                             {64, 256, 64, false}, {128, 128, 62, false}, {128, 256, 112, false}};
+  constexpr Tile kTiles[] = {{32, 16, 9, true},    {32, 32, 11, true},    {32, 128, 28, false}, {64, 128, 36, false},
+                             {64, 256, 62, false}, {128, 128, 60, false}, {128, 256, 97, false}};
   int best = 0;
   double least = 0.0;
   for (int i = 0; i < int(sizeof(kTiles) / sizeof(Tile)); ++i) {
@@ -1503,12 +1508,12 @@ hipError_t launch_int4_grouped(const uint8_t* w, const uint16_t* scale, const ui
                                int64_t G, int64_t E, int64_t T, int64_t N, int64_t K, int64_t group, int num_cus,
                                hipStream_t s) {
   const Int4Args a = make_args(w, scale, zero, K, group);
-  // By the rows a group has on average (64 experts, N = 1536, K = 2048, groups of 128, unless
-  // said), in us: to 6 the streaming form (64 rows: 29, 32x256 54; 384 rows: 50 and 58; 768 rows: 85
-  // and 57), to 32 tiles of 32x256 (1024 rows: 57, 32x128 66, 64x256 68), or of 32x128 where 32x256 would
-  // leave CUs without any (8 experts, N = K = 4096, groups of 64, 96 rows: 37 and 60), above of
-  // 64x256 (4096 rows: 102, 32x256 109, 128x256 128; those 8 experts, 512 rows: 74, 64x128 83,
-  // 128x256 128; 4096 rows: 338, 128x256 348).
+  // By the rows a group has on average (64 experts, N = 1536, K = 2048, groups of 128, counts spread by Zipf 0.5, unless
+  // said; calls behind each other, about half of the weights in the 256 MB cache), in us: to 6 the streaming form (64
+  // rows: 23, 32x256 51; 384 rows: 41 and 51; 768 rows: 75 and 51), to 32 tiles of 32x256 (1024 rows: 51, 32x128 56,
+  // 64x256 62; 2048 rows: 74, 70, 64), or of 32x128 where 32x256 would leave CUs without any (8 experts, N = K = 4096,
+  // groups of 64, 96 rows: 31 and 52), above of 64x256 (4096 rows: 90, 32x256 97, 32x128 107; those 8 experts, 512 rows: 66,
+  // 32x128 86, 32x256 103; 4096 rows: 318, 32x256 446).
   const bool few = ((T + 31) / 32 + std::min(G, T)) * ((N + 255) / 256) <= num_cus;
   // A block keeps the groups' prefix sums in LDS beside its tile: more groups take more launches.
   constexpr int64_t kMost = 16384;

@@ -84,7 +84,7 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 
 // L lanes per token (16, 32 or 64: the fewest that hold its E logits with at
 // most 16 each), so a wave takes up to 4 tokens; lane l of a token holds the R
-// logits e = l R .. l R + R - 1.  The kernel is bound by its vector instructions, and
+// logits e = l R .. l R + R - 1.  The kernel is bound by its vector instructions (87 % of the SIMDs' cycles), and
 // a pick costs the same ones however many tokens the wave holds: T = 16384, E = 256,
 // top 8, bfloat16 takes 9.0 us, 15.8 with one token per wave.
 
@@ -240,7 +240,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const void* __rest
 // are read, and every other gradient is 0.  Lane layout of the router; a row (the
 // chosen experts' gradients, or with renormalised weights the result) lies in LDS,
 // where the chosen lanes put what belongs to their experts.  T = 16384, E = 256, bfloat16:
-// 7.8 us, 2.2 TB/s; bound by the vector instructions of the softmax as the router is.
+// 7.8 us, 2.2 TB/s; bound by the vector instructions of the softmax, which fill 69 % of the SIMDs'
+// cycles while their CUs have work (the router's 87 %).
 template <int BF16, int L, int R>
 __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const void* __restrict__ logits,
                                                                        const int32_t* __restrict__ ids,
@@ -767,10 +768,10 @@ __global__ __launch_bounds__(256) void swiglu_kernel(const void* __restrict__ x,
   }
 }
 
-// Calls that move more than this go past the caches: above it the gather of 16384 tokens
-// (604 MB) took 102 us instead of 120 and the activation (302 MB) 59 instead of 62;
-// below it the next operator finds the rows in the 256 MB cache (a gradient of 126 MB:
-// 22.3 us, 23.1 past it).
+// Calls that move more than this go past the caches.  Above it: sort, gather and combine of 16384
+// tokens (604 MB each way) 231 us, 266 through the caches; a combine and its gradients (672 MB) 125 and 141; the
+// activation of 302 MB 46.5 and 50.7.  Below it the next operator finds the rows in the 256 MB cache (a
+// gradient of 126 MB: 20.4 us, 22.6 past it).
 constexpr int64_t kNtBytes = int64_t(160) << 20;
 
 template <typename F> hipError_t by_size(int64_t bytes, F&& go) {

@@ -286,7 +286,7 @@ int bf16_gemm_impl(const void* w, const void* x, void* out, int out_dtype, int64
 bool int4_group_ok(int64_t g, int64_t K) { return K < (int64_t(1) << 23) && (g >= K || (g >= 32 && (g & (g - 1)) == 0)); }
 
 // Limits of the expert calls: the router keeps a token's logits in one wave's
-// registers and pick j in lane j; slots and rows are int32.
+// registers and its picks in 64 places of LDS; slots and rows are int32.
 constexpr int64_t kMaxRouted = 1024, kMaxTopK = 64, kMaxSlots = std::numeric_limits<int32_t>::max();
 
 bool permute_sizes_ok(int64_t T, int64_t top_k, int64_t H) {
@@ -601,7 +601,7 @@ int qlinear_int4_grouped_gemm(const void* w_packed, const void* w_scale, const v
                               int64_t num_groups, int64_t max_tokens_per_group, int64_t num_experts, int64_t T,
                               int64_t N, int64_t K, int64_t group_size, void* stream) {
   if (!w_packed || !w_scale || !x || !a_offsets || !expert_ids || !out) return QLINEAR_ERR_INVALID_ARG;
-  // The kernel counts row tiles (at most T + num_groups) in int32.
+  // The kernel counts row tiles (at most T + num_groups, whatever the offsets) in int32.
   if (num_groups <= 0 || num_groups > 65535 || max_tokens_per_group < 0 || num_experts <= 0 || T < 0 ||
       T > (int64_t(1) << 30) || N <= 0 || K <= 0 || !int4_group_ok(group_size, K))
     return QLINEAR_ERR_INVALID_ARG;
