@@ -457,7 +457,7 @@ __device__ __forceinline__ void int4_stream_tile(char* lds, const Int4Args& a, c
 #pragma unroll
       for (int o = 1; o < WK; ++o) v += red[((w * WK + o) * NT + i) * kVals + m * 16 + n];
       const int at = (w * NT + i) * 16 + n;
-      if (!finite(v) && n0 + at < N) v = defined(m, at);
+      if (__builtin_expect(!finite(v) && n0 + at < N, 0)) v = defined(m, at);
       store(m, at, v);
     }
   } else {
@@ -471,7 +471,7 @@ __device__ __forceinline__ void int4_stream_tile(char* lds, const Int4Args& a, c
     }
     if (quarter >= rows) return;
     const int n = wn * NT * 16 + ln;
-    if (__ballot(sum != sum) == 0) {
+    if (__builtin_expect(__ballot(sum != sum) == 0, 1)) {
 #pragma unroll
       for (int i = 0; i < NT; ++i) store(quarter, n + i * 16, mine[i]);
       return;
@@ -804,7 +804,7 @@ __device__ __forceinline__ void int4_tile(char* lds, const Int4Args& a, const ui
   }
   const int m = (wk / NT) * 16 + quarter * 4, n = (wk % NT) * 16 + ln;
   const float sum = fmaf(v[0], 0.f, fmaf(v[1], 0.f, fmaf(v[2], 0.f, v[3] * 0.f)));
-  if (__ballot(sum != sum) == 0) {
+  if (__builtin_expect(__ballot(sum != sum) == 0, 1)) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) store(m + r, n, v[r]);
     return;
@@ -886,7 +886,7 @@ struct TileOut {
             if (row < rows && col < N && finite(acc[mt][i][r])) put(row, col, acc[mt][i][r]);
           }
     }
-    if (__ballot(sum != sum) == 0) return;
+    if (__builtin_expect(__ballot(sum != sum) == 0, 1)) return;
     uint64_t lost = 0;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
