@@ -20,6 +20,7 @@
 #include "launch.hpp"
 
 #include <algorithm>
+#include <cstddef>
 
 namespace qlinear {
 
@@ -122,24 +123,29 @@ struct Int4Args {
 
 __device__ __forceinline__ float zero_at(const Int4Args& a, int64_t i) { return a.zero ? float(a.zero[i]) : 8.f; }
 
-// How the arguments of every kernel here begin.
+// How the arguments of every kernel here begin, and where they lie.  The address exists in
+// a kernel's own body only: each kernel takes it there and hands it on, so that what uses it may also be a
+// function of its own (where it does not exist, and reading through it faults).
 struct Int4Head {
   Int4Args a;
   const uint16_t* x;
 };
+static_assert(offsetof(Int4Head, x) == sizeof(Int4Args) && sizeof(Int4Args) % 8 == 0, "arguments lie side by side");
+typedef const __attribute__((address_space(4))) Int4Head* Int4HeadPtr;
+#define QL_INT4_HEAD() ((Int4HeadPtr)__builtin_amdgcn_kernarg_segment_ptr())
 
 // One output by the definition, sum_k x[k] (code - zero) scale, in float64: what a result that is not finite is
 // replaced with.  The factored sum has no finite value where sum x code or zero sum x passes float32's range,
 // and is inf - inf = NaN wherever an activation is infinite; here only the result's own value counts.
-// m: row of x, n: row of the weights (of all experts).  One lane walks K, which costs nothing where all results
-// are finite, and it stops at the first NaN (M = 500, N = 14336, K = 4096: 108 us a call of its own, 188 if all x is
-// NaN, 363 with one infinity, 8 ms with one in every row).  The operands are
-// read from the kernel's arguments anew: kept for this from the start, they took 13 scalar
-// registers from the tiles that have none to spare.
-__device__ __forceinline__ float int4_defined(int64_t m, int64_t n, int64_t K) {
-  uint64_t args = reinterpret_cast<uint64_t>(__builtin_amdgcn_kernarg_segment_ptr());
+// at: QL_INT4_HEAD() of the kernel; m: row of x, n: row of the weights (of all experts).
+// One lane walks K, which costs nothing where all results are finite, and it stops at the first
+// NaN (M = 500, N = 14336, K = 4096: 108 us a call of its own, 188 if all x is NaN, 363 with one
+// infinity, 8 ms with one in every row).  The operands are read from the kernel's arguments anew:
+// kept for this from the start, they took 13 scalar registers from the tiles that have none to spare.
+__device__ __forceinline__ float int4_defined(Int4HeadPtr at, int64_t m, int64_t n, int64_t K) {
+  uint64_t args = reinterpret_cast<uint64_t>(at);
   asm volatile("" : "+s"(args));
-  const auto* const head = reinterpret_cast<const __attribute__((address_space(4))) Int4Head*>(args);
+  const Int4HeadPtr head = reinterpret_cast<Int4HeadPtr>(args);
   const int64_t row_bytes = head->a.row_bytes, groups = head->a.groups;
   const int shift = head->a.shift;
   const uint8_t* const w = head->a.w + n * row_bytes;
@@ -493,9 +499,10 @@ __global__ __launch_bounds__(64 * WN * WK) void int4_stream_kernel(Int4Args a, c
                                                                    int64_t N, int64_t K, float alpha, Epilogue epi) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int64_t n0 = int64_t(blockIdx.x) * (16 * NT * WN);
+  const Int4HeadPtr head = QL_INT4_HEAD();
   int4_stream_tile<M, NT, WN, WK, SH>(lds, a, x, int(rows), N, K, n0, [&](int m, int n, float v) {
     if (n0 + n < N) store_epi(out, m, n0 + n, N, v, alpha, out_bf16, epi);
-  }, [&](int m, int n) { return int4_defined(m, n0 + n, K); });
+  }, [=](int m, int n) { return int4_defined(head, m, n0 + n, K); });
 }
 
 // ---------------------------------------------------------------- matrix-core tile
@@ -833,6 +840,7 @@ struct TileOut {
   float alpha;
   int bf16;
   Epilogue epi;
+  Int4HeadPtr head;
 
   // acc[mt][i]: rows 16 mt .., columns wave_n + 16 i ..; K for the results that are not finite.
   template <int MT, int NT>
@@ -898,7 +906,7 @@ struct TileOut {
     for (; lost; lost &= lost - 1) {
       const int b = __builtin_ctzll(lost), tile = b >> 2;
       const int64_t row = tile / NT * 16 + (again & 63) / 16 * 4 + (b & 3), col = n0 + wave_n + tile % NT * 16 + (again & 15);
-      if (row < rows && col < N) put(row, col, int4_defined(row0 + row, wrow0 + col, K));
+      if (row < rows && col < N) put(row, col, int4_defined(head, row0 + row, wrow0 + col, K));
     }
   }
 
@@ -1231,13 +1239,14 @@ __global__ __launch_bounds__(64 * WN * WK) void int4_gemm_kernel(Int4Args a, con
   const int64_t tile = int64_t(blockIdx.x % 8) * per + blockIdx.x / 8;
   if (int64_t(blockIdx.x / 8) >= per || tile >= total) return;  // uniform over the block
   const int64_t m0 = tile % mtiles * L::kBM, n0 = tile / mtiles * L::kBN;
+  const Int4HeadPtr head = QL_INT4_HEAD();
   if constexpr (WK == 1) {
-    const TileOut to{static_cast<char*>(out) + m0 * N * (out_bf16 ? 2 : 4), M - m0, N, n0, m0, 0, alpha, out_bf16, epi};
+    const TileOut to{static_cast<char*>(out) + m0 * N * (out_bf16 ? 2 : 4), M - m0, N, n0, m0, 0, alpha, out_bf16, epi, head};
     int4_pipe_tile<MT, NT, WN, GS>(lds, a, x + m0 * K, M - m0, N, K, n0, to);
   } else {
     int4_tile<MT, NT, WK, GS>(lds, a, x + m0 * K, M - m0, N, K, n0, [&](int m, int n, float v) {
       if (m0 + m < M && n0 + n < N) store_epi(out, m0 + m, n0 + n, N, v, alpha, out_bf16, epi);
-    }, [&](int m, int n) { return int4_defined(m0 + m, n0 + n, K); });
+    }, [=](int m, int n) { return int4_defined(head, m0 + m, n0 + n, K); });
   }
 }
 
@@ -1301,10 +1310,11 @@ __global__ __launch_bounds__(64 * WN) void int4_grouped_kernel(Int4Args a, const
                                                                int64_t T, int64_t N, int64_t K, int64_t E) {
   using L = Int4Tile<MT, NT, WN, 1>;
   extern __shared__ __attribute__((aligned(16))) char lds[];
+  const Int4HeadPtr head = QL_INT4_HEAD();
   walk_groups<L::kBM, L::kBN, L::kThreads>(
       reinterpret_cast<int*>(lds + L::kLds), a, a_offsets, expert_ids, out, out_bf16, groups, T, N, E,
       [&](const Int4Args& b, int64_t e, int64_t m0, int64_t left, int64_t n0) {
-        const TileOut to{static_cast<char*>(out) + m0 * N * (out_bf16 ? 2 : 4), left, N, n0, m0, e * N, 1.f, out_bf16, Epilogue{}};
+        const TileOut to{static_cast<char*>(out) + m0 * N * (out_bf16 ? 2 : 4), left, N, n0, m0, e * N, 1.f, out_bf16, Epilogue{}, head};
         int4_pipe_tile<MT, NT, WN, GS>(lds, b, x + m0 * K, left, N, K, n0, to);
       });
 }
@@ -1323,12 +1333,13 @@ __global__ __launch_bounds__(64 * WN, kStreamWaves) void int4_grouped_stream_ker
                                                                          int64_t E) {
   using L = StreamLayout<4, NT, WN, 1>;
   extern __shared__ __attribute__((aligned(16))) char lds[];
+  const Int4HeadPtr head = QL_INT4_HEAD();
   walk_groups<4, 16 * NT * WN, 64 * WN>(
       reinterpret_cast<int*>(lds + L::kLds), a, a_offsets, expert_ids, out, out_bf16, groups, T, N, E,
       [&](const Int4Args& b, int64_t e, int64_t m0, int64_t left, int64_t n0) {
         int4_stream_tile<4, NT, WN, 1, SH>(lds, b, x + m0 * K, int(left < 4 ? left : 4), N, K, n0, [&](int m, int n, float v) {
           if (n0 + n < N) store_out(out, (m0 + m) * N + n0 + n, v, 1.f, out_bf16);
-        }, [&](int m, int n) { return int4_defined(m0 + m, e * N + n0 + n, K); });
+        }, [=](int m, int n) { return int4_defined(head, m0 + m, e * N + n0 + n, K); });
       });
 }
 
