@@ -922,11 +922,12 @@ struct TileOut {
 // s + 1, moves its x from registers to the other LDS buffer, and loads strip s + 2.  WN waves
 // side by side along N, one barrier per strip.  (With these phases one after the other
 // the 128x256 tile took 2.9 us for a strip of which the matrix cores need 1.1.)
-// Bound by what the 2 waves of a SIMD issue in turn: the vector ALU (decoding, and scaling, which
-// grows with the groups of a strip) and the matrix cores overlap little.  128x256 with groups of 128, 64, 32: ALU
-// busy for 38, 46, 56 % of the SIMDs' cycles, matrix cores for 39, 35, 31, LDS reads waited for by under 4 % of the
-// waves' cycles.  M = 500, N = 14336, K = 4096: 82, 98 (599 TFLOP/s), 121 us, calls behind each other
-// with the weights in the 256 MB cache.
+// Bound by what the 2 waves of a SIMD issue in turn: decoding, and scaling, which grows with the groups of
+// a strip, overlap little with the matrix cores' work.  128x256 with groups of 128, 64, 32: vector
+// instructions (the matrix ones among them) are issued in 38, 46, 56 % of the SIMDs' cycles, the matrix cores work in
+// 39, 35, 31 %, and under 5 % of the waves' cycles are waits to issue LDS instructions.
+// M = 500, N = 14336, K = 4096: 82, 98 (600 TFLOP/s), 121 us, calls behind each other with the
+// weights in the 256 MB cache; groups of 64, no weights there: 108.
 // With four strips' loads under way the smaller tiles gained nothing (64x256 58 us for 54).
 template <int MT, int NT, int WN, int GS>
 __device__ __forceinline__ void int4_pipe_tile(char* lds, const Int4Args& a, const uint16_t* __restrict__ x,
@@ -1471,7 +1472,8 @@ hipError_t launch_int4_gemm(const uint8_t* w, const uint16_t* scale, const uint8
   if (M == 2) return stream_rows<2>(a, x, out, out_bf16, M, N, K, alpha, num_cus, epi, s);
   if (M <= 4) return stream_rows<4>(a, x, out, out_bf16, M, N, K, alpha, num_cus, epi, s);
   // Up to 16 rows: tiles whose 4 waves split K, narrower where wide ones would leave CUs without any
-  // (N = K = 4096: 16x16 7.9 us, 16x32 10.3; N = 14336: 21.1 and 18.7).
+  // (16 rows, K = 4096, calls behind each other, in us: N = 4096 16x16 8.5, 16x32 10.5; N = 8192 11.2, 11.0; N = 14336
+  // 20.1, 17.2).
   if (M <= 16) {
     if (N <= int64_t(num_cus) * 32) return gemm_cfg<1, 1, 1, 4>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
     return gemm_cfg<1, 2, 1, 4>(a, x, out, out_bf16, M, N, K, alpha, epi, s);
