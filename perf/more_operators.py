@@ -297,10 +297,11 @@ def _calls(s, c):
         dpre, dx, dw = q.gated_gemm_backward(s["dy"], pre, s["w"], s["x"], activation=c["act"])
         return {"out": out, "dpre": dpre, "dx": dx, "dw": dw}
     if c["kind"] == "lora":
+        to = s["base"] if c["out"] == "f32" else None  # a float32 base is added to in place, as the plain form does
         if not c["train"]:
-            return q.lora_gemm(s["x"], s["a"], s["b"], s["offsets"], s["ids"], scale=s["scale"], base=s["base"],
+            return q.lora_gemm(s["x"], s["a"], s["b"], s["offsets"], s["ids"], scale=s["scale"], base=s["base"], out=to,
                                out_dtype=DTYPES[c["out"]])
-        out, z = q.lora_gemm(s["x"], s["a"], s["b"], s["offsets"], s["ids"], scale=s["scale"], base=s["base"],
+        out, z = q.lora_gemm(s["x"], s["a"], s["b"], s["offsets"], s["ids"], scale=s["scale"], base=s["base"], out=to,
                              out_dtype=DTYPES[c["out"]], return_z=True)
         dx, da, db = q.lora_gemm_backward(s["dy"], s["x"], z, s["a"], s["b"], s["offsets"], s["ids"], scale=s["scale"],
                                           base=s["dx"])
