@@ -601,6 +601,142 @@ int qlinear_swiglu(const void* x, void* y, int dtype, int64_t M, int64_t F, void
 int qlinear_swiglu_backward(const void* grad_y, const void* x, void* grad_x, int dtype, int64_t M,
                             int64_t F, void* stream);
 
+/*
+ * Gated product of a feed-forward layer, both projections, the activation and
+ * the product in one kernel:
+ *     g = alpha    * x W[0 .. F-1]^T  + addend[:, 0 .. F-1]
+ *     u = alpha_up * x W[F .. 2F-1]^T + addend[:, F .. 2F-1]
+ *     out = activation(g) * u
+ * w: [2F, K], gate rows first (the column order of qlinear_swiglu), of
+ * weight_format QLINEAR_WEIGHT_BF16 or QLINEAR_WEIGHT_FP8 (others give
+ * QLINEAR_ERR_INVALID_ARG); x: bfloat16 [M, K]; addend: [M, 2F] of
+ * addend_dtype (F32 or BF16) or NULL, what adapters add to the projections;
+ * activation: RELU, SILU or GELU_TANH; out: [M, F] of out_dtype.  pre: [M, 2F]
+ * of pre_dtype or NULL, g and u as the gradient takes them.  float32 sums and
+ * activation; out and pre are each rounded once.  M = 0 is allowed and does nothing.
+ */
+int qlinear_gated_gemm(const void* w, int weight_format, const void* x, const void* addend,
+                       int addend_dtype, void* out, int out_dtype, void* pre, int pre_dtype,
+                       int64_t M, int64_t F, int64_t K, float alpha, float alpha_up,
+                       int activation, void* stream);
+
+/*
+ * Gradient of qlinear_gated_gemm with respect to g and u:
+ *     grad_pre[:, 0 .. F-1]  = grad_out * u * activation'(g)
+ *     grad_pre[:, F .. 2F-1] = grad_out * activation(g)
+ * grad_out: [M, F] of grad_dtype; pre: [M, 2F] of pre_dtype, as the forward
+ * call left it; grad_pre: bfloat16 [M, 2F], the operand of the two calls below
+ * and the gradient of the addend.  ReLU's slope at 0 is 0.
+ */
+int qlinear_gated_backward(const void* grad_out, int grad_dtype, const void* pre, int pre_dtype,
+                           void* grad_pre, int64_t M, int64_t F, int activation, void* stream);
+
+/*
+ * Gradients of the dense bf16 linear layer out = x w^T (qlinear_bf16_gemm with
+ * alpha 1; the gated product with N = 2F):
+ *     grad_x[m, k] = sum_n grad_out[m, n] w[n, k]
+ *     grad_w[n, k] = sum_m grad_out[m, n] x[m, k]
+ * grad_out: bfloat16 [M, N], w: bfloat16 [N, K], x: bfloat16 [M, K]; the
+ * results of dtype F32 or BF16, float32 sums, rounded once.  M = 0: grad_x does
+ * nothing, grad_w is cleared.
+ */
+int qlinear_bf16_gemm_grad_x(const void* grad_out, const void* w, void* grad_x, int dtype,
+                             int64_t M, int64_t N, int64_t K, void* stream);
+int qlinear_bf16_gemm_grad_w(const void* grad_out, const void* x, void* grad_w, int dtype,
+                             int64_t M, int64_t N, int64_t K, void* stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection.  For every
+ * group y, rows t in [a_offsets[y], a_offsets[y+1]) and l = adapter_ids[y]:
+ *     z[t]      = x[t] a[l]^T
+ *     out[t, n] = base[t, n] + scale[l] * sum_r z[t, r] b[l, n, r]
+ * x: bfloat16 [T, K]; a: bfloat16 [L, R, K]; b: bfloat16 [L, N, R] (adapters of
+ * a smaller rank are filled up with zeros); scale: float32 [L] or NULL (all
+ * 1); base: [T, N] of out_dtype or NULL (0), which may be out itself; out: [T, N]
+ * of out_dtype (F32 or BF16); z: float32 [T, R], 16-byte aligned, or NULL:
+ * kept for the backward pass.  z is float32 throughout, taken to the second
+ * product with 24 bits for a float32 out, 16 for a bfloat16 one; float32 sums, out rounded once.  Not finite
+ * values in a, b or x give results that are not finite.
+ * Groups as in qlinear_fp8_grouped_gemm: an id outside 0 .. L-1 has no adapter
+ * (out = base, z = 0), rows in no group are left as they were, offsets are clipped
+ * to T and must not decrease.  1 <= num_groups <= 4096, 1 <= L <= 4096,
+ * 1 <= R <= 256, N and K <= 2^20, T <= 2^30.  workspace: at least the bytes of
+ * qlinear_lora_workspace_size, 16-byte aligned; a smaller one is
+ * QLINEAR_ERR_INVALID_ARG.  T = 0 is allowed and does nothing.
+ */
+int qlinear_lora_workspace_size(int64_t num_groups, int64_t T, int64_t K, int64_t R,
+                                int64_t* bytes);
+int qlinear_lora_gemm(const void* x, const void* a, const void* b, const uint32_t* a_offsets,
+                      const int32_t* adapter_ids, const float* scale, const void* base, void* out,
+                      int out_dtype, float* z, int64_t num_groups, int64_t num_adapters, int64_t T,
+                      int64_t N, int64_t K, int64_t R, void* workspace, int64_t workspace_bytes,
+                      void* stream);
+
+/*
+ * Gradients of qlinear_lora_gemm (base's is grad_out itself):
+ *     dz     = grad_out[t] b[l]
+ *     grad_x[t]  = base[t] + scale[l] * dz[t] a[l]
+ *     grad_a[l]  = scale[l] * sum_t dz[t]^T x[t],   grad_b[l] = scale[l] * sum_t grad_out[t]^T z[t]
+ * over the rows of all groups of adapter l.  grad_out: bfloat16 [T, N]; x, a,
+ * b, a_offsets, adapter_ids, scale, z as above; base: [T, K] of x_dtype or
+ * NULL, the gradient that x has from elsewhere (the shared projection), which may be
+ * grad_x itself; grad_x: [T, K] of x_dtype, rows in no group left as they were;
+ * grad_a: [L, R, K], grad_b: [L, N, R] of param_dtype (F32 or BF16), written in
+ * full, zeros for an adapter without rows (and for T = 0).  The order of all sums is fixed.
+ */
+int qlinear_lora_backward_workspace_size(int64_t num_groups, int64_t num_adapters, int64_t T,
+                                         int64_t N, int64_t K, int64_t R, int64_t* bytes);
+int qlinear_lora_gemm_backward(const void* grad_out, const void* x, const float* z, const void* a,
+                               const void* b, const uint32_t* a_offsets,
+                               const int32_t* adapter_ids, const float* scale, const void* base,
+                               void* grad_x, int x_dtype, void* grad_a, void* grad_b,
+                               int param_dtype, int64_t num_groups, int64_t num_adapters,
+                               int64_t T, int64_t N, int64_t K, int64_t R, void* workspace,
+                               int64_t workspace_bytes, void* stream);
+
+/*
+ * The norm behind a block with its gate and residual scale, fused with the
+ * norm in front of the next block:
+ *     p            = block * block_weight / sqrt(mean(block^2) + eps)
+ *     residual_out = residual_scale * residual + gate * p
+ *     out          = residual_out * weight / sqrt(mean(residual_out^2) + eps)
+ * over rows of H values, out from residual_out as it is stored.  block NULL:
+ * residual_out (NULL then, as are block_weight and gate) is residual, the
+ * plain norm.  block_weight NULL: p = block, no norm behind the block.  gate:
+ * [gates, H] of param_dtype, row t * gates / T for row t (1: one for all,
+ * T: one a row; gates divides T), or NULL with gates = 0 (all 1).  residual and residual_out:
+ * [T, H] of residual_dtype; block and out: [T, H] of dtype; weight and
+ * block_weight: [H] of param_dtype.  All F32 or BF16, a BF16 residual with a BF16
+ * block only.  residual_out may be residual.  1 <= H <= 16384, eps > 0; float32 inside, so squares
+ * have to stay in its range (values below 2^63).  T = 0 is allowed and does nothing.
+ */
+int qlinear_block_norm(const void* residual, int residual_dtype, const void* weight,
+                       int param_dtype, const void* block, int dtype, const void* block_weight,
+                       const void* gate, int64_t gates, void* residual_out, void* out, int64_t T,
+                       int64_t H, float residual_scale, float eps, void* stream);
+
+/*
+ * Gradients of qlinear_block_norm.  grad_out: [T, H] of dtype; grad_residual_out:
+ * [T, H] of residual_dtype or NULL, what residual_out has from elsewhere;
+ * residual_out as the forward call stored it (without a block: residual);
+ * weight, block, block_weight, gate as there.  With D the whole gradient of
+ * residual_out: grad_residual = residual_scale * D (residual_dtype, may be
+ * grad_residual_out; without a block D itself), grad_block (dtype), and the sums over rows grad_weight,
+ * grad_block_weight [H] and grad_gate [gates, H] (param_dtype), each NULL
+ * where its input is.  float32 sums in a fixed order.  workspace: at least the bytes of
+ * qlinear_block_norm_backward_workspace_size (post: block_weight is given; gated:
+ * gate is), 16-byte aligned.  T = 0: grad_weight, grad_block_weight and grad_gate are cleared.
+ */
+int qlinear_block_norm_backward_workspace_size(int64_t T, int64_t H, int post, int gated,
+                                               int64_t* bytes);
+int qlinear_block_norm_backward(const void* grad_out, int dtype, const void* grad_residual_out,
+                                const void* residual_out, int residual_dtype, const void* weight,
+                                int param_dtype, const void* block, const void* block_weight,
+                                const void* gate, int64_t gates, void* grad_residual,
+                                void* grad_block, void* grad_weight, void* grad_block_weight,
+                                void* grad_gate, int64_t T, int64_t H, float residual_scale,
+                                float eps, void* workspace, int64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -47,6 +48,15 @@ __all__ = [
     "moe_combine_backward",
     "swiglu",
     "swiglu_backward",
+    "gated_gemm",
+    "gated_gemm_backward",
+    "bf16_gemm_grad_x",
+    "bf16_gemm_grad_w",
+    "lora_gemm",
+    "lora_gemm_backward",
+    "block_norm",
+    "block_norm_backward",
+    "BlockNormGrads",
     "PATHS",
     "gemm_workspace_bytes",
     "WEIGHT_FP8",
@@ -114,6 +124,19 @@ EXPORTED = {
     "qlinear_moe_combine_backward": [_p, _p, _i, _p, _p, _p, _p, _i64, _i64, _i64, _p],
     "qlinear_swiglu": [_p, _p, _i, _i64, _i64, _p],
     "qlinear_swiglu_backward": [_p, _p, _p, _i, _i64, _i64, _p],
+    "qlinear_gated_gemm": [_p, _i, _p, _p, _i, _p, _i, _p, _i, _i64, _i64, _i64, _f, _f, _i, _p],
+    "qlinear_gated_backward": [_p, _i, _p, _i, _p, _i64, _i64, _i, _p],
+    "qlinear_bf16_gemm_grad_x": [_p, _p, _p, _i, _i64, _i64, _i64, _p],
+    "qlinear_bf16_gemm_grad_w": [_p, _p, _p, _i, _i64, _i64, _i64, _p],
+    "qlinear_lora_workspace_size": [_i64, _i64, _i64, _i64, ctypes.POINTER(_i64)],
+    "qlinear_lora_gemm": [_p, _p, _p, _p, _p, _p, _p, _p, _i, _p, _i64, _i64, _i64, _i64, _i64, _i64, _p, _i64, _p],
+    "qlinear_lora_backward_workspace_size": [_i64, _i64, _i64, _i64, _i64, _i64, ctypes.POINTER(_i64)],
+    "qlinear_lora_gemm_backward": [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i, _p, _p, _i, _i64, _i64, _i64, _i64, _i64,
+                                   _i64, _p, _i64, _p],
+    "qlinear_block_norm": [_p, _i, _p, _i, _p, _i, _p, _p, _i64, _p, _p, _i64, _i64, _f, _f, _p],
+    "qlinear_block_norm_backward_workspace_size": [_i64, _i64, _i, _i, ctypes.POINTER(_i64)],
+    "qlinear_block_norm_backward": [_p, _i, _p, _p, _i, _p, _i, _p, _p, _p, _i64, _p, _p, _p, _p, _p, _i64, _i64, _f, _f,
+                                    _p, _i64, _p],
 }
 
 WEIGHT_FP8, WEIGHT_NVFP4, WEIGHT_BF16 = 0, 1, 2
@@ -842,3 +865,336 @@ def swiglu_backward(grad_y: torch.Tensor, x: torch.Tensor, grad_x: torch.Tensor 
     st = lib.qlinear_swiglu_backward(_ptr(grad_y), _ptr(x), _ptr(grad_x), _OUT_CODES[x.dtype], m, f, _stream(x))
     _check(st, "qlinear_swiglu_backward")
     return grad_x
+
+
+# ---------------------------------------------------------------- the feed-forward block around the projections
+
+
+def _call(name: str, at: torch.Tensor, *args):
+    """The C call ``name`` on the current stream of ``at``'s device, made current for the
+    call where it is not."""
+    if at.is_cuda and at.get_device() != torch.cuda.current_device():
+        with torch.cuda.device(at.device):
+            st = getattr(lib, name)(*args, _stream(at))
+    else:
+        st = getattr(lib, name)(*args, _stream(at))
+    _check(st, name)
+
+
+def _together(first: torch.Tensor, *others):
+    """Every given tensor on the first one's device."""
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"all tensors must be on one device, got {first.device} and {t.device}")
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+def _code(t):
+    return F32 if t is None else _OUT_CODES[t.dtype]
+
+
+def _bf16_matrix(t: torch.Tensor, what: str, shape=None) -> torch.Tensor:
+    t = _as_bf16(t, what)
+    _require(t, what)
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{what} must be {'a matrix' if shape is None else tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _float_code(dtype: torch.dtype, what: str) -> int:
+    if dtype not in _OUT_CODES:
+        raise TypeError(f"{what} must be float32 or bfloat16, got {dtype}")
+    return _OUT_CODES[dtype]
+
+
+def _gated_activation(activation: str) -> int:
+    if activation not in ("relu", "silu", "gelu_tanh"):
+        raise ValueError("activation must be 'relu', 'silu' or 'gelu_tanh'")
+    return ACTIVATIONS[activation]
+
+
+def gated_gemm(w: torch.Tensor, x: torch.Tensor, out: torch.Tensor | None = None,
+               out_dtype: torch.dtype = torch.bfloat16, alpha: float = 1.0, alpha_up: float | None = None,
+               addend: torch.Tensor | None = None, activation: str = "silu", return_pre: bool = False,
+               pre_dtype: torch.dtype = torch.float32):
+    """activation(g) * u of a feed-forward layer in one kernel (``qlinear_gated_gemm``), with
+    g = alpha x w[:F]^T and u = alpha_up x w[F:]^T (alpha_up None: alpha), w [2F, K] bfloat16
+    or float8_e4m3fn codes, plus addend [M, 2F] where given (adapters' part) -> out [M, F].
+    return_pre: (out, pre), pre [M, 2F] of pre_dtype holding g and u for
+    ``gated_gemm_backward`` (bfloat16 halves its memory and rounds what the gradient is taken
+    from)."""
+    if w.dtype in (torch.bfloat16, torch.int16, torch.uint16):
+        w, fmt = _as_bf16(w, "w"), WEIGHT_BF16
+    else:
+        w, fmt = _as_u8(w, "w"), WEIGHT_FP8
+    _require(w, "w")
+    x = _bf16_matrix(x, "x")
+    if w.dim() != 2 or w.shape[0] % 2 != 0 or x.shape[1] != w.shape[1]:
+        raise ValueError(f"shapes: w {tuple(w.shape)} must be [2F, K], x {tuple(x.shape)} must be [M, K]")
+    m, k = x.shape
+    f = w.shape[0] // 2
+    act, code = _gated_activation(activation), _float_code(out_dtype, "out_dtype")
+    pre_code = _float_code(pre_dtype, "pre_dtype")
+    if addend is not None:
+        _float_tensor(addend, "addend", (m, 2 * f))
+    out = _out(out, (m, f), out_dtype, x.device)
+    pre = _out(None, (m, 2 * f), pre_dtype, x.device) if return_pre else None
+    _together(x, w, addend, out)
+    if m > 0:
+        _call("qlinear_gated_gemm", x, _ptr(w), fmt, _ptr(x), _opt(addend), _code(addend), _ptr(out), code, _opt(pre),
+              pre_code, m, f, k, float(alpha), float(alpha if alpha_up is None else alpha_up), act)
+    return (out, pre) if return_pre else out
+
+
+def gated_gemm_backward(grad_out: torch.Tensor, pre: torch.Tensor, w: torch.Tensor, x: torch.Tensor,
+                        activation: str = "silu", need_x: bool = True, need_w: bool = True,
+                        grad_x_dtype: torch.dtype = torch.bfloat16, grad_w_dtype: torch.dtype = torch.bfloat16):
+    """Gradients of ``gated_gemm`` with bfloat16 weights and alpha 1 from its ``pre`` ->
+    (grad_pre bfloat16 [M, 2F], which is the addend's gradient, grad_x [M, K], grad_w [2F, K];
+    None for what is not needed) (``qlinear_gated_backward``, ``qlinear_bf16_gemm_grad_x``,
+    ``qlinear_bf16_gemm_grad_w``)."""
+    w, x = _bf16_matrix(w, "w"), _bf16_matrix(x, "x")
+    if w.shape[0] % 2 != 0 or x.shape[1] != w.shape[1]:
+        raise ValueError(f"shapes: w {tuple(w.shape)} must be [2F, K], x {tuple(x.shape)} must be [M, K]")
+    m, f = x.shape[0], w.shape[0] // 2
+    _float_tensor(grad_out, "grad_out", (m, f))
+    _float_tensor(pre, "pre", (m, 2 * f))
+    act = _gated_activation(activation)
+    _together(x, w, grad_out, pre)
+    grad_pre = _out(None, (m, 2 * f), torch.bfloat16, x.device)
+    if m > 0:
+        _call("qlinear_gated_backward", x, _ptr(grad_out), _code(grad_out), _ptr(pre), _code(pre), _ptr(grad_pre), m, f,
+              act)
+    return (grad_pre, bf16_gemm_grad_x(grad_pre, w, out_dtype=grad_x_dtype) if need_x else None,
+            bf16_gemm_grad_w(grad_pre, x, out_dtype=grad_w_dtype) if need_w else None)
+
+
+def bf16_gemm_grad_x(grad_out: torch.Tensor, w: torch.Tensor, out: torch.Tensor | None = None,
+                     out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """grad_out [M, N] @ w [N, K]: the gradient of ``bf16_gemm`` with respect to x
+    (``qlinear_bf16_gemm_grad_x``)."""
+    grad_out, w = _bf16_matrix(grad_out, "grad_out"), _bf16_matrix(w, "w")
+    (m, n), k = grad_out.shape, w.shape[1]
+    if w.shape[0] != n:
+        raise ValueError(f"shapes: grad_out {tuple(grad_out.shape)} must be [M, N], w {tuple(w.shape)} must be [N, K]")
+    code = _float_code(out_dtype, "out_dtype")
+    out = _out(out, (m, k), out_dtype, w.device)
+    _together(w, grad_out, out)
+    if m > 0:
+        _call("qlinear_bf16_gemm_grad_x", w, _ptr(grad_out), _ptr(w), _ptr(out), code, m, n, k)
+    return out
+
+
+def bf16_gemm_grad_w(grad_out: torch.Tensor, x: torch.Tensor, out: torch.Tensor | None = None,
+                     out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """grad_out [M, N]^T @ x [M, K]: the gradient of ``bf16_gemm`` with respect to w
+    (``qlinear_bf16_gemm_grad_w``); zeros for M = 0."""
+    grad_out, x = _bf16_matrix(grad_out, "grad_out"), _bf16_matrix(x, "x")
+    (m, n), k = grad_out.shape, x.shape[1]
+    if x.shape[0] != m:
+        raise ValueError(f"shapes: grad_out {tuple(grad_out.shape)} must be [M, N], x {tuple(x.shape)} must be [M, K]")
+    code = _float_code(out_dtype, "out_dtype")
+    out = _out(out, (n, k), out_dtype, x.device)
+    _together(x, grad_out, out)
+    if m == 0:
+        return out.zero_()
+    _call("qlinear_bf16_gemm_grad_w", x, _ptr(grad_out), _ptr(x), _ptr(out), code, m, n, k)
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _bytes_of(name: str, *sizes) -> int:
+    """What the size call ``name`` gives, a function of the sizes alone."""
+    need = _i64(0)
+    _check(getattr(lib, name)(*sizes, ctypes.byref(need)), name)
+    return need.value
+
+
+def _bytes(workspace, need: int, device) -> torch.Tensor | None:
+    """A workspace of at least ``need`` bytes: the given one, or a new one."""
+    if workspace is not None:
+        _require(workspace, "workspace")
+        return workspace
+    return torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
+
+
+def _size_of(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _adapters(x, a, b, a_offsets, adapter_ids, scale):
+    """The checked operands of the adapter calls -> (x, a, b, T, K, N, R, groups, adapters)."""
+    x, a, b = _bf16_matrix(x, "x"), _as_bf16(a, "a"), _as_bf16(b, "b")
+    for t, name in ((a, "a"), (b, "b"), (a_offsets, "a_offsets"), (adapter_ids, "adapter_ids")):
+        _require(t, name)
+    t, k = x.shape
+    if a.dim() != 3 or b.dim() != 3 or a.shape[2] != k or b.shape[0] != a.shape[0] or b.shape[2] != a.shape[1]:
+        raise ValueError(f"shapes: x {tuple(x.shape)} must be [T, K], a {tuple(a.shape)} [L, R, K], b {tuple(b.shape)} "
+                         "[L, N, R]")
+    if a_offsets.dtype not in (torch.int32, torch.uint32) or adapter_ids.dtype != torch.int32:
+        raise TypeError("a_offsets must be uint32/int32 and adapter_ids int32")
+    g = adapter_ids.numel()
+    if a_offsets.numel() != g + 1:
+        raise ValueError("a_offsets needs num_groups + 1 entries")
+    l, r = a.shape[0], a.shape[1]
+    if scale is not None:
+        _typed(scale, "scale", torch.float32, (l,))
+    _together(x, a, b, a_offsets, adapter_ids, scale)
+    return x, a, b, t, k, b.shape[1], r, g, l
+
+
+def lora_gemm(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, a_offsets: torch.Tensor, adapter_ids: torch.Tensor,
+              scale: torch.Tensor | None = None, base: torch.Tensor | None = None, out: torch.Tensor | None = None,
+              out_dtype: torch.dtype = torch.bfloat16, return_z: bool = False, workspace: torch.Tensor | None = None):
+    """base + scale[l] * (x a[l]^T) b[l]^T for the rows a_offsets[y] .. a_offsets[y + 1] - 1 of
+    every group y, l = adapter_ids[y] (``qlinear_lora_gemm``): low-rank adapters a [L, R, K],
+    b [L, N, R] of many requests beside a projection whose result is ``base`` [T, N] (None: 0;
+    ``out`` may be ``base``).  An id outside 0 .. L - 1 has no adapter (out = base); rows in no
+    group keep whatever ``out`` held (a new ``out`` starts uninitialised).  scale: float32 [L]
+    (None: 1).  return_z: (out, z), z = x a^T float32 [T, R] for ``lora_gemm_backward``."""
+    x, a, b, t, k, n, r, g, l = _adapters(x, a, b, a_offsets, adapter_ids, scale)
+    code = _float_code(out_dtype, "out_dtype")
+    if base is not None:
+        _typed(base, "base", out_dtype, (t, n))
+    out = _out(out, (t, n), out_dtype, x.device)
+    z = _out(None, (t, r), torch.float32, x.device) if return_z else None
+    ws = _bytes(workspace, _bytes_of("qlinear_lora_workspace_size", g, t, k, r), x.device)
+    _together(x, base, out, ws)
+    if t > 0:
+        _call("qlinear_lora_gemm", x, _ptr(x), _ptr(a), _ptr(b), _ptr(a_offsets), _ptr(adapter_ids), _opt(scale),
+              _opt(base), _ptr(out), code, _opt(z), g, l, t, n, k, r, _opt(ws), _size_of(ws))
+    return (out, z) if return_z else out
+
+
+def lora_gemm_backward(grad_out: torch.Tensor, x: torch.Tensor, z: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
+                       a_offsets: torch.Tensor, adapter_ids: torch.Tensor, scale: torch.Tensor | None = None,
+                       base: torch.Tensor | None = None, grad_x: torch.Tensor | None = None,
+                       grad_x_dtype: torch.dtype = torch.bfloat16, param_dtype: torch.dtype = torch.float32,
+                       workspace: torch.Tensor | None = None):
+    """Gradients of ``lora_gemm`` (``qlinear_lora_gemm_backward``) -> (grad_x [T, K] = base +
+    scale[l] * (grad_out b[l]) a[l], grad_a [L, R, K], grad_b [L, N, R] of param_dtype).  z as
+    ``lora_gemm`` returned it; base [T, K]: what x's gradient has from the projection beside
+    (None: 0; ``grad_x`` may be ``base``).  Rows in no group keep whatever ``grad_x`` held."""
+    x, a, b, t, k, n, r, g, l = _adapters(x, a, b, a_offsets, adapter_ids, scale)
+    grad_out = _bf16_matrix(grad_out, "grad_out", (t, n))
+    _typed(z, "z", torch.float32, (t, r))
+    x_code, code = _float_code(grad_x_dtype, "grad_x_dtype"), _float_code(param_dtype, "param_dtype")
+    if base is not None:
+        _typed(base, "base", grad_x_dtype, (t, k))
+    grad_x = _out(grad_x, (t, k), grad_x_dtype, x.device)
+    grad_a = torch.empty((l, r, k), dtype=param_dtype, device=x.device)
+    grad_b = torch.empty((l, n, r), dtype=param_dtype, device=x.device)
+    ws = _bytes(workspace, _bytes_of("qlinear_lora_backward_workspace_size", g, l, t, n, k, r), x.device)
+    _together(x, grad_out, z, base, grad_x, ws)
+    if t == 0:
+        return grad_x, grad_a.zero_(), grad_b.zero_()
+    _call("qlinear_lora_gemm_backward", x, _ptr(grad_out), _ptr(x), _ptr(z), _ptr(a), _ptr(b), _ptr(a_offsets),
+          _ptr(adapter_ids), _opt(scale), _opt(base), _ptr(grad_x), x_code, _ptr(grad_a), _ptr(grad_b), code, g, l, t, n,
+          k, r, _opt(ws), _size_of(ws))
+    return grad_x, grad_a, grad_b
+
+
+def _norm_operands(residual, weight, block, block_weight, gate):
+    """The checked inputs of the norm calls -> (T, H, the rows of the gate, block and out's dtype)."""
+    _float_tensor(residual, "residual")
+    if residual.dim() != 2:
+        raise ValueError("residual must be [T, H]")
+    t, h = residual.shape
+    _float_tensor(weight, "weight", (h,))
+    if block is None:
+        if block_weight is not None or gate is not None:
+            raise ValueError("block_weight and gate need a block")
+        return t, h, 0
+    _float_tensor(block, "block", (t, h))
+    if block_weight is not None:
+        _typed(block_weight, "block_weight", weight.dtype, (h,))
+    gates = 0
+    if gate is not None:
+        if gate.dim() == 1:
+            gate = gate.unsqueeze(0)
+        gates = gate.shape[0]
+        _typed(gate, "gate", weight.dtype, (gates, h))
+        if gates == 0 or t % gates != 0:
+            raise ValueError("gate must be [G, H] with G dividing T")
+    _together(residual, weight, block, block_weight, gate)
+    return t, h, gates
+
+
+def block_norm(residual: torch.Tensor, weight: torch.Tensor, block: torch.Tensor | None = None,
+               block_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None, residual_scale: float = 1.0,
+               eps: float = 1e-6, out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+               residual_out: torch.Tensor | None = None):
+    """The end of a block and the norm in front of the next one (``qlinear_block_norm``) ->
+    (out, residual_out), [T, H] both:
+
+        residual_out = residual_scale * residual + gate * (block normed by block_weight)
+        out          = residual_out normed by weight
+
+    with x normed by w = x * w / sqrt(mean(x^2) + eps) over a row.  block_weight None: the block
+    as it is; gate [G, H] (or [H]): row t takes row t * G / T, None: 1; block None: the plain norm
+    of residual, which is residual_out then.  out has the block's dtype (without a block out_dtype,
+    None: residual's); residual_out, in residual's dtype, may be residual."""
+    t, h, gates = _norm_operands(residual, weight, block, block_weight, gate)
+    if block is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a block")
+        out_dtype = residual.dtype if out_dtype is None else out_dtype
+    else:
+        if out_dtype is not None and out_dtype != block.dtype:
+            raise ValueError("out has the block's dtype")
+        out_dtype = block.dtype
+        residual_out = _out(residual_out, (t, h), residual.dtype, residual.device)
+    code = _float_code(out_dtype, "out_dtype")
+    out = _out(out, (t, h), out_dtype, residual.device)
+    _together(residual, weight, out, residual_out)
+    if t > 0:
+        _call("qlinear_block_norm", residual, _ptr(residual), _code(residual), _ptr(weight), _code(weight), _opt(block),
+              code, _opt(block_weight), _opt(gate), gates, _opt(residual_out), _ptr(out), t, h, float(residual_scale),
+              float(eps))
+    return out, residual if block is None else residual_out
+
+
+class BlockNormGrads(NamedTuple):
+    """What ``block_norm_backward`` returns; None where there was no such input."""
+    residual: torch.Tensor
+    weight: torch.Tensor
+    block: torch.Tensor | None
+    block_weight: torch.Tensor | None
+    gate: torch.Tensor | None
+
+
+def block_norm_backward(grad_out: torch.Tensor, grad_residual_out: torch.Tensor | None, residual_out: torch.Tensor,
+                        weight: torch.Tensor, block: torch.Tensor | None = None,
+                        block_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                        residual_scale: float = 1.0, eps: float = 1e-6, grad_residual: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None) -> BlockNormGrads:
+    """Gradients of ``block_norm`` (``qlinear_block_norm_backward``): grad_out of its out,
+    grad_residual_out of its residual_out from elsewhere (None: 0), residual_out as it returned
+    it, the other inputs as it took them.  grad_residual may be grad_residual_out."""
+    t, h, gates = _norm_operands(residual_out, weight, block, block_weight, gate)
+    dev = residual_out.device
+    _float_tensor(grad_out, "grad_out", (t, h))
+    if block is not None and grad_out.dtype != block.dtype:
+        raise ValueError("grad_out must have the block's dtype")
+    if grad_residual_out is not None:
+        _typed(grad_residual_out, "grad_residual_out", residual_out.dtype, (t, h))
+    grad_residual = _out(grad_residual, (t, h), residual_out.dtype, dev)
+    new = lambda like: None if like is None else torch.empty_like(like)  # noqa: E731
+    g = BlockNormGrads(grad_residual, new(weight), new(block), new(block_weight), new(gate))
+    need = _bytes_of("qlinear_block_norm_backward_workspace_size", t, h, int(block_weight is not None),
+                     int(gate is not None))
+    ws = _bytes(workspace, need, dev)
+    _together(residual_out, weight, grad_out, grad_residual_out, grad_residual, ws)
+    if t == 0:
+        for p in (g.weight, g.block_weight, g.gate):
+            if p is not None:
+                p.zero_()
+        return g
+    _call("qlinear_block_norm_backward", residual_out, _ptr(grad_out), _code(grad_out), _opt(grad_residual_out),
+          _ptr(residual_out), _code(residual_out), _ptr(weight), _code(weight), _opt(block), _opt(block_weight), _opt(gate),
+          gates, _ptr(grad_residual), _opt(g.block), _ptr(g.weight), _opt(g.block_weight), _opt(g.gate), t, h,
+          float(residual_scale), float(eps), _opt(ws), _size_of(ws))
+    return g

@@ -1,0 +1,70 @@
+// The two element types of the row operators (1 bfloat16, 0 float32): values and 16-byte
+// pieces to and from float32.
+#pragma once
+
+#include "device.hpp"
+
+namespace qlinear {
+
+template <int BF16> struct Elem;
+template <> struct Elem<1> {
+  using T = uint16_t;
+  static constexpr int kPer16 = 8;
+  static __device__ __forceinline__ float get(T v) { return bf16_to_f32(v); }
+  static __device__ __forceinline__ T put(float v) { return __builtin_bit_cast(T, static_cast<__bf16>(v)); }
+  static __device__ __forceinline__ void unpack(u32x4 v, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16lo(v[i]);
+      f[2 * i + 1] = bf16hi(v[i]);
+    }
+  }
+  static __device__ __forceinline__ u32x4 pack(const float (&f)[8]) {
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)  // one conversion instruction per pair
+      v[i] = __builtin_bit_cast(uint32_t, v2bf{static_cast<__bf16>(f[2 * i]), static_cast<__bf16>(f[2 * i + 1])});
+    return v;
+  }
+};
+template <> struct Elem<0> {
+  using T = float;
+  static constexpr int kPer16 = 4;
+  static __device__ __forceinline__ float get(T v) { return v; }
+  static __device__ __forceinline__ T put(float v) { return v; }
+  static __device__ __forceinline__ void unpack(u32x4 v, float (&f)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v[i]);
+  }
+  static __device__ __forceinline__ u32x4 pack(const float (&f)[4]) {
+    return u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+  }
+};
+
+// Eight values at p + i (16-byte aligned) to and from float32.
+template <int BF16>
+__device__ __forceinline__ void load_eight(const void* p, int64_t i, float (&f)[8]) {
+  if constexpr (BF16) {
+    Elem<1>::unpack(ld16(reinterpret_cast<const uint16_t*>(p) + i), f);
+  } else {
+    const u32x4 a = ld16(reinterpret_cast<const float*>(p) + i), b = ld16(reinterpret_cast<const float*>(p) + i + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[e] = __uint_as_float(a[e]);
+      f[4 + e] = __uint_as_float(b[e]);
+    }
+  }
+}
+
+template <int BF16>
+__device__ __forceinline__ void store_eight(void* p, int64_t i, const float (&f)[8]) {
+  if constexpr (BF16) {
+    *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(p) + i) = Elem<1>::pack(f);
+  } else {
+    const float a[4] = {f[0], f[1], f[2], f[3]}, b[4] = {f[4], f[5], f[6], f[7]};
+    *reinterpret_cast<u32x4*>(reinterpret_cast<float*>(p) + i) = Elem<0>::pack(a);
+    *reinterpret_cast<u32x4*>(reinterpret_cast<float*>(p) + i + 4) = Elem<0>::pack(b);
+  }
+}
+
+}  // namespace qlinear

@@ -196,4 +196,38 @@ hipError_t launch_moe_combine_backward(const void* dy, const void* rows, int bf1
 // dy null: the activation; else its gradient.
 hipError_t launch_swiglu(const void* x, const void* dy, void* out, int bf16, int64_t M, int64_t F, hipStream_t s);
 
+// gated.hip (GatedOut: gated.hpp)
+struct GatedOut;
+hipError_t launch_gated_gemm(const void* w, int fp8, const uint16_t* x, const GatedOut& o, int64_t M, int64_t F, int64_t K,
+                             int num_cus, hipStream_t s);
+hipError_t launch_gated_grad(const void* dy, int dy_bf16, const void* pre, int pre_bf16, uint16_t* dpre, int act, int64_t M,
+                             int64_t F, hipStream_t s);
+hipError_t launch_bf16_grad_x(const uint16_t* dout, const uint16_t* w, void* dx, int dx_bf16, int64_t M, int64_t N,
+                              int64_t K, int num_cus, hipStream_t s);
+hipError_t launch_bf16_grad_w(const uint16_t* dout, const uint16_t* x, void* dw, int dw_bf16, int64_t M, int64_t N,
+                              int64_t K, int num_cus, hipStream_t s);
+
+// lora.hip: low-rank adapters; the workspaces' sizes depend on the sizes alone.
+// Zeros over a whole number of 2-byte values.
+hipError_t launch_clear(void* p, int64_t bytes, hipStream_t s);
+size_t lora_ws_bytes(int64_t T, int64_t G, int64_t K, int64_t R);
+size_t lora_grad_ws_bytes(int64_t T, int64_t G, int64_t L, int64_t N, int64_t K, int64_t R);
+hipError_t launch_lora(const uint16_t* x, const uint16_t* a, const uint16_t* b, const uint32_t* offsets,
+                       const int32_t* ids, const float* scale, const void* base, void* out, int out_bf16, float* z,
+                       int64_t G, int64_t L, int64_t T, int64_t N, int64_t K, int64_t R, float* ws, hipStream_t s);
+hipError_t launch_lora_grad(const uint16_t* dout, const uint16_t* x, const float* z, const uint16_t* a, const uint16_t* b,
+                            const uint32_t* offsets, const int32_t* ids, const float* scale, const void* base, void* dx,
+                            int dx_bf16, void* da, void* db, int grad_bf16, int64_t G, int64_t L, int64_t T, int64_t N,
+                            int64_t K, int64_t R, char* ws, hipStream_t s);
+
+// block_norm.hip
+hipError_t launch_block_norm(const void* res, int r_bf16, const void* w, int p_bf16, const void* block, int io_bf16,
+                             const void* wo, const void* gate, int64_t gates, void* res_out, void* y, int64_t T,
+                             int64_t H, float scale, float eps, hipStream_t s);
+size_t block_norm_grad_ws_bytes(int64_t T, int64_t H, bool post, bool gate);
+hipError_t launch_block_norm_grad(const void* dy, int io_bf16, const void* dres_in, const void* res, int r_bf16,
+                                  const void* w, int p_bf16, const void* block, const void* wo, const void* gate,
+                                  int64_t gates, void* dres, void* dblock, void* dw, void* dwo, void* dgate, int64_t T,
+                                  int64_t H, float scale, float eps, float* ws, hipStream_t s);
+
 }  // namespace qlinear

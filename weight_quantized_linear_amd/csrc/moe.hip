@@ -2,7 +2,9 @@
 // softmax router and its gradient, the stable sort of token slots by expert,
 // the gather of token rows into expert order, the weighted way back and its
 // gradient, and the experts' gated activation with its gradient.
+#include "activation.hpp"
 #include "device.hpp"
+#include "elem.hpp"
 #include "launch.hpp"
 
 namespace qlinear {
@@ -23,41 +25,6 @@ template <bool NT> __device__ __forceinline__ void st16_at(void* p, u32x4 v) {
   if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any*>(p));
   else st16_any(p, v);
 }
-
-template <int BF16> struct Elem;
-template <> struct Elem<1> {
-  using T = uint16_t;
-  static constexpr int kPer16 = 8;
-  static __device__ __forceinline__ float get(T v) { return bf16_to_f32(v); }
-  static __device__ __forceinline__ T put(float v) { return __builtin_bit_cast(T, static_cast<__bf16>(v)); }
-  static __device__ __forceinline__ void unpack(u32x4 v, float (&f)[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = bf16lo(v[i]);
-      f[2 * i + 1] = bf16hi(v[i]);
-    }
-  }
-  static __device__ __forceinline__ u32x4 pack(const float (&f)[8]) {
-    u32x4 v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)  // one conversion instruction per pair
-      v[i] = __builtin_bit_cast(uint32_t, v2bf{static_cast<__bf16>(f[2 * i]), static_cast<__bf16>(f[2 * i + 1])});
-    return v;
-  }
-};
-template <> struct Elem<0> {
-  using T = float;
-  static constexpr int kPer16 = 4;
-  static __device__ __forceinline__ float get(T v) { return v; }
-  static __device__ __forceinline__ T put(float v) { return v; }
-  static __device__ __forceinline__ void unpack(u32x4 v, float (&f)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v[i]);
-  }
-  static __device__ __forceinline__ u32x4 pack(const float (&f)[4]) {
-    return u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
-  }
-};
 
 // ---------------------------------------------------------------- wave helpers
 
@@ -659,45 +626,6 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(
 }
 
 // ---------------------------------------------------------------- gated activation
-
-// What sigmoid(g) and sigmoid(-g) are made of, from h = exp(-|g| / 2): near = 1 / (1 + h^2) =
-// sigmoid(|g|); half = 1 for g >= 0, else h, so that sigmoid(g) = half^2 near; rest = sigmoid(-g).  Nothing
-// overflows or cancels.  A negative gate's two halves go to different factors of a
-// product: h^2 leaves float32's normal range below g = -87 (and the exponential instruction gives 0
-// there), where its product with u or dy need not, and h only below g = -174.
-// Good to a few float32 roundings (u = 2^-24): |g| log2(e) / 2 is taken with the
-// rounding error of its product, so h is off by 3 u (the instruction itself by 2) and h^2 by 7, 1 + h^2
-// adds one, and a Newton step leaves one of the reciprocal.  Beyond |g| = 256 nothing changes (h = 0).
-// The library's expf and division would be twice the instructions, and the forward pass over
-// bfloat16 was bound by them.
-__device__ __forceinline__ void sigmoids(float g, float& near, float& half, float& rest) {
-  constexpr float kHi = 0.5f * 1.44269502f, kLo = 0.5f * 1.92596299e-8f;  // log2(e) / 2
-  const float a = fminf(fabsf(g), 256.f);
-  const float t = -a * kHi;
-  const float r = fmaf(-a, kLo, fmaf(-a, kHi, -t));
-  float h = __builtin_amdgcn_exp2f(t);
-  h = fmaf(h, r * 0.693147182f, h);
-  const float d = fmaf(h, h, 1.f), y = __builtin_amdgcn_rcpf(d);
-  near = fmaf(y, fmaf(-d, y, 1.f), y);
-  half = g >= 0.f ? 1.f : h;
-  rest = g >= 0.f ? h * h * near : near;
-}
-
-__device__ __forceinline__ float swiglu_one(float g, float u) {
-  float near, half, rest;
-  sigmoids(g, near, half, rest);
-  return (g * near * half) * (u * half);
-}
-
-// dgate = dy u sig (1 + g (1 - sig)), dup = dy g sig, with sigmoid(-g) for 1 - sig.  dy u alone
-// could overflow where the gradient does not.
-__device__ __forceinline__ void swiglu_grad(float g, float u, float dy, float& dg, float& du) {
-  float near, half, rest;
-  sigmoids(g, near, half, rest);
-  const float dh = dy * half;
-  dg = dh * (u * half) * (near * fmaf(g, rest, 1.f));
-  du = dh * (g * near * half);
-}
 
 // n / d for n < 2^31 as a product: m = floor(2^(31 + l) / d) + 1 with l = ceil(log2 d) is
 // off by less than 2^-31 of itself, so n m / 2^(31 + l) by less than 1 / d.

@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "launch.hpp"
+#include "gated_out.hpp"
 
 namespace {
 
@@ -97,6 +98,32 @@ int to_epilogue(const qlinear_epilogue* e, int64_t M, int64_t N, Epilogue* out) 
 int check_workspace(const void* ws, int64_t ws_bytes) {
   if (ws_bytes < 0 || (!ws && ws_bytes != 0) || (ws && !aligned(ws, 16))) return QLINEAR_ERR_INVALID_ARG;
   return QLINEAR_OK;
+}
+
+// Sizes and choices of the feed-forward block's operators.
+constexpr int64_t kMaxLoraGroups = 4096, kMaxAdapters = 4096, kMaxRank = 256, kMaxLoraWidth = int64_t(1) << 20;
+constexpr int64_t kMaxNormWidth = 16384;
+
+bool gated_act_ok(int act) { return act >= QLINEAR_ACT_RELU && act <= QLINEAR_ACT_GELU_TANH; }
+bool gated_sizes_ok(int64_t M, int64_t F) { return F > 0 && fits(M > 0 ? M : 1, F, 2); }
+
+bool linear_grad_ok(const void* dout, const void* other, const void* grad, int dtype, int64_t M, int64_t N, int64_t K) {
+  return dout && other && grad && M >= 0 && N > 0 && K > 0 && fits(M ? M : 1, N) && fits(M ? M : 1, K) && fits(N, K) &&
+         float_out_ok(dtype) && aligned(dout, 2) && aligned(other, 2) && aligned(grad, out_size(dtype));
+}
+
+bool lora_sizes_ok(int64_t G, int64_t L, int64_t T, int64_t N, int64_t K, int64_t R) {
+  return G > 0 && G <= kMaxLoraGroups && L > 0 && L <= kMaxAdapters && T >= 0 && T <= (int64_t(1) << 30) && N > 0 &&
+         N <= kMaxLoraWidth && K > 0 && K <= kMaxLoraWidth && R > 0 && R <= kMaxRank;
+}
+
+bool norm_ok(int res_dtype, int dtype, int param_dtype, const void* block, const void* block_weight, const void* gate,
+             int64_t gates, int64_t T, int64_t H, float eps) {
+  if (!float_out_ok(res_dtype) || !float_out_ok(dtype) || !float_out_ok(param_dtype)) return false;
+  if (res_dtype == QLINEAR_BF16 && dtype == QLINEAR_F32) return false;
+  if (T < 0 || H <= 0 || H > kMaxNormWidth || !fits(T ? T : 1, H) || !(eps > 0.f)) return false;
+  if (!block && (block_weight || gate)) return false;
+  return gate ? gates > 0 && T % gates == 0 && fits(gates, H) : gates == 0;
 }
 
 // The FP8 kernel family that a call takes: `path` if forced, else the
@@ -734,6 +761,191 @@ int qlinear_swiglu_backward(const void* grad_y, const void* x, void* grad_x, int
   if (int st = current_device(&num_cus)) return st;
   if (M == 0) return QLINEAR_OK;
   return finish(launch_swiglu(x, grad_y, grad_x, dtype == QLINEAR_BF16, M, F, static_cast<hipStream_t>(stream)));
+}
+
+int qlinear_gated_gemm(const void* w, int weight_format, const void* x, const void* addend, int addend_dtype, void* out,
+                       int out_dtype, void* pre, int pre_dtype, int64_t M, int64_t F, int64_t K, float alpha,
+                       float alpha_up, int activation, void* stream) {
+  if (!w || !x || !out || M < 0 || !gated_sizes_ok(M, F) || K <= 0 || !fits(2, F, K) || !fits(M ? M : 1, K) ||
+      !gated_act_ok(activation))
+    return QLINEAR_ERR_INVALID_ARG;
+  if (weight_format != QLINEAR_WEIGHT_BF16 && weight_format != QLINEAR_WEIGHT_FP8) return QLINEAR_ERR_INVALID_ARG;
+  if (!float_out_ok(out_dtype) || (addend && !float_out_ok(addend_dtype)) || (pre && !float_out_ok(pre_dtype)))
+    return QLINEAR_ERR_INVALID_ARG;
+  const bool fp8 = weight_format == QLINEAR_WEIGHT_FP8;
+  if (!aligned(x, 2) || (!fp8 && !aligned(w, 2)) || !aligned(out, out_size(out_dtype)) ||
+      (addend && !aligned(addend, out_size(addend_dtype))) || (pre && !aligned(pre, out_size(pre_dtype))))
+    return QLINEAR_ERR_INVALID_ARG;
+  int num_cus = 0;
+  if (int st = current_device(&num_cus)) return st;
+  if (M == 0) return QLINEAR_OK;
+  const GatedOut o{addend, out, pre, alpha, alpha_up, activation, out_dtype == QLINEAR_BF16,
+                   addend_dtype == QLINEAR_BF16, pre_dtype == QLINEAR_BF16};
+  return finish(launch_gated_gemm(w, fp8, static_cast<const uint16_t*>(x), o, M, F, K, num_cus,
+                                  static_cast<hipStream_t>(stream)));
+}
+
+int qlinear_gated_backward(const void* grad_out, int grad_dtype, const void* pre, int pre_dtype, void* grad_pre, int64_t M,
+                           int64_t F, int activation, void* stream) {
+  if (!grad_out || !pre || !grad_pre || M < 0 || !gated_sizes_ok(M, F) || !gated_act_ok(activation) ||
+      !float_out_ok(grad_dtype) || !float_out_ok(pre_dtype))
+    return QLINEAR_ERR_INVALID_ARG;
+  if (!aligned(grad_out, out_size(grad_dtype)) || !aligned(pre, out_size(pre_dtype)) || !aligned(grad_pre, 2))
+    return QLINEAR_ERR_INVALID_ARG;
+  int num_cus = 0;
+  if (int st = current_device(&num_cus)) return st;
+  if (M == 0) return QLINEAR_OK;
+  return finish(launch_gated_grad(grad_out, grad_dtype == QLINEAR_BF16, pre, pre_dtype == QLINEAR_BF16,
+                                  static_cast<uint16_t*>(grad_pre), activation, M, F, static_cast<hipStream_t>(stream)));
+}
+
+int qlinear_bf16_gemm_grad_x(const void* grad_out, const void* w, void* grad_x, int dtype, int64_t M, int64_t N, int64_t K,
+                             void* stream) {
+  if (!linear_grad_ok(grad_out, w, grad_x, dtype, M, N, K)) return QLINEAR_ERR_INVALID_ARG;
+  int num_cus = 0;
+  if (int st = current_device(&num_cus)) return st;
+  if (M == 0) return QLINEAR_OK;
+  return finish(launch_bf16_grad_x(static_cast<const uint16_t*>(grad_out), static_cast<const uint16_t*>(w), grad_x,
+                                   dtype == QLINEAR_BF16, M, N, K, num_cus, static_cast<hipStream_t>(stream)));
+}
+
+int qlinear_bf16_gemm_grad_w(const void* grad_out, const void* x, void* grad_w, int dtype, int64_t M, int64_t N, int64_t K,
+                             void* stream) {
+  if (!linear_grad_ok(grad_out, x, grad_w, dtype, M, N, K)) return QLINEAR_ERR_INVALID_ARG;
+  int num_cus = 0;
+  if (int st = current_device(&num_cus)) return st;
+  if (M == 0) return finish(launch_clear(grad_w, N * K * int64_t(out_size(dtype)), static_cast<hipStream_t>(stream)));
+  return finish(launch_bf16_grad_w(static_cast<const uint16_t*>(grad_out), static_cast<const uint16_t*>(x), grad_w,
+                                   dtype == QLINEAR_BF16, M, N, K, num_cus, static_cast<hipStream_t>(stream)));
+}
+
+int qlinear_lora_workspace_size(int64_t num_groups, int64_t T, int64_t K, int64_t R, int64_t* bytes) {
+  if (!bytes) return QLINEAR_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (!lora_sizes_ok(num_groups, 1, T, 1, K, R)) return QLINEAR_ERR_INVALID_ARG;
+  *bytes = int64_t(lora_ws_bytes(T, num_groups, K, R));
+  return QLINEAR_OK;
+}
+
+int qlinear_lora_gemm(const void* x, const void* a, const void* b, const uint32_t* a_offsets, const int32_t* adapter_ids,
+                      const float* scale, const void* base, void* out, int out_dtype, float* z, int64_t num_groups,
+                      int64_t num_adapters, int64_t T, int64_t N, int64_t K, int64_t R, void* workspace,
+                      int64_t workspace_bytes, void* stream) {
+  if (!x || !a || !b || !a_offsets || !adapter_ids || !out || !float_out_ok(out_dtype) ||
+      !lora_sizes_ok(num_groups, num_adapters, T, N, K, R))
+    return QLINEAR_ERR_INVALID_ARG;
+  if (int st = check_workspace(workspace, workspace_bytes)) return st;
+  if (workspace_bytes < int64_t(lora_ws_bytes(T, num_groups, K, R))) return QLINEAR_ERR_INVALID_ARG;
+  const size_t es = out_size(out_dtype);
+  if (!aligned(x, 2) || !aligned(a, 2) || !aligned(b, 2) || !aligned(a_offsets, 4) || !aligned(adapter_ids, 4) ||
+      !aligned(scale, 4) || !aligned(base, es) || !aligned(out, es) || !aligned(z, 16))
+    return QLINEAR_ERR_INVALID_ARG;
+  int num_cus = 0;
+  if (int st = current_device(&num_cus)) return st;
+  if (T == 0) return QLINEAR_OK;
+  return finish(launch_lora(static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(a),
+                            static_cast<const uint16_t*>(b), a_offsets, adapter_ids, scale, base, out,
+                            out_dtype == QLINEAR_BF16, z, num_groups, num_adapters, T, N, K, R,
+                            static_cast<float*>(workspace), static_cast<hipStream_t>(stream)));
+}
+
+int qlinear_lora_backward_workspace_size(int64_t num_groups, int64_t num_adapters, int64_t T, int64_t N, int64_t K,
+                                         int64_t R, int64_t* bytes) {
+  if (!bytes) return QLINEAR_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (!lora_sizes_ok(num_groups, num_adapters, T, N, K, R)) return QLINEAR_ERR_INVALID_ARG;
+  *bytes = int64_t(lora_grad_ws_bytes(T, num_groups, num_adapters, N, K, R));
+  return QLINEAR_OK;
+}
+
+int qlinear_lora_gemm_backward(const void* grad_out, const void* x, const float* z, const void* a, const void* b,
+                               const uint32_t* a_offsets, const int32_t* adapter_ids, const float* scale, const void* base,
+                               void* grad_x, int x_dtype, void* grad_a, void* grad_b, int param_dtype, int64_t num_groups,
+                               int64_t num_adapters, int64_t T, int64_t N, int64_t K, int64_t R, void* workspace,
+                               int64_t workspace_bytes, void* stream) {
+  if (!grad_out || !x || !z || !a || !b || !a_offsets || !adapter_ids || !grad_x || !grad_a || !grad_b ||
+      !float_out_ok(x_dtype) || !float_out_ok(param_dtype) || !lora_sizes_ok(num_groups, num_adapters, T, N, K, R))
+    return QLINEAR_ERR_INVALID_ARG;
+  if (int st = check_workspace(workspace, workspace_bytes)) return st;
+  if (workspace_bytes < int64_t(lora_grad_ws_bytes(T, num_groups, num_adapters, N, K, R))) return QLINEAR_ERR_INVALID_ARG;
+  const size_t xs = out_size(x_dtype), ps = out_size(param_dtype);
+  if (!aligned(grad_out, 2) || !aligned(x, 2) || !aligned(z, 4) || !aligned(a, 2) || !aligned(b, 2) ||
+      !aligned(a_offsets, 4) || !aligned(adapter_ids, 4) || !aligned(scale, 4) || !aligned(base, xs) ||
+      !aligned(grad_x, xs) || !aligned(grad_a, ps) || !aligned(grad_b, ps))
+    return QLINEAR_ERR_INVALID_ARG;
+  int num_cus = 0;
+  if (int st = current_device(&num_cus)) return st;
+  const auto s = static_cast<hipStream_t>(stream);
+  if (T == 0) {
+    if (int st = finish(launch_clear(grad_a, num_adapters * R * K * int64_t(ps), s))) return st;
+    return finish(launch_clear(grad_b, num_adapters * R * N * int64_t(ps), s));
+  }
+  return finish(launch_lora_grad(static_cast<const uint16_t*>(grad_out), static_cast<const uint16_t*>(x), z,
+                                 static_cast<const uint16_t*>(a), static_cast<const uint16_t*>(b), a_offsets, adapter_ids,
+                                 scale, base, grad_x, x_dtype == QLINEAR_BF16, grad_a, grad_b,
+                                 param_dtype == QLINEAR_BF16, num_groups, num_adapters, T, N, K, R,
+                                 static_cast<char*>(workspace), s));
+}
+
+int qlinear_block_norm(const void* residual, int residual_dtype, const void* weight, int param_dtype, const void* block,
+                       int dtype, const void* block_weight, const void* gate, int64_t gates, void* residual_out,
+                       void* out, int64_t T, int64_t H, float residual_scale, float eps, void* stream) {
+  if (!residual || !weight || !out || !norm_ok(residual_dtype, dtype, param_dtype, block, block_weight, gate, gates, T, H, eps) ||
+      (block != nullptr) != (residual_out != nullptr))
+    return QLINEAR_ERR_INVALID_ARG;
+  const size_t rs = out_size(residual_dtype), es = out_size(dtype), ps = out_size(param_dtype);
+  if (!aligned(residual, rs) || !aligned(residual_out, rs) || !aligned(block, es) || !aligned(out, es) ||
+      !aligned(weight, ps) || !aligned(block_weight, ps) || !aligned(gate, ps))
+    return QLINEAR_ERR_INVALID_ARG;
+  int num_cus = 0;
+  if (int st = current_device(&num_cus)) return st;
+  if (T == 0) return QLINEAR_OK;
+  return finish(launch_block_norm(residual, residual_dtype == QLINEAR_BF16, weight, param_dtype == QLINEAR_BF16, block,
+                                  dtype == QLINEAR_BF16, block_weight, gate, gates, residual_out, out, T, H,
+                                  residual_scale, eps, static_cast<hipStream_t>(stream)));
+}
+
+int qlinear_block_norm_backward_workspace_size(int64_t T, int64_t H, int post, int gated, int64_t* bytes) {
+  if (!bytes) return QLINEAR_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (T < 0 || H <= 0 || H > kMaxNormWidth || !fits(T ? T : 1, H)) return QLINEAR_ERR_INVALID_ARG;
+  *bytes = int64_t(block_norm_grad_ws_bytes(T, H, post != 0, gated != 0));
+  return QLINEAR_OK;
+}
+
+int qlinear_block_norm_backward(const void* grad_out, int dtype, const void* grad_residual_out, const void* residual_out,
+                                int residual_dtype, const void* weight, int param_dtype, const void* block,
+                                const void* block_weight, const void* gate, int64_t gates, void* grad_residual,
+                                void* grad_block, void* grad_weight, void* grad_block_weight, void* grad_gate, int64_t T,
+                                int64_t H, float residual_scale, float eps, void* workspace, int64_t workspace_bytes,
+                                void* stream) {
+  if (!grad_out || !residual_out || !weight || !grad_residual || !grad_weight ||
+      !norm_ok(residual_dtype, dtype, param_dtype, block, block_weight, gate, gates, T, H, eps) ||
+      (block != nullptr) != (grad_block != nullptr) || (block_weight != nullptr) != (grad_block_weight != nullptr) ||
+      (gate != nullptr) != (grad_gate != nullptr))
+    return QLINEAR_ERR_INVALID_ARG;
+  if (int st = check_workspace(workspace, workspace_bytes)) return st;
+  if (workspace_bytes < int64_t(block_norm_grad_ws_bytes(T, H, block_weight != nullptr, gate != nullptr)))
+    return QLINEAR_ERR_INVALID_ARG;
+  const size_t rs = out_size(residual_dtype), es = out_size(dtype), ps = out_size(param_dtype);
+  if (!aligned(grad_out, es) || !aligned(grad_residual_out, rs) || !aligned(residual_out, rs) || !aligned(weight, ps) ||
+      !aligned(block, es) || !aligned(block_weight, ps) || !aligned(gate, ps) || !aligned(grad_residual, rs) ||
+      !aligned(grad_block, es) || !aligned(grad_weight, ps) || !aligned(grad_block_weight, ps) || !aligned(grad_gate, ps))
+    return QLINEAR_ERR_INVALID_ARG;
+  int num_cus = 0;
+  if (int st = current_device(&num_cus)) return st;
+  const auto s = static_cast<hipStream_t>(stream);
+  if (T == 0) {
+    if (int st = finish(launch_clear(grad_weight, H * int64_t(ps), s))) return st;
+    if (block_weight)
+      if (int st = finish(launch_clear(grad_block_weight, H * int64_t(ps), s))) return st;
+    return gate ? finish(launch_clear(grad_gate, gates * H * int64_t(ps), s)) : QLINEAR_OK;
+  }
+  return finish(launch_block_norm_grad(grad_out, dtype == QLINEAR_BF16, grad_residual_out, residual_out,
+                                       residual_dtype == QLINEAR_BF16, weight, param_dtype == QLINEAR_BF16, block,
+                                       block_weight, gate, gates, grad_residual, grad_block, grad_weight,
+                                       grad_block_weight, grad_gate, T, H, block ? residual_scale : 1.f, eps,
+                                       static_cast<float*>(workspace), s));
 }
 
 }  // extern "C"
