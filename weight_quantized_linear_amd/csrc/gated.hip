@@ -9,6 +9,7 @@
 #include "elem.hpp"
 #include "gated.hpp"
 #include "launch.hpp"
+#include "product_lds.hpp"
 
 namespace qlinear {
 
@@ -127,6 +128,152 @@ __global__ __launch_bounds__(kThreads) void product_any_kernel(const uint16_t* _
                           });
 }
 
+// ---------------------------------------------------------------- products in large tiles
+
+// A slab of 32 rows and COLS columns of a wave's results on their way to 16-byte stores.  Rows of
+// COLS values and 16 or 32 bytes between them, so that a wave's two halves of a write hit different banks.
+template <int OUT, int COLS>
+struct OutSlab {
+  static constexpr int kEs = OUT ? 2 : 4, kStride = COLS * kEs + (OUT ? 16 : 32), kBytes = 32 * kStride;
+  char* base;
+  __device__ __forceinline__ void put(int row, int col, float v) const {
+    if constexpr (OUT) *reinterpret_cast<__bf16*>(base + row * kStride + col * 2) = static_cast<__bf16>(v);
+    else *reinterpret_cast<float*>(base + row * kStride + col * 4) = v;
+  }
+  // Rows row0 .. + 31 (below M), columns col0 .. + COLS - 1 (below N) of out, rows of ld values; vec: whole
+  // 16-byte pieces at aligned addresses.
+  __device__ __forceinline__ void flush(void* out, int64_t ld, int64_t row0, int64_t col0, int64_t M, int64_t N,
+                                        bool vec) const {
+    constexpr int kPiece = 16 / kEs, kPieces = COLS / kPiece;
+    const int lane = threadIdx.x & 63;
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int q = 0; q < 32 * kPieces / 64; ++q) {
+      const int row = (64 * q + lane) / kPieces, col = (64 * q + lane) % kPieces * kPiece;
+      if (row0 + row >= M || col0 + col >= N) continue;
+      const char* from = base + row * kStride + col * kEs;
+      char* to = reinterpret_cast<char*>(out) + ((row0 + row) * ld + col0 + col) * kEs;
+      if (vec) {
+        *reinterpret_cast<u32x4*>(to) = lds16(from);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kPiece; ++e) {
+          if (col0 + col + e >= N) break;
+          if constexpr (OUT) reinterpret_cast<uint16_t*>(to)[e] = reinterpret_cast<const uint16_t*>(from)[e];
+          else reinterpret_cast<float*>(to)[e] = reinterpret_cast<const float*>(from)[e];
+        }
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slab is read before it is written again
+  }
+};
+
+// TA, TB: operand stored across k.
+template <bool TA, bool TB, int BM, int BN, int S, int WY, int NW, int OUT>
+__global__ __launch_bounds__(64 * NW) void product_kernel(Operand a, Operand b, void* __restrict__ out, int64_t M,
+                                                          int64_t N, int64_t K, int vec) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  using AOp = std::conditional_t<TA, TurnedOperand<BM, NW>, RowsOperand<BM, NW, 2, PlainRows>>;
+  using BOp = std::conditional_t<TB, TurnedOperand<BN, NW>, RowsOperand<BN, NW, 2, PlainRows>>;
+  using L = ProductLayout<AOp, BOp, BM, BN, S, WY, NW>;
+  int64_t tm, tn;
+  tile_of_block(blockIdx.x, (M + BM - 1) / BM, (N + BN - 1) / BN, tm, tn);
+  AOp ao;
+  BOp bo;
+  ao.init(a, PlainRows{tm * BM, M}, K);
+  bo.init(b, PlainRows{tn * BN, N}, K);
+  v16f acc[L::FM][L::FN];
+  product_tile<AOp, BOp, BM, BN, S, WY, NW>(lds, ao, bo, K, acc);
+
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, r = lane & 31, h = lane >> 5;
+  const int64_t m0 = tm * BM + wid / L::WX * (BM / WY), n0 = tn * BN + wid % L::WX * (BN / L::WX);
+  using Out = OutSlab<OUT, 32 * L::FN>;
+  static_assert(NW * Out::kBytes <= L::kLds, "staging");
+  block_barrier();  // every wave is done with the last strip
+  const Out slab{lds + wid * Out::kBytes};
+#pragma unroll
+  for (int i = 0; i < L::FM; ++i) {
+#pragma unroll
+    for (int j = 0; j < L::FN; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) slab.put(8 * (v / 4) + 4 * h + v % 4, 32 * j + r, acc[i][j][v]);
+    slab.flush(out, N, m0 + 32 * i, n0, M, N, vec);
+  }
+}
+
+// The gated product: a wave's columns are FN / 2 times 32 gate and the 32 up columns beside them.
+template <int EB, int BM, int BF, int S, int WY, int NW, int OUT>
+__global__ __launch_bounds__(64 * NW) void gated_kernel(Operand x, Operand w, GatedOut o, int64_t M, int64_t F, int64_t K,
+                                                        int vec, int pre_vec) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  constexpr int BN = 2 * BF;
+  using AOp = RowsOperand<BM, NW, 2, PlainRows>;
+  using BOp = RowsOperand<BN, NW, EB, GatedRows>;
+  using L = ProductLayout<AOp, BOp, BM, BN, S, WY, NW>;
+  static_assert(L::FN % 2 == 0, "gate and up of a column in one wave");
+  int64_t tm, tn;
+  tile_of_block(blockIdx.x, (M + BM - 1) / BM, (F + BF - 1) / BF, tm, tn);
+  AOp ao;
+  BOp bo;
+  ao.init(x, PlainRows{tm * BM, M}, K);
+  bo.init(w, GatedRows{tn * BF, F}, K);
+  v16f acc[L::FM][L::FN];
+  product_tile<AOp, BOp, BM, BN, S, WY, NW>(lds, ao, bo, K, acc);
+
+  constexpr int FC = L::FN / 2;  // blocks of 32 columns
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, r = lane & 31, h = lane >> 5;
+  const int64_t m0 = tm * BM + wid / L::WX * (BM / WY), f0 = tn * BF + wid % L::WX * (BF / L::WX);
+  using Out = OutSlab<0, 32 * FC>;  // the wider of the types that leave by it
+  static_assert(NW * Out::kBytes <= L::kLds, "staging");
+  block_barrier();  // every wave is done with the last strip
+  char* const mine = lds + wid * Out::kBytes;
+#pragma unroll
+  for (int i = 0; i < L::FM; ++i) {
+#pragma unroll
+    for (int j = 0; j < FC; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        float g = o.alpha * acc[i][2 * j][v], u = o.alpha_up * acc[i][2 * j + 1][v];
+        if (o.addend) {
+          const int64_t m = m0 + 32 * i + 8 * (v / 4) + 4 * h + v % 4, f = f0 + 32 * j + r;
+          if (m < M && f < F) {
+            g += get_float(o.addend, m * 2 * F + f, o.addend_bf16);
+            u += get_float(o.addend, m * 2 * F + F + f, o.addend_bf16);
+          }
+        }
+        acc[i][2 * j][v] = g;
+        acc[i][2 * j + 1][v] = u;
+      }
+    auto leave = [&](auto type, void* out, int64_t ld, int64_t col, int64_t cols, bool v16, auto value) {
+      const OutSlab<decltype(type)::value, 32 * FC> slab{mine};
+#pragma unroll
+      for (int j = 0; j < FC; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) slab.put(8 * (v / 4) + 4 * h + v % 4, 32 * j + r, value(j, v));
+      slab.flush(out, ld, m0 + 32 * i, col, M, cols, v16);
+    };
+    if (o.pre) {
+      auto gate = [&](int j, int v) { return acc[i][2 * j][v]; };
+      auto up = [&](int j, int v) { return acc[i][2 * j + 1][v]; };
+      if (o.pre_bf16) {
+        leave(std::integral_constant<int, 1>{}, o.pre, 2 * F, f0, F, pre_vec, gate);
+        leave(std::integral_constant<int, 1>{}, reinterpret_cast<uint16_t*>(o.pre) + F, 2 * F, f0, F, pre_vec, up);
+      } else {
+        leave(std::integral_constant<int, 0>{}, o.pre, 2 * F, f0, F, pre_vec, gate);
+        leave(std::integral_constant<int, 0>{}, reinterpret_cast<float*>(o.pre) + F, 2 * F, f0, F, pre_vec, up);
+      }
+    }
+    auto value = [&](auto act) {
+      leave(std::integral_constant<int, OUT>{}, o.out, F, f0, F, vec, [&](int j, int v) {
+        return gated_one<decltype(act)::value>(acc[i][2 * j][v], acc[i][2 * j + 1][v]);
+      });
+    };
+    if (o.act == 1) value(std::integral_constant<int, 1>{});
+    else if (o.act == 2) value(std::integral_constant<int, 2>{});
+    else value(std::integral_constant<int, 3>{});
+  }
+}
+
 // ---------------------------------------------------------------- gradient of the activation
 
 // dpre of kPer values a thread; VEC: 16-byte aligned rows, whole pieces.
@@ -175,10 +322,66 @@ hipError_t by_act(int act, F&& go) {
   return go(std::integral_constant<int, 3>{});
 }
 
+template <int V> using Int = std::integral_constant<int, V>;
+
+// The large tiles' loads: 16-byte rows at aligned addresses, and a strip of a tile within 32-bit offsets.
+bool tiled_rows(const void* p, int64_t row_bytes) {
+  return aligned16(p) && row_bytes % 16 == 0 && row_bytes < (int64_t(1) << 23);
+}
+
+template <bool TA, bool TB>
+hipError_t launch_product(const Operand& a, const Operand& b, void* out, int out_bf16, int64_t M, int64_t N, int64_t K,
+                          int num_cus, hipStream_t s) {
+  const int vec = aligned16(out) && N * (out_bf16 ? 2 : 4) % 16 == 0;
+  auto go = [&](auto bm, auto bn, auto stages, auto wy, auto type) {
+    constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value, S = decltype(stages)::value;
+    constexpr int WY = decltype(wy)::value, OUT = decltype(type)::value;
+    const int64_t blocks = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
+    if (blocks > kMaxGrid) return hipErrorInvalidValue;
+    return launch_big_lds<product_kernel<TA, TB, BM, BN, S, WY, 8, OUT>>(S * (BM + BN) * 128, blocks, 512, s, a, b, out, M,
+                                                                         N, K, vec);
+  };
+  auto by_type = [&](auto bm, auto bn, auto stages, auto wy) {
+    return out_bf16 ? go(bm, bn, stages, wy, Int<1>{}) : go(bm, bn, stages, wy, Int<0>{});
+  };
+  if (((M + 255) / 256) * ((N + 255) / 256) >= num_cus) return by_type(Int<256>{}, Int<256>{}, Int<2>{}, Int<2>{});
+  return by_type(Int<128>{}, Int<256>{}, Int<3>{}, Int<2>{});
+}
+
+template <bool TA, bool TB>
+hipError_t launch_product_any(const uint16_t* a, int64_t lda, const uint16_t* b, int64_t ldb, void* out, int out_bf16,
+                              int64_t M, int64_t N, int64_t K, hipStream_t s) {
+  const int64_t blocks = (M + kAnyTile - 1) / kAnyTile * ((N + kAnyTile - 1) / kAnyTile);
+  if (blocks > kMaxGrid) return hipErrorInvalidValue;
+  return launch(product_any_kernel<TA, TB>, dim3(unsigned(blocks)), dim3(kThreads), 0, s, a, lda, b, ldb, out, out_bf16, M,
+                N, K);
+}
+
 }  // namespace
 
 hipError_t launch_gated_gemm(const void* w, int fp8, const uint16_t* x, const GatedOut& o, int64_t M, int64_t F, int64_t K,
                              int num_cus, hipStream_t s) {
+  const int eb = fp8 ? 1 : 2;
+  if (tiled_rows(x, K * 2) && tiled_rows(w, K * eb) && 2 * F * K * eb < kNowhere) {
+    const Operand xo{reinterpret_cast<const char*>(x), 2 * K, M}, wo{static_cast<const char*>(w), K * eb, 2 * F};
+    const int vec = aligned16(o.out) && F * (o.out_bf16 ? 2 : 4) % 16 == 0;
+    const int pre_vec = aligned16(o.pre) && F * (o.pre_bf16 ? 2 : 4) % 16 == 0;
+    auto go = [&](auto bytes, auto bm, auto bf, auto stages, auto wy, auto out) {
+      constexpr int EB = decltype(bytes)::value, BM = decltype(bm)::value, BF = decltype(bf)::value;
+      constexpr int S = decltype(stages)::value, WY = decltype(wy)::value, OUT = decltype(out)::value;
+      using L = ProductLayout<RowsOperand<BM, 8, 2, PlainRows>, RowsOperand<2 * BF, 8, EB, GatedRows>, BM, 2 * BF, S, WY, 8>;
+      const int64_t blocks = ((M + BM - 1) / BM) * ((F + BF - 1) / BF);
+      if (blocks > kMaxGrid) return hipErrorInvalidValue;
+      return launch_big_lds<gated_kernel<EB, BM, BF, S, WY, 8, OUT>>(L::kLds, blocks, 512, s, xo, wo, o, M, F, K, vec,
+                                                                     pre_vec);
+    };
+    auto by_tile = [&](auto bytes, auto out) {
+      if (M > 128) return go(bytes, Int<256>{}, Int<128>{}, Int<2>{}, Int<2>{}, out);
+      return go(bytes, Int<64>{}, Int<128>{}, Int<3>{}, Int<2>{}, out);
+    };
+    auto by_out = [&](auto bytes) { return o.out_bf16 ? by_tile(bytes, Int<1>{}) : by_tile(bytes, Int<0>{}); };
+    return fp8 ? by_out(Int<1>{}) : by_out(Int<2>{});
+  }
   const int64_t blocks = (M + kAnyTile - 1) / kAnyTile * ((F + 31) / 32);
   if (blocks > kMaxGrid) return hipErrorInvalidValue;
   if (fp8)
@@ -209,19 +412,19 @@ hipError_t launch_gated_grad(const void* dy, int dy_bf16, const void* pre, int p
 // dx[m, k] = sum_n dout[m, n] w[n, k]
 hipError_t launch_bf16_grad_x(const uint16_t* dout, const uint16_t* w, void* dx, int dx_bf16, int64_t M, int64_t N,
                               int64_t K, int num_cus, hipStream_t s) {
-  const int64_t blocks = (M + kAnyTile - 1) / kAnyTile * ((K + kAnyTile - 1) / kAnyTile);
-  if (blocks > kMaxGrid) return hipErrorInvalidValue;
-  return launch(product_any_kernel<false, true>, dim3(unsigned(blocks)), dim3(kThreads), 0, s, dout, N, w, K, dx, dx_bf16,
-                M, K, N);
+  if (tiled_rows(dout, 2 * N) && tiled_rows(w, 2 * K))
+    return launch_product<false, true>(Operand{reinterpret_cast<const char*>(dout), 2 * N, M},
+                                       Operand{reinterpret_cast<const char*>(w), 2 * K, N}, dx, dx_bf16, M, K, N, num_cus, s);
+  return launch_product_any<false, true>(dout, N, w, K, dx, dx_bf16, M, K, N, s);
 }
 
 // dw[n, k] = sum_m dout[m, n] x[m, k]
 hipError_t launch_bf16_grad_w(const uint16_t* dout, const uint16_t* x, void* dw, int dw_bf16, int64_t M, int64_t N,
                               int64_t K, int num_cus, hipStream_t s) {
-  const int64_t blocks = (N + kAnyTile - 1) / kAnyTile * ((K + kAnyTile - 1) / kAnyTile);
-  if (blocks > kMaxGrid) return hipErrorInvalidValue;
-  return launch(product_any_kernel<true, true>, dim3(unsigned(blocks)), dim3(kThreads), 0, s, dout, N, x, K, dw, dw_bf16,
-                N, K, M);
+  if (tiled_rows(dout, 2 * N) && tiled_rows(x, 2 * K))
+    return launch_product<true, true>(Operand{reinterpret_cast<const char*>(dout), 2 * N, M},
+                                      Operand{reinterpret_cast<const char*>(x), 2 * K, M}, dw, dw_bf16, N, K, M, num_cus, s);
+  return launch_product_any<true, true>(dout, N, x, K, dw, dw_bf16, N, K, M, s);
 }
 
 }  // namespace qlinear

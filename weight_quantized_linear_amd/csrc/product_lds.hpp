@@ -1,0 +1,263 @@
+// A tile of C[m, n] = sum_k A[m, k] B[n, k] on the matrix cores, with either operand stored
+// along k ("rows": [M, K], bfloat16 or FP8) or across it ("turned": [K, M], bfloat16).
+//
+// * A block of NW waves owns BM x BN, a wave (BM / WY) x (BN / WX) of 32 x 32 MFMA blocks. K goes in strips of 64
+//   through a ring of S LDS stages, filled by loads that write LDS directly; a strip is four
+//   steps of 16, and while the matrix cores work on one, the operands of the next are read.
+// * Rows operands lie in LDS as 128-byte rows (FP8: 64) with their 16-byte pieces permuted; a lane
+//   reads the 8 values of its row with one load (FP8: 16 values for two steps, widened exactly).
+// * Turned operands lie as 64 rows of k.  The transposing LDS read hands lane l of 16 the values k .. k + 3
+//   of column l from four rows: two reads give the 8 values that the MFMA wants.  Their 64-byte pieces
+//   are permuted by k so that the four rows of a read lie in different banks.
+// * Inside a strip, lane half h takes k = 32 t + 16 h + 8 e .. + 7 in step 2 t + e, for both operands.
+// * The strips' addresses move in the buffer resource, 64 bits wide, so an operand may be larger than 4 GiB; what
+//   lies past the operand's end is zero by the resource's bound, and in the last strip of a rows
+//   operand what lies past K is sent past that bound.
+#pragma once
+
+#include "lds_gemm.hpp"
+
+namespace qlinear {
+
+constexpr int kStripK = 64;
+
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4s lds_v4s_t;
+
+// Where an operand lies: rows operand: `ld` bytes a row of k; turned: `ld` bytes a row of the
+// other axis, K rows.
+struct Operand {
+  const char* p;
+  int64_t ld;
+  int64_t extent;  // rows operand: its rows; turned: K
+};
+
+constexpr uint32_t kNowhere = 0xFFFFFFF0u;  // an offset past every resource's bound
+
+// A resource of `bytes` bytes at p, bounded so that kNowhere lies outside; none: nothing lies inside.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t strip_rsrc(const char* p, int64_t bytes, bool none) {
+  return make_rsrc(p, none ? 0 : bytes < int64_t(kNowhere) ? bytes : int64_t(kNowhere));
+}
+
+// Row r of the tile is row `first + r` of the operand.
+struct PlainRows {
+  int64_t first, rows;
+  __device__ __forceinline__ int64_t at(int r) const { return r; }
+  __device__ __forceinline__ bool in(int r) const { return first + r < rows; }
+};
+// Of every 64 rows of the tile 32 are gate rows and 32 the up rows of the same columns.
+struct GatedRows {
+  int64_t first, rows;  // of F
+  __device__ __forceinline__ int64_t at(int r) const { return r / 64 * 32 + r % 32 + (r / 32 % 2 ? rows : 0); }
+  __device__ __forceinline__ bool in(int r) const { return first + r / 64 * 32 + r % 32 < rows; }
+};
+
+// ROWS rows of 64 values of k, EB bytes each (2: bfloat16, 1: FP8).
+template <int ROWS, int NW, int EB, class Map>
+struct RowsOperand {
+  static constexpr int kRowBytes = kStripK * EB, kCpr = kRowBytes / 16, kBytes = ROWS * kRowBytes;
+  static constexpr int kInst = ROWS * kCpr / (64 * NW);
+  static_assert(ROWS * kCpr % (64 * NW) == 0, "whole instructions");
+  static constexpr bool kPairs = EB == 1;  // one read serves two steps
+  const char* base;
+  int64_t bytes;  // from base to the operand's end
+  uint32_t off[kInst], tail[kInst];
+
+  __device__ __forceinline__ void init(const Operand& o, const Map& map, int64_t K) {
+    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+    base = o.p + map.first * o.ld;
+    bytes = (o.extent - map.first) * o.ld;
+#pragma unroll
+    for (int q = 0; q < kInst; ++q) {
+      const int c = (q * NW + wid) * 64 + lane, r = c / kCpr, g = (c % kCpr) ^ swz<kCpr>(r);
+      off[q] = map.in(r) ? uint32_t(map.at(r) * o.ld + 16 * g) : kNowhere;
+      const int left = int(K % kStripK) * EB;  // bytes of a row in the last strip, 0: all
+      tail[q] = left && 16 * g >= left ? kNowhere : off[q];
+    }
+  }
+  __device__ __forceinline__ void fetch(char* tile, int64_t strip, bool last, bool none) const {
+    const int wid = threadIdx.x >> 6;
+    const int64_t at = strip * kRowBytes;
+    const __amdgpu_buffer_rsrc_t r = strip_rsrc(base + at, bytes - at, none);
+#pragma unroll
+    for (int q = 0; q < kInst; ++q) bdma16(r, tile + (q * NW + wid) * 1024, last ? tail[q] : off[q], 0);
+  }
+};
+
+// 64 rows of k, COLS values (bfloat16) each.
+template <int COLS, int NW>
+struct TurnedOperand {
+  static constexpr int kRowBytes = COLS * 2, kCpr = kRowBytes / 16, kBytes = kStripK * kRowBytes;
+  static constexpr int kInst = kStripK * kCpr / (64 * NW);
+  static_assert(kStripK * kCpr % (64 * NW) == 0 && kCpr >= 16, "whole instructions");
+  static constexpr bool kPairs = false;
+  const char* base;
+  int64_t bytes, step;
+  uint32_t off[kInst];
+
+  __device__ __forceinline__ void init(const Operand& o, const PlainRows& map, int64_t) {
+    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+    base = o.p + map.first * 2;
+    bytes = o.extent * o.ld - map.first * 2;
+    step = kStripK * o.ld;
+#pragma unroll
+    for (int q = 0; q < kInst; ++q) {
+      const int c = (q * NW + wid) * 64 + lane, k = c / kCpr, g = (c % kCpr) ^ ((k & 3) << 2);
+      off[q] = uint32_t(k * o.ld + 16 * g);
+    }
+  }
+  __device__ __forceinline__ void fetch(char* tile, int64_t strip, bool, bool none) const {
+    const int wid = threadIdx.x >> 6;
+    const int64_t at = strip * step;
+    const __amdgpu_buffer_rsrc_t r = strip_rsrc(base + at, bytes - at, none);
+#pragma unroll
+    for (int q = 0; q < kInst; ++q) bdma16(r, tile + (q * NW + wid) * 1024, off[q], 0);
+  }
+};
+
+// The wave's fragments of NF blocks of 32 rows from `row0` on.
+template <class Op, int NF> struct Fragments;
+
+template <int ROWS, int NW, class Map, int NF>
+struct Fragments<RowsOperand<ROWS, NW, 2, Map>, NF> {
+  static constexpr int kReads = NF;  // LDS reads of a step
+  uint32_t at[4];
+  __device__ __forceinline__ void init(int row0) {
+    const int r = threadIdx.x & 31, h = (threadIdx.x >> 5) & 1;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) at[u] = uint32_t((row0 + r) * 128 + 16 * ((4 * (u / 2) + 2 * h + u % 2) ^ swz<8>(r)));
+  }
+  template <int U>
+  __device__ __forceinline__ void read(const char* tile, v8bf (&f)[NF]) {
+#pragma unroll
+    for (int j = 0; j < NF; ++j) f[j] = __builtin_bit_cast(v8bf, lds16(tile + at[U] + j * 32 * 128));
+  }
+};
+
+template <int ROWS, int NW, class Map, int NF>
+struct Fragments<RowsOperand<ROWS, NW, 1, Map>, NF> {
+  static constexpr int kReads = NF;
+  uint32_t at[2];
+  u32x4 raw[NF];
+  __device__ __forceinline__ void init(int row0) {
+    const int r = threadIdx.x & 31, h = (threadIdx.x >> 5) & 1;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) at[t] = uint32_t((row0 + r) * 64 + 16 * ((2 * t + h) ^ swz<4>(r)));
+  }
+  template <int U>
+  __device__ __forceinline__ void read(const char* tile, v8bf (&f)[NF]) {
+#pragma unroll
+    for (int j = 0; j < NF; ++j) {
+      if constexpr (U % 2 == 0) raw[j] = lds16(tile + at[U / 2] + j * 32 * 64);
+      f[j] = U % 2 == 0 ? e4m3x8_to_bf16x8(raw[j].x, raw[j].y) : e4m3x8_to_bf16x8(raw[j].z, raw[j].w);
+    }
+  }
+};
+
+template <int COLS, int NW, int NF>
+struct Fragments<TurnedOperand<COLS, NW>, NF> {
+  static constexpr int kReads = 2 * NF;
+  uint32_t at[NF];
+  // Lane 16 g + 4 j + c of a read supplies k row j of its half's eight (+ 4 in the second read), columns 16 (g % 2) + 4 c.
+  __device__ __forceinline__ void init(int row0) {
+    const int lane = threadIdx.x & 63, j = lane / 4 % 4, h = lane / 32;
+#pragma unroll
+    for (int n = 0; n < NF; ++n) {
+      const int byte = (row0 + 32 * n + 16 * (lane / 16 % 2) + 4 * (lane % 4)) * 2;
+      at[n] = uint32_t((16 * h + j) * COLS * 2 + (byte ^ (j << 6)));
+    }
+  }
+  template <int U>
+  __device__ __forceinline__ void read(const char* tile, v8bf (&f)[NF]) {
+    constexpr int k = 32 * (U / 2) + 8 * (U % 2);
+#pragma unroll
+    for (int n = 0; n < NF; ++n) {
+      char* p = const_cast<char*>(tile) + at[n] + k * COLS * 2;
+      const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t*)p);
+      const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t*)(p + 4 * COLS * 2));
+      f[n] = __builtin_bit_cast(v8bf, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  }
+};
+
+template <class AOp, class BOp, int BM, int BN, int S, int WY, int NW>
+struct ProductLayout {
+  static constexpr int WX = NW / WY, FM = BM / WY / 32, FN = BN / WX / 32;
+  static constexpr int kStage = AOp::kBytes + BOp::kBytes, kLds = S * kStage;
+  static constexpr int kLoads = AOp::kInst + BOp::kInst;
+  static_assert(kLds <= 160 * 1024 && (S - 1) * kLoads < 64 && S >= 2, "ring");
+};
+
+// The sums of the tile whose operands `a` and `b` were set to: acc[i][j][v] belongs to row
+// 32 i + 8 (v / 4) + 4 h + v % 4 and column 32 j + lane % 32 of the wave's part.
+template <class AOp, class BOp, int BM, int BN, int S, int WY, int NW>
+__device__ __forceinline__ void product_tile(
+    char* lds, const AOp& a, const BOp& b, int64_t K,
+    v16f (&acc)[ProductLayout<AOp, BOp, BM, BN, S, WY, NW>::FM][ProductLayout<AOp, BOp, BM, BN, S, WY, NW>::FN]) {
+  using L = ProductLayout<AOp, BOp, BM, BN, S, WY, NW>;
+  constexpr int FM = L::FM, FN = L::FN, NM = FM * FN;
+  const int wid = threadIdx.x >> 6;
+  Fragments<AOp, FM> fa;
+  Fragments<BOp, FN> fb;
+  fa.init(wid / L::WX * (BM / WY));
+  fb.init(wid % L::WX * (BN / L::WX));
+  const int64_t nk = (K + kStripK - 1) / kStripK;
+  auto fetch = [&](int64_t s) {
+    char* st = lds + int(s % S) * L::kStage;
+    const bool last = s == nk - 1, none = s >= nk;
+    a.fetch(st, none ? 0 : s, last, none);
+    b.fetch(st + AOp::kBytes, none ? 0 : s, last, none);
+  };
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = v16f{};
+  v8bf aX[FM], aY[FM], bX[FN], bY[FN];
+  auto mma = [&](const v8bf (&x)[FM], const v8bf (&y)[FN]) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], y[j], acc[i][j], 0, 0, 0);
+  };
+  constexpr int kReads = Fragments<AOp, FM>::kReads + Fragments<BOp, FN>::kReads;
+#pragma unroll
+  for (int s = 0; s < S; ++s) fetch(s);
+  wait_vm<(S - 1) * L::kLoads>();
+  block_barrier();
+  fa.template read<0>(lds, aX);
+  fb.template read<0>(lds + AOp::kBytes, bX);
+  auto inner = [&](const char* st) {
+    const char* sb = st + AOp::kBytes;
+    fa.template read<1>(st, aY);
+    fb.template read<1>(sb, bY);
+    mma(aX, bX);
+    interleave<NM, 0, kReads, 0>();
+    fa.template read<2>(st, aX);
+    fb.template read<2>(sb, bX);
+    mma(aY, bY);
+    interleave<NM, 0, kReads, 0>();
+    fa.template read<3>(st, aY);
+    fb.template read<3>(sb, bY);
+    mma(aX, bX);
+    interleave<NM, 0, kReads, 0>();
+  };
+  for (int64_t kt = 0; kt < nk - 1; ++kt) {
+    inner(lds + int(kt % S) * L::kStage);
+    // Into the next strip: it has landed for every wave after the barrier, and this one's slot is free
+    // once every wave's reads of it returned.
+    wait_lds();
+    wait_vm<(S - 2) * L::kLoads>();
+    block_barrier();
+    fetch(kt + S);
+    const char* sn = lds + int((kt + 1) % S) * L::kStage;
+    fa.template read<0>(sn, aX);
+    fb.template read<0>(sn + AOp::kBytes, bX);
+    mma(aY, bY);
+    interleave<NM, L::kLoads, kReads, 0>();
+  }
+  inner(lds + int((nk - 1) % S) * L::kStage);
+  mma(aY, bY);
+  wait_vm<0>();  // no LDS write may land after the block ends
+}
+
+}  // namespace qlinear
