@@ -104,7 +104,8 @@ def check_forward(q, rng, m, f, k, fp8, act, out_dtype, addend=None, odd=False):
 
 
 SHAPES = [(1, 1, 1), (1, 16, 32), (2, 5, 7), (3, 33, 64), (4, 40, 100), (1, 130, 1023), (5, 64, 65), (16, 48, 256), (17, 31, 130),
-          (33, 64, 64), (64, 128, 512), (65, 100, 96), (100, 257, 320), (130, 384, 1024), (300, 70, 2050)]
+          (33, 64, 64), (64, 128, 512), (65, 100, 96), (100, 257, 320), (130, 384, 1024), (300, 70, 2050),
+          (3, 40, 2056), (16, 24, 8192), (9, 17, 4104), (5, 70, 6000), (4, 21, 16400), (2, 9, 517)]
 
 
 @pytest.mark.parametrize("fp8", [False, True])

@@ -14,7 +14,6 @@
 // A row belongs to TPR threads (64 .. 512, whole waves), V values each in pieces of 8
 // (V / 8 16-byte loads of bfloat16, twice as many of float32), so a wave's load covers
 // 1 KiB of the row.  Rows of up to 64 * 8 values are one wave's and take no barrier.
-#include <initializer_list>
 #include <type_traits>
 
 #include "device.hpp"
@@ -27,35 +26,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPiece = 8;  // values of a thread that lie together
-
-// Eight values at p + i as float32; past `end` zeros.  VEC: 16-byte aligned and whole pieces.
-template <int BF16, bool VEC>
-__device__ __forceinline__ void load8(const void* p, int64_t i, int64_t left, float (&f)[8]) {
-  if constexpr (VEC) {
-    if (left >= kPiece) {
-      load_eight<BF16>(p, i, f);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = 0.f;
-    }
-  } else {
-    const auto* q = reinterpret_cast<const typename Elem<BF16>::T*>(p) + i;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = e < left ? Elem<BF16>::get(q[e]) : 0.f;
-  }
-}
-
-template <int BF16, bool VEC>
-__device__ __forceinline__ void store8(void* p, int64_t i, int64_t left, const float (&f)[8]) {
-  if constexpr (VEC) {
-    if (left >= kPiece) store_eight<BF16>(p, i, f);
-  } else {
-    auto* q = reinterpret_cast<typename Elem<BF16>::T*>(p) + i;
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < left) q[e] = Elem<BF16>::put(f[e]);
-  }
-}
 
 // The value as the type holds it.
 template <int BF16>
@@ -92,8 +62,9 @@ struct NormArgs {
   float scale, eps;
 };
 
-// R, IO, P: element types of the residual, of block output and y, of the parameters.
-template <int R, int IO, int P, int TPR, int V, bool VEC>
+// R, IO, P: element types of the residual, of block output and y, of the parameters.  TAIL: H % 8 != 0.
+// Bound by HBM: FWDFIGURE
+template <int R, int IO, int P, int TPR, int V, bool TAIL>
 __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void norm_kernel(NormArgs a) {
   constexpr int THREADS = TPR > kThreads ? TPR : kThreads, ROWS = THREADS / TPR, C = V / kPiece;
   __shared__ float part[4][THREADS / kWave];
@@ -104,15 +75,28 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void norm_kernel(N
   for (int64_t t0 = int64_t(blockIdx.x) * ROWS; t0 < a.T; t0 += int64_t(gridDim.x) * ROWS, turn ^= 2) {
     const bool live = t0 + mine < a.T;
     const int64_t t = live ? t0 + mine : a.T - 1, at = t * a.H;
-    float r[C][8], o[C][8];
+    const int64_t grow = a.gate ? t / a.per * a.H : 0;
+    // Everything that the row needs is on its way before the first sum waits.
+    Eight<R> r8[C];
+    Eight<IO> o8[C];
+    Eight<P> w8[C], wo8[C], g8[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int64_t i = int64_t(c * TPR + lane) * kPiece;
-      load8<R, VEC>(a.res, at + i, a.H - i, r[c]);
-      if (a.block) load8<IO, VEC>(a.block, at + i, a.H - i, o[c]);
+      r8[c].template load<TAIL>(a.res, at + i, a.H - i);
+      if (a.block) o8[c].template load<TAIL>(a.block, at + i, a.H - i);
+      w8[c].template load<TAIL>(a.w, i, a.H - i);
+      if (a.wo) wo8[c].template load<TAIL>(a.wo, i, a.H - i);
+      if (a.gate) g8[c].template load<TAIL>(a.gate, grow + i, a.H - i);
     }
+    float r[C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c) r8[c].get(r[c]);
     if (a.block) {
+      float o[C][8];
       float inv = 1.f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) o8[c].get(o[c]);
       if (a.wo) {
         float s = 0.f;
 #pragma unroll
@@ -121,25 +105,26 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void norm_kernel(N
           for (int e = 0; e < 8; ++e) s = fmaf(o[c][e], o[c][e], s);
         inv = rsqrtf(row_sum<TPR, THREADS>(s, part[turn]) * inv_h + a.eps);
       }
-      const int64_t grow = a.gate ? t / a.per * a.H : 0;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const int64_t i = int64_t(c * TPR + lane) * kPiece;
         if (a.wo) {
           float w[8];
-          load8<P, VEC>(a.wo, i, a.H - i, w);
+          wo8[c].get(w);
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[c][e] = o[c][e] * inv * w[e];
         }
         if (a.gate) {
           float g[8];
-          load8<P, VEC>(a.gate, grow + i, a.H - i, g);
+          g8[c].get(g);
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[c][e] *= g[e];
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[c][e] = stored<R>(fmaf(a.scale, r[c][e], o[c][e]));
-        if (live) store8<R, VEC>(a.res_out, at + i, a.H - i, r[c]);
+        for (int e = 0; e < 8; ++e) r[c][e] = fmaf(a.scale, r[c][e], o[c][e]);
+        r8[c].put(r[c]);
+        r8[c].get(r[c]);  // as it is stored
+        if (live) r8[c].template store<TAIL>(a.res_out, at + i, a.H - i);
       }
     }
     float s = 0.f;
@@ -152,10 +137,12 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void norm_kernel(N
     for (int c = 0; c < C; ++c) {
       const int64_t i = int64_t(c * TPR + lane) * kPiece;
       float w[8];
-      load8<P, VEC>(a.w, i, a.H - i, w);
+      w8[c].get(w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] = r[c][e] * inv * w[e];
-      if (live) store8<IO, VEC>(a.y, at + i, a.H - i, w);
+      Eight<IO> y;
+      y.put(w);
+      if (live) y.template store<TAIL>(a.y, at + i, a.H - i);
     }
   }
 }
@@ -168,34 +155,71 @@ struct NormGradArgs {
   float scale, eps;
 };
 
-// A worker is the TPR threads of a row.  It takes `rows` rows one after the other and keeps
-// the columns' sums in registers; the workers' sums are added afterwards in their order.  A
-// gate whose rows lie in one worker's range is finished by it; of others it leaves a part:
-// [0] of the gate that its range begins in the middle of, [1] of the one that it ends in the middle of.
-template <int R, int IO, int P, int TPR, int V, bool VEC>
+// A worker is the TPR threads of a row.  It takes `rows` rows one after the other and keeps the columns'
+// sums in registers; the workers' sums are added afterwards in their order.  Gates of no more rows than a
+// worker's lie whole in one (rows is a multiple of theirs) and are finished by it; of others it leaves parts:
+// [0] of the gate that its range begins in the middle of, [1] of the one that begins in its range.
+// With V = 8 the parameters stay in registers and the next row is on its way while one is worked on; wider
+// rows have no registers for that.
+template <int R, int IO, int P, int TPR, int V, bool TAIL>
 __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void norm_grad_kernel(NormGradArgs a) {
   constexpr int THREADS = TPR > kThreads ? TPR : kThreads, WORKERS = THREADS / TPR, C = V / kPiece;
+  constexpr bool kAhead = V == 8;
   __shared__ float part[6][THREADS / kWave];
   const int lane = threadIdx.x % TPR;
   const float inv_h = 1.f / float(a.H);
   const int64_t worker = int64_t(blockIdx.x) * WORKERS + threadIdx.x / TPR;
   const int64_t begin = worker * a.rows, end = begin + a.rows < a.T ? begin + a.rows : a.T;
+  const bool with_o = a.wo || a.gate;
+  auto piece = [&](int c) { return int64_t(c * TPR + lane) * kPiece; };
+
+  struct Row {
+    Eight<R> r[C], dr[C];
+    Eight<IO> dy[C], o[C];
+  };
+  auto row_of = [&](int64_t n) { return begin + n < a.T ? begin + n : a.T - 1; };
+  auto load = [&](Row& row, int64_t t) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int64_t i = piece(c), at = t * a.H + i;
+      row.r[c].template load<TAIL>(a.res, at, a.H - i);
+      row.dy[c].template load<TAIL>(a.dy, at, a.H - i);
+      if (a.dres_in) row.dr[c].template load<TAIL>(a.dres_in, at, a.H - i);
+      if (with_o) row.o[c].template load<TAIL>(a.block, at, a.H - i);
+    }
+  };
+  auto parameter = [&](const void* p, int64_t at, int c, float (&f)[8]) {
+    Eight<P> v;
+    v.template load<TAIL>(p, at + piece(c), a.H - piece(c));
+    v.get(f);
+  };
+  float w[C][8], wo[C][8], g[C][8];
+  if (kAhead) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      parameter(a.w, 0, c, w[c]);
+      if (a.wo) parameter(a.wo, 0, c, wo[c]);
+    }
+  }
+  int64_t held = -1;  // the gate in g
   float sw[C][8], swo[C][8], sg[C][8];
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int e = 0; e < 8; ++e) sw[c][e] = swo[c][e] = sg[c][e] = 0.f;
+  Row cur, next;
+  load(cur, row_of(0));
   int turn = 0;
   for (int64_t n = 0; n < a.rows; ++n, turn = 3 - turn) {  // as many turns for every worker of the block: barriers
     const bool live = begin + n < end;
-    const int64_t t = live ? begin + n : a.T - 1, at = t * a.H;
+    const int64_t t = row_of(n), at = t * a.H;
+    if (kAhead) load(next, row_of(n + 1 < a.rows ? n + 1 : n));
     float r[C][8], dy[C][8];
     float s = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int64_t i = int64_t(c * TPR + lane) * kPiece;
-      load8<R, VEC>(a.res, at + i, a.H - i, r[c]);
-      load8<IO, VEC>(a.dy, at + i, a.H - i, dy[c]);
+      cur.r[c].get(r[c]);
+      cur.dy[c].get(dy[c]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) s = fmaf(r[c][e], r[c][e], s);
     }
@@ -203,14 +227,12 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void norm_grad_ker
     s = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int64_t i = int64_t(c * TPR + lane) * kPiece;
-      float w[8];
-      load8<P, VEC>(a.w, i, a.H - i, w);
+      if (!kAhead) parameter(a.w, 0, c, w[c]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         r[c][e] *= inv;
         if (live) sw[c][e] = fmaf(dy[c][e], r[c][e], sw[c][e]);
-        dy[c][e] *= w[e];
+        dy[c][e] *= w[c][e];
         s = fmaf(dy[c][e], r[c][e], s);
       }
     }
@@ -218,89 +240,102 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void norm_grad_ker
     float d[C][8];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int64_t i = int64_t(c * TPR + lane) * kPiece;
       float in[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (a.dres_in) load8<R, VEC>(a.dres_in, at + i, a.H - i, in);
+      if (a.dres_in) cur.dr[c].get(in);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         d[c][e] = fmaf(inv, fmaf(-r[c][e], mean, dy[c][e]), in[e]);
         in[e] = a.scale * d[c][e];
       }
-      if (live) store8<R, VEC>(a.dres, at + i, a.H - i, in);
+      Eight<R> out;
+      out.put(in);
+      if (live) out.template store<TAIL>(a.dres, at + piece(c), a.H - piece(c));
     }
-    if (!a.block) continue;
-    const int64_t grow = a.gate ? t / a.per : 0;
-    float o[C][8];
-    float inv_o = 1.f;
-    if (a.wo || a.gate) {
+    if (a.block) {
+      const int64_t gate = a.gate ? t / a.per : 0;
+      float o[C][8];
+      float inv_o = 1.f;
+      if (with_o) {
+        s = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          cur.o[c].get(o[c]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s = fmaf(o[c][e], o[c][e], s);
+        }
+        if (a.wo) inv_o = rsqrtf(row_sum<TPR, THREADS>(s, part[turn + 2]) * inv_h + a.eps);
+      }
+      if (a.gate && (!kAhead || gate != held)) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) parameter(a.gate, gate * a.H, c, g[c]);
+        held = gate;
+      }
       s = 0.f;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int64_t i = int64_t(c * TPR + lane) * kPiece;
-        load8<IO, VEC>(a.block, at + i, a.H - i, o[c]);
+        if (!kAhead && a.wo) parameter(a.wo, 0, c, wo[c]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s = fmaf(o[c][e], o[c][e], s);
-      }
-      if (a.wo) inv_o = rsqrtf(row_sum<TPR, THREADS>(s, part[turn + 2]) * inv_h + a.eps);
-    }
-    s = 0.f;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int64_t i = int64_t(c * TPR + lane) * kPiece;
-      float g[8], w[8];
-      if (a.gate) load8<P, VEC>(a.gate, grow * a.H + i, a.H - i, g);
-      if (a.wo) load8<P, VEC>(a.wo, i, a.H - i, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (a.wo) o[c][e] *= inv_o;
-        if (a.gate) {
-          if (live) sg[c][e] = fmaf(d[c][e], a.wo ? o[c][e] * w[e] : o[c][e], sg[c][e]);
-          d[c][e] *= g[e];
-        }
-        if (a.wo) {
-          if (live) swo[c][e] = fmaf(d[c][e], o[c][e], swo[c][e]);
-          d[c][e] *= w[e];
-          s = fmaf(d[c][e], o[c][e], s);
+        for (int e = 0; e < 8; ++e) {
+          if (a.wo) o[c][e] *= inv_o;
+          if (a.gate) {
+            if (live) sg[c][e] = fmaf(d[c][e], a.wo ? o[c][e] * wo[c][e] : o[c][e], sg[c][e]);
+            d[c][e] *= g[c][e];
+          }
+          if (a.wo) {
+            if (live) swo[c][e] = fmaf(d[c][e], o[c][e], swo[c][e]);
+            d[c][e] *= wo[c][e];
+            s = fmaf(d[c][e], o[c][e], s);
+          }
         }
       }
-    }
-    float mean_o = 0.f;
-    if (a.wo) mean_o = row_sum<TPR, THREADS>(s, part[turn]) * inv_h;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int64_t i = int64_t(c * TPR + lane) * kPiece;
-      if (a.wo) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) d[c][e] = inv_o * fmaf(-o[c][e], mean_o, d[c][e]);
-      }
-      if (live) store8<IO, VEC>(a.dblock, at + i, a.H - i, d[c]);
-    }
-    // The gate's last row of this range: its sum leaves.
-    if (a.gate && live && (t + 1 == end || (t + 1) % a.per == 0)) {
-      const int64_t first = grow * a.per;
-      const bool whole = first >= begin && first + a.per <= end;
+      float mean_o = 0.f;
+      if (a.wo) mean_o = row_sum<TPR, THREADS>(s, part[turn]) * inv_h;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int64_t i = int64_t(c * TPR + lane) * kPiece;
-        if (whole) store8<P, VEC>(a.dgate, grow * a.H + i, a.H - i, sg[c]);
-        else store8<0, VEC>(a.part_gate, (2 * worker + (first >= begin)) * a.H + i, a.H - i, sg[c]);
+        if (a.wo) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sg[c][e] = 0.f;
+          for (int e = 0; e < 8; ++e) d[c][e] = inv_o * fmaf(-o[c][e], mean_o, d[c][e]);
+        }
+        Eight<IO> out;
+        out.put(d[c]);
+        if (live) out.template store<TAIL>(a.dblock, at + piece(c), a.H - piece(c));
+      }
+      // The gate's last row of this range: its sum leaves.
+      if (a.gate && live && (t + 1 == end || (t + 1) % a.per == 0)) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          if (a.per <= a.rows) {
+            Eight<P> out;
+            out.put(sg[c]);
+            out.template store<TAIL>(a.dgate, gate * a.H + piece(c), a.H - piece(c));
+          } else {
+            Eight<0> out;
+            out.put(sg[c]);
+            out.template store<TAIL>(a.part_gate, (2 * worker + (gate * a.per >= begin)) * a.H + piece(c), a.H - piece(c));
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sg[c][e] = 0.f;
+        }
       }
     }
+    if (kAhead) cur = next;
+    else if (n + 1 < a.rows) load(cur, row_of(n + 1));
   }
   if (begin >= a.T) return;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int64_t i = int64_t(c * TPR + lane) * kPiece;
-    store8<0, VEC>(a.part_w, worker * a.H + i, a.H - i, sw[c]);
-    if (a.wo) store8<0, VEC>(a.part_wo, worker * a.H + i, a.H - i, swo[c]);
+    Eight<0> out;
+    out.put(sw[c]);
+    out.template store<TAIL>(a.part_w, worker * a.H + piece(c), a.H - piece(c));
+    if (a.wo) {
+      out.put(swo[c]);
+      out.template store<TAIL>(a.part_wo, worker * a.H + piece(c), a.H - piece(c));
+    }
   }
 }
 
-// Adds the workers' sums in their order: 64 columns a block, its 16 waves a sixteenth of the
-// workers each.  blockIdx.y: 0 dw, 1 dw_o, from 2 on the gate that worker y - 1 begins in the
-// middle of, if worker y - 2 holds that gate's first row.
+// Adds the workers' sums in their order: 64 columns a block, each of its 16 waves every sixteenth worker.
+// blockIdx.y: 0 dw, 1 dw_o, from 2 on the gates, where they have more rows than a worker.
 struct NormJoinArgs {
   const float *part_w, *part_wo, *part_gate;
   void *dw, *dwo, *dgate;
@@ -314,30 +349,35 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void norm_join_kernel(NormJoinAr
   const int lane = threadIdx.x % kWave, wid = threadIdx.x / kWave;
   const int64_t col = int64_t(blockIdx.x) * kWave + lane;
   const bool live = col < a.H;
-  const float* src;
-  void* out;
-  int64_t count, stride = a.H, first_at = 0, next_at, at = 0;  // terms: first_at, then next_at + n stride
-  if (blockIdx.y < 2) {
-    src = blockIdx.y ? a.part_wo : a.part_w;
-    out = blockIdx.y ? a.dwo : a.dw;
-    if (!out) return;
-    count = a.workers;
-    next_at = a.H;
-  } else {
-    const int64_t worker = blockIdx.y - 1, begin = worker * a.rows, g = begin / a.per, first = g * a.per;
-    if (first >= begin || first < begin - a.rows) return;
-    const int64_t last = (first + a.per - 1) / a.rows;  // the worker of the gate's last row
+  const float* src = blockIdx.y ? a.part_wo : a.part_w;  // term n: the first at first_at, then next_at + (n - 1) stride
+  void* out = blockIdx.y ? a.dwo : a.dw;
+  int64_t count = a.workers, stride = a.H, first_at = 0, next_at = a.H, at = 0;
+  if (blockIdx.y >= 2) {
+    const int64_t g = blockIdx.y - 2, w0 = g * a.per / a.rows, w1 = ((g + 1) * a.per - 1) / a.rows;  // its workers
     src = a.part_gate;
     out = a.dgate;
     stride = 2 * a.H;
-    first_at = (2 * (worker - 1) + 1) * a.H;
-    next_at = 2 * worker * a.H;
-    count = last - worker + 2;
+    first_at = (2 * w0 + 1) * a.H;  // the gate begins in the first worker's range, and the others begin in it
+    next_at = 2 * (w0 + 1) * a.H;
+    count = w1 - w0 + 1;
     at = g * a.H;
   }
+  if (!out) return;
   float s = 0.f;
-  if (live)
-    for (int64_t n = wid; n < count; n += kJoinWaves) s += src[(n ? next_at + (n - 1) * stride : first_at) + col];
+  if (live) {
+    int64_t n = wid;
+    for (; n + 7 * kJoinWaves < count; n += 8 * kJoinWaves) {  // eight loads on their way at once
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int64_t m = n + e * kJoinWaves;
+        v[e] = src[(m ? next_at + (m - 1) * stride : first_at) + col];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += v[e];
+    }
+    for (; n < count; n += kJoinWaves) s += src[(n ? next_at + (n - 1) * stride : first_at) + col];
+  }
   part[wid][lane] = s;
   __syncthreads();
   if (wid || !live) return;
@@ -362,33 +402,28 @@ auto by_width(int64_t H, F&& go) {
   return go(RowShape<512, 32>{});
 }
 
-bool all_vec(int64_t H, std::initializer_list<const void*> ps) {
-  if (H % kPiece) return false;
-  for (const void* p : ps)
-    if (reinterpret_cast<uintptr_t>(p) % 16) return false;
-  return true;
-}
-
-template <int R_, int IO_, int P_, bool VEC_> struct RowTypes {
+template <int R_, int IO_, int P_, bool TAIL_> struct RowTypes {
   static constexpr int R = R_, IO = IO_, P = P_;
-  static constexpr bool VEC = VEC_;
+  static constexpr bool TAIL = TAIL_;
 };
 template <typename F>
-hipError_t by_types(int r, int io, int p, bool vec, F&& go) {
-  auto with = [&](auto vec_) {
-    constexpr bool VEC = decltype(vec_)::value;
-    if (r) return p ? go(RowTypes<1, 1, 1, VEC>{}) : go(RowTypes<1, 1, 0, VEC>{});
-    if (io) return p ? go(RowTypes<0, 1, 1, VEC>{}) : go(RowTypes<0, 1, 0, VEC>{});
-    return p ? go(RowTypes<0, 0, 1, VEC>{}) : go(RowTypes<0, 0, 0, VEC>{});
+hipError_t by_types(int r, int io, int p, bool tail, F&& go) {
+  auto with = [&](auto tail_) {
+    constexpr bool TAIL = decltype(tail_)::value;
+    if (r) return p ? go(RowTypes<1, 1, 1, TAIL>{}) : go(RowTypes<1, 1, 0, TAIL>{});
+    if (io) return p ? go(RowTypes<0, 1, 1, TAIL>{}) : go(RowTypes<0, 1, 0, TAIL>{});
+    return p ? go(RowTypes<0, 0, 1, TAIL>{}) : go(RowTypes<0, 0, 0, TAIL>{});
   };
-  return vec ? with(std::true_type{}) : with(std::false_type{});
+  return tail ? with(std::true_type{}) : with(std::false_type{});
 }
 
-// Workers of the backward pass: two blocks per CU of a 256 CU card, a row each at least.
+// Workers of the backward pass: two blocks per CU of a 256 CU card, a row each at least.  Where a gate's
+// rows are fewer than a worker's, these are a multiple of them.
 constexpr int64_t kGradBlocks = 512;
-void grad_split(int64_t T, int rows_per_block, int64_t* rows, int64_t* workers) {
+void grad_split(int64_t T, int64_t per, int rows_per_block, int64_t* rows, int64_t* workers) {
   const int64_t most = kGradBlocks * rows_per_block;
   *rows = (T + most - 1) / most;
+  if (per < *rows) *rows = (*rows + per - 1) / per * per;
   *workers = (T + *rows - 1) / *rows;
 }
 
@@ -398,13 +433,12 @@ hipError_t launch_block_norm(const void* res, int r_bf16, const void* w, int p_b
                              const void* wo, const void* gate, int64_t gates, void* res_out, void* y, int64_t T,
                              int64_t H, float scale, float eps, hipStream_t s) {
   const NormArgs a{res, block, w, wo, gate, y, res_out, T, H, gates ? T / gates : T, scale, eps};
-  const bool vec = all_vec(H, {res, w, block, wo, gate, res_out, y});
-  return by_types(r_bf16, io_bf16, p_bf16, vec, [&](auto ty) {
+  return by_types(r_bf16, io_bf16, p_bf16, H % kPiece != 0, [&](auto ty) {
     using Ty = decltype(ty);
     return by_width(H, [&](auto shape) {
       using S = decltype(shape);
       const int64_t blocks = (T + S::kRows - 1) / S::kRows;
-      return launch(norm_kernel<Ty::R, Ty::IO, Ty::P, S::kTpr, S::kV, Ty::VEC>,
+      return launch(norm_kernel<Ty::R, Ty::IO, Ty::P, S::kTpr, S::kV, Ty::TAIL>,
                     dim3(unsigned(blocks < 65536 ? blocks : 65536)), dim3(S::kTpr > kThreads ? S::kTpr : kThreads), 0, s, a);
     });
   });
@@ -414,7 +448,7 @@ size_t block_norm_grad_ws_bytes(int64_t T, int64_t H, bool post, bool gate) {
   if (T <= 0) return 0;
   return by_width(H, [&](auto shape) {
     int64_t rows, workers;
-    grad_split(T, decltype(shape)::kRows, &rows, &workers);
+    grad_split(T, T, decltype(shape)::kRows, &rows, &workers);  // the most workers that any gate leaves
     return size_t(workers) * size_t(H) * 4 * (1 + (post ? 1 : 0) + (gate ? 2 : 0));
   });
 }
@@ -423,26 +457,25 @@ hipError_t launch_block_norm_grad(const void* dy, int io_bf16, const void* dres_
                                   const void* w, int p_bf16, const void* block, const void* wo, const void* gate,
                                   int64_t gates, void* dres, void* dblock, void* dw, void* dwo, void* dgate, int64_t T,
                                   int64_t H, float scale, float eps, float* ws, hipStream_t s) {
-  const bool vec = all_vec(H, {dy, dres_in, res, w, block, wo, gate, dres, dblock, dgate});
   int64_t rows = 0, workers = 0;
   NormGradArgs a{dy, dres_in, res, w, block, wo, gate, dres, dblock, dgate, ws, nullptr, nullptr, T, H,
                  gates ? T / gates : T, 0, scale, eps};
-  const hipError_t e = by_types(r_bf16, io_bf16, p_bf16, vec, [&](auto ty) {
+  const hipError_t e = by_types(r_bf16, io_bf16, p_bf16, H % kPiece != 0, [&](auto ty) {
     using Ty = decltype(ty);
     return by_width(H, [&](auto shape) {
       using S = decltype(shape);
-      grad_split(T, S::kRows, &rows, &workers);
+      grad_split(T, a.per, S::kRows, &rows, &workers);
       a.rows = rows;
       a.part_wo = a.part_w + workers * H;
       a.part_gate = a.part_wo + (wo ? workers * H : 0);
-      return launch(norm_grad_kernel<Ty::R, Ty::IO, Ty::P, S::kTpr, S::kV, Ty::VEC>,
+      return launch(norm_grad_kernel<Ty::R, Ty::IO, Ty::P, S::kTpr, S::kV, Ty::TAIL>,
                     dim3(unsigned((workers + S::kRows - 1) / S::kRows)),
                     dim3(S::kTpr > kThreads ? S::kTpr : kThreads), 0, s, a);
     });
   });
   if (e != hipSuccess) return e;
   const NormJoinArgs j{a.part_w, a.part_wo, a.part_gate, dw, wo ? dwo : nullptr, dgate, T, H, a.per, rows, workers, p_bf16};
-  const unsigned joins = unsigned(gate ? 2 + (workers - 1) : wo ? 2 : 1);
+  const unsigned joins = gate && a.per > rows ? unsigned(2 + gates) : wo ? 2u : 1u;  // such gates are fewer than the workers
   return launch(norm_join_kernel, dim3(unsigned((H + kWave - 1) / kWave), joins), dim3(kJoinWaves * kWave), 0, s, j);
 }
 

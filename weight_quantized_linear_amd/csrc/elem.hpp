@@ -41,6 +41,65 @@ template <> struct Elem<0> {
   }
 };
 
+// Eight values as they lie in memory, at any address of their type (global loads and stores of
+// 16 bytes need no alignment here); `left` of them exist, none where it is not positive.  TAIL: a
+// row may end inside eight values, else left is 8 or more or nothing.
+typedef u32x4 u32x4_loose __attribute__((aligned(2)));
+template <int BF16>
+struct Eight {
+  u32x4 v[BF16 ? 1 : 2];
+  template <bool TAIL>
+  __device__ __forceinline__ void load(const void* p, int64_t i, int64_t left) {
+    using V = typename Elem<BF16>::T;
+    const V* q = reinterpret_cast<const V*>(p) + i;
+    v[0] = u32x4{0, 0, 0, 0};
+    if constexpr (!BF16) v[1] = u32x4{0, 0, 0, 0};
+    if (left >= 8) {
+      v[0] = *reinterpret_cast<const u32x4_loose*>(q);
+      if constexpr (!BF16) v[1] = *reinterpret_cast<const u32x4_loose*>(q + 4);
+    } else if (TAIL) {
+#pragma unroll
+      for (int e = 0; e < 7; ++e)
+        if (e < left) {
+          if constexpr (BF16) v[0][e / 2] |= uint32_t(q[e]) << (16 * (e % 2));
+          else v[e / 4][e % 4] = __float_as_uint(q[e]);
+        }
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    if constexpr (BF16) {
+      Elem<1>::unpack(v[0], f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[e / 4][e % 4]);
+    }
+  }
+  __device__ __forceinline__ void put(const float (&f)[8]) {
+    if constexpr (BF16) {
+      v[0] = Elem<1>::pack(f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e / 4][e % 4] = __float_as_uint(f[e]);
+    }
+  }
+  template <bool TAIL>
+  __device__ __forceinline__ void store(void* p, int64_t i, int64_t left) const {
+    using V = typename Elem<BF16>::T;
+    V* q = reinterpret_cast<V*>(p) + i;
+    if (left >= 8) {
+      *reinterpret_cast<u32x4_loose*>(q) = v[0];
+      if constexpr (!BF16) *reinterpret_cast<u32x4_loose*>(q + 4) = v[1];
+    } else if (TAIL) {
+#pragma unroll
+      for (int e = 0; e < 7; ++e)
+        if (e < left) {
+          if constexpr (BF16) q[e] = uint16_t(v[0][e / 2] >> (16 * (e % 2)));
+          else q[e] = __uint_as_float(v[e / 4][e % 4]);
+        }
+    }
+  }
+};
+
 // Eight values at p + i (16-byte aligned) to and from float32.
 template <int BF16>
 __device__ __forceinline__ void load_eight(const void* p, int64_t i, float (&f)[8]) {

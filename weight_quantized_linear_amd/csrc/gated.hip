@@ -4,6 +4,8 @@
 //   dpre = [dy pre_up act'(pre_gate), dy act(pre_gate)],   dx = dpre W,   dW = dpre^T x.
 // float32 sums; pre-activations leave the registers only where the caller keeps them for
 // the backward pass, so the 2F columns are neither written nor read again.
+#include <algorithm>
+
 #include "activation.hpp"
 #include "device.hpp"
 #include "elem.hpp"
@@ -126,6 +128,197 @@ __global__ __launch_bounds__(kThreads) void product_any_kernel(const uint16_t* _
                             if (out_bf16) reinterpret_cast<uint16_t*>(out)[m * N + n] = Elem<1>::put(v);
                             else reinterpret_cast<float*>(out)[m * N + n] = v;
                           });
+}
+
+// ---------------------------------------------------------------- few rows
+
+// Sixteen bytes at any address (global loads need no alignment here).
+typedef u32x4 u32x4_loose __attribute__((aligned(1)));
+__device__ __forceinline__ u32x4 ld16_loose(const void* p) { return *reinterpret_cast<const u32x4_loose*>(p); }
+__device__ __forceinline__ u32x4 ld16_loose_stream(const void* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4_loose*>(p));
+}
+
+// M <= 4 rows at any size and address, on the vector ALU: a wave has one column, whose gate and up rows it reads in
+// contiguous KiB, 2 U loads in flight a lane; products of pairs by the bfloat16 dot instruction (exact,
+// float32 sums).  Bound by HBM: one row of x, F = 14336, K = 4096, FP8: 19 us, 6.2 TB/s;
+// bfloat16 35.5, 6.6 TB/s.
+template <int EB, int M, int U>
+__global__ __launch_bounds__(256) void gated_gemv_kernel(const char* __restrict__ w, const uint16_t* __restrict__ x,
+                                                        GatedOut o, int64_t F, int64_t K) {
+  constexpr int kValues = 16 / EB, X = kValues / 8;  // values of a load of w, loads of x beside it
+  const int lane = threadIdx.x % kWave;
+  const int64_t f = int64_t(blockIdx.x) * (256 / kWave) + threadIdx.x / kWave;
+  if (f >= F) return;  // the whole wave
+  const int64_t row_bytes = K * EB;
+  const char* const rows[2] = {w + f * row_bytes, w + (F + f) * row_bytes};
+  float acc[M][2];
+#pragma unroll
+  for (int m = 0; m < M; ++m) acc[m][0] = acc[m][1] = 0.f;
+  const int64_t whole = K / kValues;  // whole loads of a row
+  for (int64_t c0 = 0; c0 < whole; c0 += kWave * U) {
+    u32x4 wv[U][2], xv[U][M][X];
+#pragma unroll
+    for (int n = 0; n < U; ++n) {
+      const int64_t c = c0 + n * kWave + lane;
+      const bool ok = c < whole;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) wv[n][r] = ok ? ld16_loose_stream(rows[r] + 16 * c) : u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int e = 0; e < X; ++e)
+          xv[n][m][e] = ok ? ld16_loose(x + m * K + c * kValues + 8 * e) : u32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int n = 0; n < U; ++n)
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int m = 0; m < M; ++m) {
+            const uint32_t word = wv[n][r][d];
+            if constexpr (EB == 1) {
+              const u32x4& xa = xv[n][m][d / 2];
+              const uint32_t x01 = xa[2 * (d % 2)], x23 = xa[2 * (d % 2) + 1];
+              acc[m][r] = __builtin_amdgcn_fdot2_f32_bf16(as_bf16x2(e4m3x2_to_bf16x2<false>(word)), as_bf16x2(x01),
+                                                          acc[m][r], false);
+              acc[m][r] = __builtin_amdgcn_fdot2_f32_bf16(as_bf16x2(e4m3x2_to_bf16x2<true>(word)), as_bf16x2(x23),
+                                                          acc[m][r], false);
+            } else {
+              const uint32_t xw = xv[n][m][0][d];
+              acc[m][r] = __builtin_amdgcn_fdot2_f32_bf16(as_bf16x2(word), as_bf16x2(xw), acc[m][r], false);
+            }
+          }
+  }
+  if (const int64_t k = whole * kValues + lane; k < K) {  // the values behind the last whole load, one a lane
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float v;
+        if constexpr (EB == 1) v = e4m3_to_f32(uint8_t(rows[r][k]));
+        else v = bf16_to_f32(reinterpret_cast<const uint16_t*>(rows[r])[k]);
+        acc[m][r] = fmaf(v, bf16_to_f32(x[m * K + k]), acc[m][r]);
+      }
+  }
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    const float g = wave_sum(acc[m][0]), u = wave_sum(acc[m][1]);
+    if (lane == m) gated_put(o, m, f, F, g, u);
+  }
+}
+
+// M <= 16 rows: bound by the weights' bytes, which therefore go to LDS in whole 1 KiB pieces of a row (into
+// registers, 64 bytes of 16 rows a load, the same bytes come at 3.5 to 4.5 TB/s).  A block walks tiles of 8 columns, that
+// is 8 gate and 8 up rows, as the 16 rows of one MFMA operand, through a ring of S stages of 2 KiB a row; each of its
+// 8 waves takes an eighth of every stage, so the part of x that it meets stays in its registers (KS
+// stages a row), and the waves' sums meet in LDS at a tile's end.  MFMA 16x16x32: the weights' rows are the
+// result's rows and the tokens its columns: lanes 0 .. 31 end with four gate columns of a token, lanes 32 .. 63
+// with the up ones.  FP8: a lane's 16 bytes are the operands of two steps, and x is held in that order.
+// M = 13, K = 4096, F = 14336: 28 us FP8 (4.2 TB/s), 43 bfloat16 (5.5); K = 2048, F = 5504, bfloat16 13 (3.4: three tiles a
+// block, the first loads' and the last sums' latency shows).  Weights kept in the caches: 1 to 2 us more.
+template <int EB, int KS, int S>
+__global__ __launch_bounds__(512) void gated_rows_kernel(const char* __restrict__ w, const uint16_t* __restrict__ x,
+                                                        GatedOut o, int M, int64_t F, int64_t K) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  constexpr int NW = 8, kRow = 2048, kStage = 16 * kRow;
+  constexpr int kParts = kRow / 1024, kDma = 16 * kParts / NW;
+  constexpr int kSteps = kRow / NW / 64;      // loads of 16 bytes a lane per stage
+  constexpr int kValues = 16 / EB, E = kValues / 8;  // values of a load, MFMA steps of it
+  v4f(*const sums)[kWave] = reinterpret_cast<v4f(*)[kWave]>(lds + S * kStage);
+  const int lane = threadIdx.x % kWave, wid = threadIdx.x / kWave, i = lane % 16, q = lane / 16;
+  const int64_t tiles = (F + 7) / 8, row_bytes = K * EB;
+  const int stages = int((tiles - 1 - blockIdx.x) / gridDim.x + 1) * KS;
+
+  // Stage j is part j % KS of the rows of the block's tile j / KS.  Row r: gate f0 + r, or up f0 + r - 8.
+  // Pieces past a row's end are zeros; rows past F hold others' values or zeros and are not stored.
+  uint32_t off[kDma];
+#pragma unroll
+  for (int n = 0; n < kDma; ++n) {
+    const int r = (wid * kDma + n) / kParts;
+    off[n] = uint32_t(((r & 7) + (r & 8 ? F : 0)) * row_bytes);
+  }
+  auto issue = [&](int j) {
+    const int64_t f0 = (blockIdx.x + int64_t(j / KS) * gridDim.x) * 8;
+    const __amdgpu_buffer_rsrc_t res = strip_rsrc(w + f0 * row_bytes, (2 * F - f0) * row_bytes, false);
+    char* const slot = lds + j % S * kStage;
+#pragma unroll
+    for (int n = 0; n < kDma; ++n) {
+      const int r = (wid * kDma + n) / kParts, p = (wid * kDma + n) % kParts;
+      const uint32_t at = j % KS * kRow + 1024 * p + 16 * (lane ^ r);
+      bdma16_nt(res, slot + r * kRow + 1024 * p, at < uint32_t(row_bytes) ? off[n] + at : kNowhere);
+    }
+  };
+  issue(0);
+  // This lane's part of x: bounded loads, so that none waits for another's condition.
+  v8bf xf[KS][kSteps][E];
+  const __amdgpu_buffer_rsrc_t xres = make_rsrc(x, M * K * 2);
+#pragma unroll
+  for (int h = 0; h < KS; ++h)
+#pragma unroll
+    for (int c = 0; c < kSteps; ++c)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint32_t k = (h * kRow + wid * (kRow / NW) + 64 * c + 16 * q) / EB + 8 * e;
+        const uint32_t at = i < M && k < uint32_t(K) ? (i * uint32_t(K) + k) * 2 : kNowhere;
+        xf[h][c][e] = __builtin_bit_cast(v8bf, __builtin_amdgcn_raw_buffer_load_b128(xres, at, 0, 0));
+      }
+#pragma unroll
+  for (int j = 1; j < S; ++j)
+    if (j < stages) issue(j);
+
+  v4f acc[2] = {v4f{}, v4f{}};
+  for (int j = 0; j < stages; ++j) {
+    const int ahead = stages - 1 - j;  // later stages, of which at most S - 1 are on their way
+    if (ahead >= S - 1) wait_vm<(S - 1) * kDma>();
+    else if (S > 3 && ahead == 2) wait_vm<2 * kDma>();
+    else if (ahead == 1) wait_vm<kDma>();
+    else wait_vm<0>();
+    block_barrier();
+    const int h = j % KS;
+    const char* const row = lds + j % S * kStage + i * kRow;
+    u32x4 wv[kSteps];
+#pragma unroll
+    for (int c = 0; c < kSteps; ++c) {
+      const int at = wid * (kRow / NW) + 64 * c + 16 * q;  // a permuted piece stays in its KiB
+      wv[c] = lds16(row + (at ^ (i << 4)));
+    }
+#pragma unroll
+    for (int hh = 0; hh < KS; ++hh) {
+      if (hh != h) continue;  // uniform; the register arrays keep constant indexes
+#pragma unroll
+      for (int c = 0; c < kSteps; ++c)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          v8bf a;
+          if constexpr (EB == 1) a = e4m3x8_to_bf16x8(wv[c][2 * e], wv[c][2 * e + 1]);
+          else a = __builtin_bit_cast(v8bf, wv[c]);
+          acc[(c * E + e) % 2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, xf[hh][c][e], acc[(c * E + e) % 2], 0, 0, 0);
+        }
+    }
+    const bool last = h == KS - 1;
+    if (last) sums[wid][lane] = acc[0] + acc[1];
+    wait_lds();
+    block_barrier();  // the slot is read, and at a tile's end the sums are there
+    if (j + S < stages) issue(j + S);
+    if (last) {
+      const int n = j / KS;
+      if (wid == n % NW) {
+        v4f sum = sums[0][lane];
+#pragma unroll
+        for (int v = 1; v < NW; ++v) sum += sums[v][lane];
+        const int64_t f = (blockIdx.x + int64_t(n) * gridDim.x) * 8 + 4 * (q & 1);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float up = __shfl_down(sum[v], 32, kWave);
+          if (q < 2 && i < M && f + v < F) gated_put(o, i, f + v, F, sum[v], up);
+        }
+      }
+      acc[0] = acc[1] = v4f{};
+    }
+  }
 }
 
 // ---------------------------------------------------------------- products in large tiles
@@ -323,6 +516,7 @@ hipError_t by_act(int act, F&& go) {
 }
 
 template <int V> using Int = std::integral_constant<int, V>;
+constexpr int64_t kRowsSpan = 2048;  // bytes of a weight row in a stage of gated_rows_kernel
 
 // The large tiles' loads: 16-byte rows at aligned addresses, and a strip of a tile within 32-bit offsets.
 bool tiled_rows(const void* p, int64_t row_bytes) {
@@ -362,6 +556,40 @@ hipError_t launch_product_any(const uint16_t* a, int64_t lda, const uint16_t* b,
 hipError_t launch_gated_gemm(const void* w, int fp8, const uint16_t* x, const GatedOut& o, int64_t M, int64_t F, int64_t K,
                              int num_cus, hipStream_t s) {
   const int eb = fp8 ? 1 : 2;
+  // Few rows.  F = 14336, K = 4096, us (vector ALU, stages in LDS, tiles of 64 rows): FP8 M = 1 19, 27, -; M = 2
+  // 23.6, 27, -; M = 4 38, 27, -; M = 13 -, 28, 41; bfloat16 M = 2 37, 42, -; M = 4 48, 42, -; M = 13 -, 43, 46.
+  const bool in_stages = K * eb <= (fp8 ? 4 : 8) * kRowsSpan && aligned16(x) && aligned16(w) && K * eb % 16 == 0 &&
+                         K % 8 == 0 && 2 * F * K * eb < kNowhere;
+  if (M <= 2 || (M <= 4 && !in_stages)) {
+    const int64_t blocks = (F + 3) / 4;
+    if (blocks > kMaxGrid) return hipErrorInvalidValue;
+    auto go = [&](auto kernel) {
+      return launch(kernel, dim3(unsigned(blocks)), dim3(256), 0, s, static_cast<const char*>(w), x, o, F, K);
+    };
+    if (fp8)
+      return M == 1   ? go(gated_gemv_kernel<1, 1, 4>)
+             : M == 2 ? go(gated_gemv_kernel<1, 2, 2>)
+             : M == 3 ? go(gated_gemv_kernel<1, 3, 2>)
+                      : go(gated_gemv_kernel<1, 4, 2>);
+    return M == 1   ? go(gated_gemv_kernel<2, 1, 4>)
+           : M == 2 ? go(gated_gemv_kernel<2, 2, 4>)
+           : M == 3 ? go(gated_gemv_kernel<2, 3, 2>)
+                    : go(gated_gemv_kernel<2, 4, 2>);
+  }
+  if (M <= 16 && in_stages) {
+    auto go = [&](auto bytes, auto parts) {
+      constexpr int S = 4, kLds = S * 16 * kRowsSpan + 8 * kWave * 16;
+      return launch_big_lds<gated_rows_kernel<decltype(bytes)::value, decltype(parts)::value, S>>(
+          kLds, std::min<int64_t>((F + 7) / 8, num_cus), 512, s, static_cast<const char*>(w), x, o, int(M), F, K);
+    };
+    auto by_parts = [&](auto bytes) {
+      if (K * eb <= kRowsSpan) return go(bytes, Int<1>{});
+      if (K * eb <= 2 * kRowsSpan) return go(bytes, Int<2>{});
+      if (K * eb <= 4 * kRowsSpan) return go(bytes, Int<4>{});
+      return go(Int<2>{}, Int<8>{});
+    };
+    return fp8 ? by_parts(Int<1>{}) : by_parts(Int<2>{});
+  }
   if (tiled_rows(x, K * 2) && tiled_rows(w, K * eb) && 2 * F * K * eb < kNowhere) {
     const Operand xo{reinterpret_cast<const char*>(x), 2 * K, M}, wo{static_cast<const char*>(w), K * eb, 2 * F};
     const int vec = aligned16(o.out) && F * (o.out_bf16 ? 2 : 4) % 16 == 0;

@@ -39,6 +39,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t strip_rsrc(const char* p, int6
   return make_rsrc(p, none ? 0 : bytes < int64_t(kNowhere) ? bytes : int64_t(kNowhere));
 }
 
+// 16 bytes per lane straight into LDS, not kept in the caches.
+__device__ __forceinline__ void bdma16_nt(__amdgpu_buffer_rsrc_t rsrc, char* lds, uint32_t voff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void_t*)lds, 16, voff, 0, 0, 2);
+}
+
 // Row r of the tile is row `first + r` of the operand.
 struct PlainRows {
   int64_t first, rows;
