@@ -34,24 +34,26 @@ __device__ __forceinline__ float stored(float v) {
   else return v;
 }
 
-// Sums over the TPR threads of a row; every thread gets the result.  `part`: LDS of
-// kThreads / 64 floats for each call in a row's work, so that no barrier is needed between
-// one call's reads and the next one's writes but the next one's own.
-template <int TPR, int THREADS>
-__device__ __forceinline__ float row_sum(float v, float* part) {
-  v = wave_sum(v);
-  if constexpr (TPR == kWave) {
-    return v;
-  } else {
+// N sums over the TPR threads of a row; every thread gets the results.  `part`: LDS of its own for two calls in
+// a row, so that a call's one barrier also lies between the reads of one and the writes of the next but one.
+template <int TPR, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*part)[N]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) v[n] = wave_sum(v[n]);
+  if constexpr (TPR > kWave) {
     constexpr int W = TPR / kWave;
     const int wid = threadIdx.x / kWave;
-    if (threadIdx.x % kWave == 0) part[wid] = v;
+    if (threadIdx.x % kWave == 0)
+#pragma unroll
+      for (int n = 0; n < N; ++n) part[wid][n] = v[n];
     __syncthreads();
     const int first = wid / W * W;
-    float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < W; ++i) s += part[first + i];
-    return s;
+    for (int n = 0; n < N; ++n) {
+      v[n] = 0.f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) v[n] += part[first + i][n];
+    }
   }
 }
 
@@ -63,11 +65,12 @@ struct NormArgs {
 };
 
 // R, IO, P: element types of the residual, of block output and y, of the parameters.  TAIL: H % 8 != 0.
-// Bound by HBM: FWDFIGURE
-template <int R, int IO, int P, int TPR, int V, bool TAIL>
+// NT: results past the caches.  Bound by HBM: 16384 x 4096, float32
+// residual, 157 us, 5.1 TB/s; 16384 x 2048 in bfloat16 45 us, 6.0; a 2 GiB copy reaches 5.0.
+template <int R, int IO, int P, int TPR, int V, bool TAIL, bool NT>
 __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void norm_kernel(NormArgs a) {
   constexpr int THREADS = TPR > kThreads ? TPR : kThreads, ROWS = THREADS / TPR, C = V / kPiece;
-  __shared__ float part[4][THREADS / kWave];
+  __shared__ float part[4][THREADS / kWave][1];
   const int lane = threadIdx.x % TPR, mine = threadIdx.x / TPR;
   const float inv_h = 1.f / float(a.H);
   int turn = 0;
@@ -76,19 +79,19 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void norm_kernel(N
     const bool live = t0 + mine < a.T;
     const int64_t t = live ? t0 + mine : a.T - 1, at = t * a.H;
     const int64_t grow = a.gate ? t / a.per * a.H : 0;
-    // Everything that the row needs is on its way before the first sum waits.
     Eight<R> r8[C];
     Eight<IO> o8[C];
-    Eight<P> w8[C], wo8[C], g8[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int64_t i = int64_t(c * TPR + lane) * kPiece;
       r8[c].template load<TAIL>(a.res, at + i, a.H - i);
       if (a.block) o8[c].template load<TAIL>(a.block, at + i, a.H - i);
-      w8[c].template load<TAIL>(a.w, i, a.H - i);
-      if (a.wo) wo8[c].template load<TAIL>(a.wo, i, a.H - i);
-      if (a.gate) g8[c].template load<TAIL>(a.gate, grow + i, a.H - i);
     }
+    auto parameter = [&](const void* p, int64_t from, int64_t i, float (&f)[8]) {
+      Eight<P> v;
+      v.template load<TAIL>(p, from + i, a.H - i);
+      v.get(f);
+    };
     float r[C][8];
 #pragma unroll
     for (int c = 0; c < C; ++c) r8[c].get(r[c]);
@@ -98,25 +101,26 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void norm_kernel(N
 #pragma unroll
       for (int c = 0; c < C; ++c) o8[c].get(o[c]);
       if (a.wo) {
-        float s = 0.f;
+        float s[1] = {0.f};
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s = fmaf(o[c][e], o[c][e], s);
-        inv = rsqrtf(row_sum<TPR, THREADS>(s, part[turn]) * inv_h + a.eps);
+          for (int e = 0; e < 8; ++e) s[0] = fmaf(o[c][e], o[c][e], s[0]);
+        row_sums<TPR>(s, part[turn]);
+        inv = rsqrtf(s[0] * inv_h + a.eps);
       }
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const int64_t i = int64_t(c * TPR + lane) * kPiece;
         if (a.wo) {
           float w[8];
-          wo8[c].get(w);
+          parameter(a.wo, 0, i, w);
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[c][e] = o[c][e] * inv * w[e];
         }
         if (a.gate) {
           float g[8];
-          g8[c].get(g);
+          parameter(a.gate, grow, i, g);
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[c][e] *= g[e];
         }
@@ -124,25 +128,26 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void norm_kernel(N
         for (int e = 0; e < 8; ++e) r[c][e] = fmaf(a.scale, r[c][e], o[c][e]);
         r8[c].put(r[c]);
         r8[c].get(r[c]);  // as it is stored
-        if (live) r8[c].template store<TAIL>(a.res_out, at + i, a.H - i);
+        if (live) r8[c].template store<TAIL, NT>(a.res_out, at + i, a.H - i);
       }
     }
-    float s = 0.f;
+    float s[1] = {0.f};
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s = fmaf(r[c][e], r[c][e], s);
-    const float inv = rsqrtf(row_sum<TPR, THREADS>(s, part[turn + 1]) * inv_h + a.eps);
+      for (int e = 0; e < 8; ++e) s[0] = fmaf(r[c][e], r[c][e], s[0]);
+    row_sums<TPR>(s, part[turn + 1]);
+    const float inv = rsqrtf(s[0] * inv_h + a.eps);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int64_t i = int64_t(c * TPR + lane) * kPiece;
       float w[8];
-      w8[c].get(w);
+      parameter(a.w, 0, i, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] = r[c][e] * inv * w[e];
       Eight<IO> y;
       y.put(w);
-      if (live) y.template store<TAIL>(a.y, at + i, a.H - i);
+      if (live) y.template store<TAIL, NT>(a.y, at + i, a.H - i);
     }
   }
 }
@@ -160,12 +165,14 @@ struct NormGradArgs {
 // worker's lie whole in one (rows is a multiple of theirs) and are finished by it; of others it leaves parts:
 // [0] of the gate that its range begins in the middle of, [1] of the one that begins in its range.
 // With V = 8 the parameters stay in registers and the next row is on its way while one is worked on; wider
-// rows have no registers for that.
+// rows have no registers for that.  Both means come from sums over the row as it was read, so that a row meets
+// one barrier.  Bound by HBM: 8192 x 2048 in bfloat16 45 us, 4.4 TB/s; 16384 x 4096 203 us, 4.0; results past the
+// caches changed neither.  256 or 1024 blocks take 1.5 and 1.1 times as long at 8192 x 2048.
 template <int R, int IO, int P, int TPR, int V, bool TAIL>
 __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void norm_grad_kernel(NormGradArgs a) {
   constexpr int THREADS = TPR > kThreads ? TPR : kThreads, WORKERS = THREADS / TPR, C = V / kPiece;
   constexpr bool kAhead = V == 8;
-  __shared__ float part[6][THREADS / kWave];
+  __shared__ float part[2][THREADS / kWave][6];
   const int lane = threadIdx.x % TPR;
   const float inv_h = 1.f / float(a.H);
   const int64_t worker = int64_t(blockIdx.x) * WORKERS + threadIdx.x / TPR;
@@ -209,97 +216,89 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void norm_grad_ker
     for (int e = 0; e < 8; ++e) sw[c][e] = swo[c][e] = sg[c][e] = 0.f;
   Row cur, next;
   load(cur, row_of(0));
-  int turn = 0;
-  for (int64_t n = 0; n < a.rows; ++n, turn = 3 - turn) {  // as many turns for every worker of the block: barriers
+  for (int64_t n = 0; n < a.rows; ++n) {  // as many turns for every worker of the block: barriers
     const bool live = begin + n < end;
     const int64_t t = row_of(n), at = t * a.H;
     if (kAhead) load(next, row_of(n + 1 < a.rows ? n + 1 : n));
-    float r[C][8], dy[C][8];
-    float s = 0.f;
+    const int64_t gate = a.gate ? t / a.per : 0;
+    if (a.gate && (!kAhead || gate != held)) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      cur.r[c].get(r[c]);
-      cur.dy[c].get(dy[c]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s = fmaf(r[c][e], r[c][e], s);
+      for (int c = 0; c < C; ++c) parameter(a.gate, gate * a.H, c, g[c]);
+      held = gate;
     }
-    const float inv = rsqrtf(row_sum<TPR, THREADS>(s, part[turn]) * inv_h + a.eps);
-    s = 0.f;
+    // All sums over the row at once: of r^2, dy w r, o^2, and with q = gate w_o o those of dr' q, dy w q, r q, of
+    // which sum(b o) = sum(D q) is made.
+    float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < C; ++c) {
+      float r[8], dy[8];
+      cur.r[c].get(r);
+      cur.dy[c].get(dy);
       if (!kAhead) parameter(a.w, 0, c, w[c]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        r[c][e] *= inv;
-        if (live) sw[c][e] = fmaf(dy[c][e], r[c][e], sw[c][e]);
-        dy[c][e] *= w[c][e];
-        s = fmaf(dy[c][e], r[c][e], s);
+        dy[e] *= w[c][e];
+        s[0] = fmaf(r[e], r[e], s[0]);
+        s[1] = fmaf(dy[e], r[e], s[1]);
       }
-    }
-    const float mean = row_sum<TPR, THREADS>(s, part[turn + 1]) * inv_h;
-    float d[C][8];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      float in[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (a.dres_in) cur.dr[c].get(in);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        d[c][e] = fmaf(inv, fmaf(-r[c][e], mean, dy[c][e]), in[e]);
-        in[e] = a.scale * d[c][e];
-      }
-      Eight<R> out;
-      out.put(in);
-      if (live) out.template store<TAIL>(a.dres, at + piece(c), a.H - piece(c));
-    }
-    if (a.block) {
-      const int64_t gate = a.gate ? t / a.per : 0;
-      float o[C][8];
-      float inv_o = 1.f;
-      if (with_o) {
-        s = 0.f;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          cur.o[c].get(o[c]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) s = fmaf(o[c][e], o[c][e], s);
-        }
-        if (a.wo) inv_o = rsqrtf(row_sum<TPR, THREADS>(s, part[turn + 2]) * inv_h + a.eps);
-      }
-      if (a.gate && (!kAhead || gate != held)) {
-#pragma unroll
-        for (int c = 0; c < C; ++c) parameter(a.gate, gate * a.H, c, g[c]);
-        held = gate;
-      }
-      s = 0.f;
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        if (!kAhead && a.wo) parameter(a.wo, 0, c, wo[c]);
+      if (a.wo) {
+        float o[8], in[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        cur.o[c].get(o);
+        if (a.dres_in) cur.dr[c].get(in);
+        if (!kAhead) parameter(a.wo, 0, c, wo[c]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          if (a.wo) o[c][e] *= inv_o;
-          if (a.gate) {
-            if (live) sg[c][e] = fmaf(d[c][e], a.wo ? o[c][e] * wo[c][e] : o[c][e], sg[c][e]);
-            d[c][e] *= g[c][e];
-          }
-          if (a.wo) {
-            if (live) swo[c][e] = fmaf(d[c][e], o[c][e], swo[c][e]);
-            d[c][e] *= wo[c][e];
-            s = fmaf(d[c][e], o[c][e], s);
-          }
+          s[2] = fmaf(o[e], o[e], s[2]);
+          const float q = a.gate ? o[e] * wo[c][e] * g[c][e] : o[e] * wo[c][e];
+          s[3] = fmaf(in[e], q, s[3]);
+          s[4] = fmaf(dy[e], q, s[4]);
+          s[5] = fmaf(r[e], q, s[5]);
         }
       }
-      float mean_o = 0.f;
-      if (a.wo) mean_o = row_sum<TPR, THREADS>(s, part[turn]) * inv_h;
+    }
+    row_sums<TPR>(s, part[n & 1]);
+    const float inv = rsqrtf(s[0] * inv_h + a.eps), mean = s[1] * inv * inv_h;
+    const float inv_o = a.wo ? rsqrtf(s[2] * inv_h + a.eps) : 1.f;
+    const float mean_o = (s[3] + inv * (s[4] - inv * mean * s[5])) * inv_o * inv_h;
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
+    for (int c = 0; c < C; ++c) {
+      float r[8], d[8], out[8], in[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      cur.r[c].get(r);
+      cur.dy[c].get(d);
+      if (a.dres_in) cur.dr[c].get(in);
+      if (!kAhead) parameter(a.w, 0, c, w[c]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        r[e] *= inv;
+        if (live) sw[c][e] = fmaf(d[e], r[e], sw[c][e]);
+        d[e] = fmaf(inv, fmaf(-r[e], mean, d[e] * w[c][e]), in[e]);
+        out[e] = a.scale * d[e];
+      }
+      Eight<R> dres;
+      dres.put(out);
+      if (live) dres.template store<TAIL>(a.dres, at + piece(c), a.H - piece(c));
+      if (!a.block) continue;
+      float o[8];
+      if (with_o) cur.o[c].get(o);
+      if (!kAhead && a.wo) parameter(a.wo, 0, c, wo[c]);
+      if (!kAhead && a.gate) parameter(a.gate, gate * a.H, c, g[c]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (a.wo) o[e] *= inv_o;
+        if (a.gate) {
+          if (live) sg[c][e] = fmaf(d[e], a.wo ? o[e] * wo[c][e] : o[e], sg[c][e]);
+          d[e] *= g[c][e];
+        }
         if (a.wo) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) d[c][e] = inv_o * fmaf(-o[c][e], mean_o, d[c][e]);
+          if (live) swo[c][e] = fmaf(d[e], o[e], swo[c][e]);
+          d[e] = inv_o * fmaf(-o[e], mean_o, d[e] * wo[c][e]);
         }
-        Eight<IO> out;
-        out.put(d[c]);
-        if (live) out.template store<TAIL>(a.dblock, at + piece(c), a.H - piece(c));
       }
+      Eight<IO> dblock;
+      dblock.put(d);
+      if (live) dblock.template store<TAIL>(a.dblock, at + piece(c), a.H - piece(c));
+    }
+    if (a.block) {
       // The gate's last row of this range: its sum leaves.
       if (a.gate && live && (t + 1 == end || (t + 1) % a.per == 0)) {
 #pragma unroll
@@ -417,6 +416,10 @@ hipError_t by_types(int r, int io, int p, bool tail, F&& go) {
   return tail ? with(std::true_type{}) : with(std::false_type{});
 }
 
+// Calls that move more leave their results past the caches: 16384 x 2048 in bfloat16 (268 MB) 43 us, 55 through
+// them; 4096 x 4096 (134 MB) 23.5 us either way, and the next operator finds the rows.
+constexpr int64_t kNtBytes = int64_t(160) << 20;
+
 // Workers of the backward pass: two blocks per CU of a 256 CU card, a row each at least.  Where a gate's
 // rows are fewer than a worker's, these are a multiple of them.
 constexpr int64_t kGradBlocks = 512;
@@ -438,8 +441,13 @@ hipError_t launch_block_norm(const void* res, int r_bf16, const void* w, int p_b
     return by_width(H, [&](auto shape) {
       using S = decltype(shape);
       const int64_t blocks = (T + S::kRows - 1) / S::kRows;
-      return launch(norm_kernel<Ty::R, Ty::IO, Ty::P, S::kTpr, S::kV, Ty::TAIL>,
-                    dim3(unsigned(blocks < 65536 ? blocks : 65536)), dim3(S::kTpr > kThreads ? S::kTpr : kThreads), 0, s, a);
+      auto go = [&](auto kernel) {
+        return launch(kernel, dim3(unsigned(blocks < 65536 ? blocks : 65536)),
+                      dim3(S::kTpr > kThreads ? S::kTpr : kThreads), 0, s, a);
+      };
+      const int64_t bytes = T * H * ((block ? 2 : 1) * (r_bf16 ? 2 : 4) + (block ? 2 : 1) * (io_bf16 ? 2 : 4));
+      return bytes > kNtBytes ? go(norm_kernel<Ty::R, Ty::IO, Ty::P, S::kTpr, S::kV, Ty::TAIL, true>)
+                              : go(norm_kernel<Ty::R, Ty::IO, Ty::P, S::kTpr, S::kV, Ty::TAIL, false>);
     });
   });
 }

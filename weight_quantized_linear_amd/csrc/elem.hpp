@@ -48,15 +48,26 @@ typedef u32x4 u32x4_loose __attribute__((aligned(2)));
 template <int BF16>
 struct Eight {
   u32x4 v[BF16 ? 1 : 2];
-  template <bool TAIL>
+  // NT: past the caches.
+  template <bool NT>
+  static __device__ __forceinline__ u32x4 fetch(const void* p) {
+    if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const u32x4_loose*>(p));
+    else return *reinterpret_cast<const u32x4_loose*>(p);
+  }
+  template <bool NT>
+  static __device__ __forceinline__ void leave(void* p, u32x4 x) {
+    if constexpr (NT) __builtin_nontemporal_store(x, reinterpret_cast<u32x4_loose*>(p));
+    else *reinterpret_cast<u32x4_loose*>(p) = x;
+  }
+  template <bool TAIL, bool NT = false>
   __device__ __forceinline__ void load(const void* p, int64_t i, int64_t left) {
     using V = typename Elem<BF16>::T;
     const V* q = reinterpret_cast<const V*>(p) + i;
     v[0] = u32x4{0, 0, 0, 0};
     if constexpr (!BF16) v[1] = u32x4{0, 0, 0, 0};
     if (left >= 8) {
-      v[0] = *reinterpret_cast<const u32x4_loose*>(q);
-      if constexpr (!BF16) v[1] = *reinterpret_cast<const u32x4_loose*>(q + 4);
+      v[0] = fetch<NT>(q);
+      if constexpr (!BF16) v[1] = fetch<NT>(q + 4);
     } else if (TAIL) {
 #pragma unroll
       for (int e = 0; e < 7; ++e)
@@ -82,13 +93,13 @@ struct Eight {
       for (int e = 0; e < 8; ++e) v[e / 4][e % 4] = __float_as_uint(f[e]);
     }
   }
-  template <bool TAIL>
+  template <bool TAIL, bool NT = false>
   __device__ __forceinline__ void store(void* p, int64_t i, int64_t left) const {
     using V = typename Elem<BF16>::T;
     V* q = reinterpret_cast<V*>(p) + i;
     if (left >= 8) {
-      *reinterpret_cast<u32x4_loose*>(q) = v[0];
-      if constexpr (!BF16) *reinterpret_cast<u32x4_loose*>(q + 4) = v[1];
+      leave<NT>(q, v[0]);
+      if constexpr (!BF16) leave<NT>(q + 4, v[1]);
     } else if (TAIL) {
 #pragma unroll
       for (int e = 0; e < 7; ++e)
