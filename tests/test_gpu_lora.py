@@ -109,6 +109,10 @@ CASES = [  # counts, adapters, r, k, n
     ([70, 30], 3, 128, 136, 72),
     ([9, 80], 1, 256, 264, 40),
     ([33, 34, 35], 2, 7, 63, 65),
+    ([40, 3], 2, 12, 5, 6),
+    ([20], 1, 16, 7, 300),
+    ([70, 2], 2, 9, 301, 3),
+    ([130, 66], 2, 33, 1030, 2001),
 ]
 
 

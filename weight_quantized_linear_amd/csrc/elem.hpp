@@ -77,6 +77,12 @@ struct Eight {
         }
     }
   }
+  // The same without a condition.
+  __device__ __forceinline__ void get_at(const void* p, int64_t i) {
+    const auto* q = reinterpret_cast<const typename Elem<BF16>::T*>(p) + i;
+    v[0] = fetch<false>(q);
+    if constexpr (!BF16) v[1] = fetch<false>(q + 4);
+  }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     if constexpr (BF16) {
       Elem<1>::unpack(v[0], f);
@@ -135,6 +141,15 @@ __device__ __forceinline__ void store_eight(void* p, int64_t i, const float (&f)
     *reinterpret_cast<u32x4*>(reinterpret_cast<float*>(p) + i) = Elem<0>::pack(a);
     *reinterpret_cast<u32x4*>(reinterpret_cast<float*>(p) + i + 4) = Elem<0>::pack(b);
   }
+}
+
+// One value at p[at].
+__device__ __forceinline__ void put_float(void* p, int64_t at, float v, int bf16) {
+  if (bf16) reinterpret_cast<uint16_t*>(p)[at] = Elem<1>::put(v);
+  else reinterpret_cast<float*>(p)[at] = v;
+}
+__device__ __forceinline__ float get_float(const void* p, int64_t at, int bf16) {
+  return bf16 ? bf16_to_f32(reinterpret_cast<const uint16_t*>(p)[at]) : reinterpret_cast<const float*>(p)[at];
 }
 
 }  // namespace qlinear

@@ -14,14 +14,6 @@ __device__ __forceinline__ float gated_value(int act, float g, float u) {
   return gated_one<3>(g, u);
 }
 
-__device__ __forceinline__ void put_float(void* p, int64_t at, float v, int bf16) {
-  if (bf16) reinterpret_cast<uint16_t*>(p)[at] = Elem<1>::put(v);
-  else reinterpret_cast<float*>(p)[at] = v;
-}
-__device__ __forceinline__ float get_float(const void* p, int64_t at, int bf16) {
-  return bf16 ? bf16_to_f32(reinterpret_cast<const uint16_t*>(p)[at]) : reinterpret_cast<const float*>(p)[at];
-}
-
 // One output from its two sums.
 __device__ __forceinline__ void gated_put(const GatedOut& o, int64_t m, int64_t f, int64_t F, float gate, float up) {
   float g = o.alpha * gate, u = o.alpha_up * up;
