@@ -638,12 +638,18 @@ int qlinear_gated_backward(const void* grad_out, int grad_dtype, const void* pre
  *     grad_w[n, k] = sum_m grad_out[m, n] x[m, k]
  * grad_out: bfloat16 [M, N], w: bfloat16 [N, K], x: bfloat16 [M, K]; the
  * results of dtype F32 or BF16, float32 sums, rounded once.  M = 0: grad_x does
- * nothing, grad_w is cleared.
+ * nothing, grad_w is cleared.  workspace: as of the *_ws calls, at least the
+ * bytes of qlinear_bf16_gemm_grad_workspace_size (x_bytes and w_bytes, either may
+ * be NULL) where the sum is split over blocks; a smaller one or NULL runs it whole.
  */
+int qlinear_bf16_gemm_grad_workspace_size(int64_t M, int64_t N, int64_t K, int64_t* x_bytes,
+                                          int64_t* w_bytes);
 int qlinear_bf16_gemm_grad_x(const void* grad_out, const void* w, void* grad_x, int dtype,
-                             int64_t M, int64_t N, int64_t K, void* stream);
+                             int64_t M, int64_t N, int64_t K, void* workspace,
+                             int64_t workspace_bytes, void* stream);
 int qlinear_bf16_gemm_grad_w(const void* grad_out, const void* x, void* grad_w, int dtype,
-                             int64_t M, int64_t N, int64_t K, void* stream);
+                             int64_t M, int64_t N, int64_t K, void* workspace,
+                             int64_t workspace_bytes, void* stream);
 
 /*
  * Low-rank adapters of many requests beside a shared projection.  For every

@@ -38,7 +38,13 @@ def test_gated_refusals(q):
                      (FAKE, FAKE, FAKE, 2, 2, 8, 4), (FAKE, FAKE, FAKE, 0, -1, 8, 4), (FAKE, FAKE, FAKE, 0, 2, 0, 4),
                      (FAKE, FAKE, FAKE, 0, 2, 8, 0), (ODD, FAKE, FAKE, 0, 2, 8, 4), (FAKE, FAKE, TWO, 0, 2, 8, 4),
                      (FAKE, FAKE, FAKE, 0, 1 << 40, 1 << 40, 4)):
-            assert call(*args, None) == q.ERR_INVALID_ARG, args
+            assert call(*args, None, 0, None) == q.ERR_INVALID_ARG, args
+        for ws, size in ((None, 16), (FAKE, -1), (TWO, 64)):
+            assert call(FAKE, FAKE, FAKE, 0, 2, 8, 4, ws, size, None) == q.ERR_INVALID_ARG
+    need = ctypes.c_int64(-1)
+    for m, n, k in ((-1, 8, 4), (2, 0, 4), (2, 8, 0), (1 << 40, 1 << 40, 4)):
+        assert L.qlinear_bf16_gemm_grad_workspace_size(m, n, k, ctypes.byref(need), None) == q.ERR_INVALID_ARG
+    assert L.qlinear_bf16_gemm_grad_workspace_size(2, 8, 4, None, None) == q.ERR_INVALID_ARG
 
 
 def test_lora_refusals(q):

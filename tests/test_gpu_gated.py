@@ -6,6 +6,8 @@ are off by t = (K + 8) u B; |act'| is at most 1.13, so the product by 1.13 t_g |
 and by (32 + 4 |z|) u of itself for the activation's own float32 steps, z its sigmoid's argument (its
 rounding reaches the result |z|-fold).  An output rounded to bfloat16 adds half a step, 2^-8."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -105,7 +107,7 @@ def check_forward(q, rng, m, f, k, fp8, act, out_dtype, addend=None, odd=False):
 
 SHAPES = [(1, 1, 1), (1, 16, 32), (2, 5, 7), (3, 33, 64), (4, 40, 100), (1, 130, 1023), (5, 64, 65), (16, 48, 256), (17, 31, 130),
           (33, 64, 64), (64, 128, 512), (65, 100, 96), (100, 257, 320), (130, 384, 1024), (300, 70, 2050),
-          (3, 40, 2056), (16, 24, 8192), (9, 17, 4104), (5, 70, 6000), (4, 21, 16400), (2, 9, 517)]
+          (260, 100, 133), (200, 4000, 192), (3, 40, 2056), (16, 24, 8192), (9, 17, 4104), (5, 70, 6000), (4, 21, 16400), (2, 9, 517)]
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -193,9 +195,24 @@ def test_linear_gradients(q, dtype, m, n, k, odd):
         assert close(got, ref, (terms + 8) * U * bound, dtype)
 
 
-@pytest.mark.parametrize("m,n,k", [(2048, 2816, 1024), (1000, 4096, 1536), (4099, 520, 2048)])
+@pytest.mark.parametrize("m,n,k", [(2048, 2816, 1024), (1000, 4096, 1536), (4099, 520, 2048), (4096, 3000, 3328), (300, 9000, 264),
+                                   (3000, 264, 520), (1500, 8256, 2040)])
 def test_linear_gradients_large(q, m, n, k):
     test_linear_gradients(q, torch.bfloat16, m, n, k, False)
+
+
+def test_linear_gradients_with_and_without_workspace(q):
+    """Sums split over blocks and whole ones: both within the tolerance, and repeatable."""
+    m, n, k = 200, 6000, 136
+    rng = np.random.default_rng(8)
+    dy, w, x = random(rng, (m, n)), random(rng, (n, k)), random(rng, (m, k))
+    need = ctypes.c_int64(0)
+    assert q.lib.qlinear_bf16_gemm_grad_workspace_size(m, n, k, ctypes.byref(need), None) == 0 and need.value > 0
+    ref, bound = f64(dy) @ f64(w), np.abs(f64(dy)) @ np.abs(f64(w))
+    for ws in (torch.empty(need.value, dtype=torch.uint8, device=DEV), torch.empty(16, dtype=torch.uint8, device=DEV)):
+        got = q.bf16_gemm_grad_x(dy, w, out_dtype=torch.float32, workspace=ws)
+        assert close(got, ref, (n + 8) * U * bound, torch.float32)
+        assert torch.equal(got, q.bf16_gemm_grad_x(dy, w, out_dtype=torch.float32, workspace=ws))
 
 
 @pytest.mark.parametrize("act", ACTS)

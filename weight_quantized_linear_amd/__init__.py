@@ -126,8 +126,9 @@ EXPORTED = {
     "qlinear_swiglu_backward": [_p, _p, _p, _i, _i64, _i64, _p],
     "qlinear_gated_gemm": [_p, _i, _p, _p, _i, _p, _i, _p, _i, _i64, _i64, _i64, _f, _f, _i, _p],
     "qlinear_gated_backward": [_p, _i, _p, _i, _p, _i64, _i64, _i, _p],
-    "qlinear_bf16_gemm_grad_x": [_p, _p, _p, _i, _i64, _i64, _i64, _p],
-    "qlinear_bf16_gemm_grad_w": [_p, _p, _p, _i, _i64, _i64, _i64, _p],
+    "qlinear_bf16_gemm_grad_workspace_size": [_i64, _i64, _i64, ctypes.POINTER(_i64), ctypes.POINTER(_i64)],
+    "qlinear_bf16_gemm_grad_x": [_p, _p, _p, _i, _i64, _i64, _i64, _p, _i64, _p],
+    "qlinear_bf16_gemm_grad_w": [_p, _p, _p, _i, _i64, _i64, _i64, _p, _i64, _p],
     "qlinear_lora_workspace_size": [_i64, _i64, _i64, _i64, ctypes.POINTER(_i64)],
     "qlinear_lora_gemm": [_p, _p, _p, _p, _p, _p, _p, _p, _i, _p, _i64, _i64, _i64, _i64, _i64, _i64, _p, _i64, _p],
     "qlinear_lora_backward_workspace_size": [_i64, _i64, _i64, _i64, _i64, _i64, ctypes.POINTER(_i64)],
@@ -972,36 +973,50 @@ def gated_gemm_backward(grad_out: torch.Tensor, pre: torch.Tensor, w: torch.Tens
             bf16_gemm_grad_w(grad_pre, x, out_dtype=grad_w_dtype) if need_w else None)
 
 
+@functools.lru_cache(maxsize=1024)
+def _grad_bytes(m: int, n: int, k: int, device: int):
+    """The workspaces of the dense layer's gradients (``qlinear_bf16_gemm_grad_workspace_size``) on a device."""
+    x, w = _i64(0), _i64(0)
+    with torch.cuda.device(device):
+        _check(lib.qlinear_bf16_gemm_grad_workspace_size(m, n, k, ctypes.byref(x), ctypes.byref(w)),
+               "qlinear_bf16_gemm_grad_workspace_size")
+    return x.value, w.value
+
+
 def bf16_gemm_grad_x(grad_out: torch.Tensor, w: torch.Tensor, out: torch.Tensor | None = None,
-                     out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+                     out_dtype: torch.dtype = torch.bfloat16, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """grad_out [M, N] @ w [N, K]: the gradient of ``bf16_gemm`` with respect to x
-    (``qlinear_bf16_gemm_grad_x``)."""
+    (``qlinear_bf16_gemm_grad_x``).  ``workspace``: a device tensor (None: allocated where
+    the call takes one)."""
     grad_out, w = _bf16_matrix(grad_out, "grad_out"), _bf16_matrix(w, "w")
     (m, n), k = grad_out.shape, w.shape[1]
     if w.shape[0] != n:
         raise ValueError(f"shapes: grad_out {tuple(grad_out.shape)} must be [M, N], w {tuple(w.shape)} must be [N, K]")
     code = _float_code(out_dtype, "out_dtype")
     out = _out(out, (m, k), out_dtype, w.device)
-    _together(w, grad_out, out)
-    if m > 0:
-        _call("qlinear_bf16_gemm_grad_x", w, _ptr(grad_out), _ptr(w), _ptr(out), code, m, n, k)
+    if m == 0:
+        return out
+    ws = _bytes(workspace, _grad_bytes(m, n, k, w.get_device())[0], w.device)
+    _together(w, grad_out, out, ws)
+    _call("qlinear_bf16_gemm_grad_x", w, _ptr(grad_out), _ptr(w), _ptr(out), code, m, n, k, _opt(ws), _size_of(ws))
     return out
 
 
 def bf16_gemm_grad_w(grad_out: torch.Tensor, x: torch.Tensor, out: torch.Tensor | None = None,
-                     out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+                     out_dtype: torch.dtype = torch.bfloat16, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """grad_out [M, N]^T @ x [M, K]: the gradient of ``bf16_gemm`` with respect to w
-    (``qlinear_bf16_gemm_grad_w``); zeros for M = 0."""
+    (``qlinear_bf16_gemm_grad_w``); zeros for M = 0.  ``workspace`` as ``bf16_gemm_grad_x``."""
     grad_out, x = _bf16_matrix(grad_out, "grad_out"), _bf16_matrix(x, "x")
     (m, n), k = grad_out.shape, x.shape[1]
     if x.shape[0] != m:
         raise ValueError(f"shapes: grad_out {tuple(grad_out.shape)} must be [M, N], x {tuple(x.shape)} must be [M, K]")
     code = _float_code(out_dtype, "out_dtype")
     out = _out(out, (n, k), out_dtype, x.device)
-    _together(x, grad_out, out)
     if m == 0:
         return out.zero_()
-    _call("qlinear_bf16_gemm_grad_w", x, _ptr(grad_out), _ptr(x), _ptr(out), code, m, n, k)
+    ws = _bytes(workspace, _grad_bytes(m, n, k, x.get_device())[1], x.device)
+    _together(x, grad_out, out, ws)
+    _call("qlinear_bf16_gemm_grad_w", x, _ptr(grad_out), _ptr(x), _ptr(out), code, m, n, k, _opt(ws), _size_of(ws))
     return out
 
 

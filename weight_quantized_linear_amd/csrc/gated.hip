@@ -21,8 +21,8 @@ constexpr int kThreads = 256;
 
 // ---------------------------------------------------------------- products of any shape
 
-// C[m, n] = sum_k A[m, k] B[n, k] in tiles of 64 x 64, for sizes and addresses that the tiles
-// with wide loads do not take.  A and B lie with k contiguous (TA / TB false: rows of `lda`) or
+// C[m, n] = sum_k A[m, k] B[n, k] in tiles of 64 x 64, for K below the 8 or 16 values that the other tiles
+// load at once.  A and B lie with k contiguous (TA / TB false: rows of `lda`) or
 // with the other axis contiguous.  Operands go through LDS as bfloat16 (FP8 codes widen exactly).
 // 4 waves of 32 x 32, MFMA 16x16x32.  GATED: rows 0 .. 31 of the tile's B are gate rows, 32 .. 63
 // the up rows of the same columns, so a lane holds both factors of its outputs.
@@ -361,14 +361,31 @@ struct OutSlab {
   }
 };
 
-// TA, TB: operand stored across k.
+// A wave's results, FM x FN blocks of 32 x 32 from row m0 and column n0 on, through its slab at `mine`.
+template <int OUT, int FM, int FN>
+__device__ __forceinline__ void product_out(char* mine, const v16f (&acc)[FM][FN], void* out, int64_t m0, int64_t n0,
+                                            int64_t M, int64_t N, bool vec) {
+  const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+  const OutSlab<OUT, 32 * FN> slab{mine};
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) slab.put(8 * (v / 4) + 4 * h + v % 4, 32 * j + r, acc[i][j][v]);
+    slab.flush(out, N, m0 + 32 * i, n0, M, N, vec);
+  }
+}
+
+// TA, TB: operand stored across k.  blockIdx.y: a part of K, whose sums go to the float32 plane of its own behind out.
 template <bool TA, bool TB, int BM, int BN, int S, int WY, int NW, int OUT>
 __global__ __launch_bounds__(64 * NW) void product_kernel(Operand a, Operand b, void* __restrict__ out, int64_t M,
-                                                          int64_t N, int64_t K, int vec) {
+                                                          int64_t N, int64_t K, int64_t strips, int vec) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   using AOp = std::conditional_t<TA, TurnedOperand<BM, NW>, RowsOperand<BM, NW, 2, PlainRows>>;
   using BOp = std::conditional_t<TB, TurnedOperand<BN, NW>, RowsOperand<BN, NW, 2, PlainRows>>;
   using L = ProductLayout<AOp, BOp, BM, BN, S, WY, NW>;
+  static_assert(NW * OutSlab<OUT, 32 * L::FN>::kBytes <= L::kLds, "staging");
   int64_t tm, tn;
   tile_of_block(blockIdx.x, (M + BM - 1) / BM, (N + BN - 1) / BN, tm, tn);
   AOp ao;
@@ -376,52 +393,47 @@ __global__ __launch_bounds__(64 * NW) void product_kernel(Operand a, Operand b, 
   ao.init(a, PlainRows{tm * BM, M}, K);
   bo.init(b, PlainRows{tn * BN, N}, K);
   v16f acc[L::FM][L::FN];
-  product_tile<AOp, BOp, BM, BN, S, WY, NW>(lds, ao, bo, K, acc);
-
-  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, r = lane & 31, h = lane >> 5;
-  const int64_t m0 = tm * BM + wid / L::WX * (BM / WY), n0 = tn * BN + wid % L::WX * (BN / L::WX);
-  using Out = OutSlab<OUT, 32 * L::FN>;
-  static_assert(NW * Out::kBytes <= L::kLds, "staging");
+  const int64_t all = (K + kStripK - 1) / kStripK, s0 = blockIdx.y * strips;
+  product_tile<AOp, BOp, BM, BN, S, WY, NW>(lds, ao, bo, K, s0, all - s0 < strips ? all - s0 : strips, acc);
+  const int wid = threadIdx.x >> 6;
   block_barrier();  // every wave is done with the last strip
-  const Out slab{lds + wid * Out::kBytes};
-#pragma unroll
-  for (int i = 0; i < L::FM; ++i) {
-#pragma unroll
-    for (int j = 0; j < L::FN; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) slab.put(8 * (v / 4) + 4 * h + v % 4, 32 * j + r, acc[i][j][v]);
-    slab.flush(out, N, m0 + 32 * i, n0, M, N, vec);
-  }
+  product_out<OUT>(lds + wid * OutSlab<OUT, 32 * L::FN>::kBytes, acc,
+                   reinterpret_cast<char*>(out) + blockIdx.y * M * N * (OUT ? 2 : 4), tm * BM + wid / L::WX * (BM / WY),
+                   tn * BN + wid % L::WX * (BN / L::WX), M, N, vec);
 }
 
-// The gated product: a wave's columns are FN / 2 times 32 gate and the 32 up columns beside them.
-template <int EB, int BM, int BF, int S, int WY, int NW, int OUT>
-__global__ __launch_bounds__(64 * NW) void gated_kernel(Operand x, Operand w, GatedOut o, int64_t M, int64_t F, int64_t K,
-                                                        int vec, int pre_vec) {
-  extern __shared__ __attribute__((aligned(16))) char lds[];
-  constexpr int BN = 2 * BF;
-  using AOp = RowsOperand<BM, NW, 2, PlainRows>;
-  using BOp = RowsOperand<BN, NW, EB, GatedRows>;
-  using L = ProductLayout<AOp, BOp, BM, BN, S, WY, NW>;
-  static_assert(L::FN % 2 == 0, "gate and up of a column in one wave");
+// The same at any address and size (K >= 8), 128 x 128.
+template <bool TA, bool TB, int OUT>
+__global__ __launch_bounds__(256) void product_staged_kernel(Operand a, Operand b, void* __restrict__ out, int64_t M,
+                                                            int64_t N, int64_t K) {
+  constexpr int BM = 128, BN = 128, WY = 2, NW = 4;
+  using AOp = std::conditional_t<TA, StagedTurned<BM, NW, 8>, StagedRows<BM, NW, 2, PlainRows, 8>>;
+  using BOp = std::conditional_t<TB, StagedTurned<BN, NW, 8>, StagedRows<BN, NW, 2, PlainRows, 8>>;
+  constexpr int kSlab = OutSlab<OUT, 64>::kBytes, kTiles = AOp::kBytes + BOp::kBytes;
+  __shared__ __attribute__((aligned(16))) char lds[kTiles > NW * kSlab ? kTiles : NW * kSlab];
   int64_t tm, tn;
-  tile_of_block(blockIdx.x, (M + BM - 1) / BM, (F + BF - 1) / BF, tm, tn);
+  tile_of_block(blockIdx.x, (M + BM - 1) / BM, (N + BN - 1) / BN, tm, tn);
   AOp ao;
   BOp bo;
-  ao.init(x, PlainRows{tm * BM, M}, K);
-  bo.init(w, GatedRows{tn * BF, F}, K);
-  v16f acc[L::FM][L::FN];
-  product_tile<AOp, BOp, BM, BN, S, WY, NW>(lds, ao, bo, K, acc);
+  ao.init(a, PlainRows{tm * BM, M}, K);
+  bo.init(b, PlainRows{tn * BN, N}, K);
+  v16f acc[2][2];
+  staged_tile<AOp, BOp, BM, BN, WY, NW>(lds, ao, bo, K, acc);
+  const int wid = threadIdx.x >> 6;
+  wait_lds();
+  block_barrier();
+  product_out<OUT>(lds + wid * kSlab, acc, out, tm * BM + wid / 2 * 64, tn * BN + wid % 2 * 64, M, N, false);
+}
 
-  constexpr int FC = L::FN / 2;  // blocks of 32 columns
-  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, r = lane & 31, h = lane >> 5;
-  const int64_t m0 = tm * BM + wid / L::WX * (BM / WY), f0 = tn * BF + wid % L::WX * (BF / L::WX);
-  using Out = OutSlab<0, 32 * FC>;  // the wider of the types that leave by it
-  static_assert(NW * Out::kBytes <= L::kLds, "staging");
-  block_barrier();  // every wave is done with the last strip
-  char* const mine = lds + wid * Out::kBytes;
+// A wave's part of a gated product: its columns are FN / 2 times 32 gate and the 32 up columns beside them.
+template <int OUT, int FM, int FN>
+__device__ __forceinline__ void gated_out(char* mine, v16f (&acc)[FM][FN], const GatedOut& o, int64_t m0, int64_t f0,
+                                          int64_t M, int64_t F, bool vec, bool pre_vec) {
+  static_assert(FN % 2 == 0, "gate and up of a column in one wave");
+  constexpr int FC = FN / 2;  // blocks of 32 columns
+  const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
 #pragma unroll
-  for (int i = 0; i < L::FM; ++i) {
+  for (int i = 0; i < FM; ++i) {
 #pragma unroll
     for (int j = 0; j < FC; ++j)
 #pragma unroll
@@ -437,34 +449,80 @@ __global__ __launch_bounds__(64 * NW) void gated_kernel(Operand x, Operand w, Ga
         acc[i][2 * j][v] = g;
         acc[i][2 * j + 1][v] = u;
       }
-    auto leave = [&](auto type, void* out, int64_t ld, int64_t col, int64_t cols, bool v16, auto value) {
+    auto leave = [&](auto type, void* out, int64_t ld, bool v16, auto value) {
       const OutSlab<decltype(type)::value, 32 * FC> slab{mine};
 #pragma unroll
       for (int j = 0; j < FC; ++j)
 #pragma unroll
         for (int v = 0; v < 16; ++v) slab.put(8 * (v / 4) + 4 * h + v % 4, 32 * j + r, value(j, v));
-      slab.flush(out, ld, m0 + 32 * i, col, M, cols, v16);
+      slab.flush(out, ld, m0 + 32 * i, f0, M, F, v16);
     };
     if (o.pre) {
       auto gate = [&](int j, int v) { return acc[i][2 * j][v]; };
       auto up = [&](int j, int v) { return acc[i][2 * j + 1][v]; };
       if (o.pre_bf16) {
-        leave(std::integral_constant<int, 1>{}, o.pre, 2 * F, f0, F, pre_vec, gate);
-        leave(std::integral_constant<int, 1>{}, reinterpret_cast<uint16_t*>(o.pre) + F, 2 * F, f0, F, pre_vec, up);
+        leave(std::integral_constant<int, 1>{}, o.pre, 2 * F, pre_vec, gate);
+        leave(std::integral_constant<int, 1>{}, reinterpret_cast<uint16_t*>(o.pre) + F, 2 * F, pre_vec, up);
       } else {
-        leave(std::integral_constant<int, 0>{}, o.pre, 2 * F, f0, F, pre_vec, gate);
-        leave(std::integral_constant<int, 0>{}, reinterpret_cast<float*>(o.pre) + F, 2 * F, f0, F, pre_vec, up);
+        leave(std::integral_constant<int, 0>{}, o.pre, 2 * F, pre_vec, gate);
+        leave(std::integral_constant<int, 0>{}, reinterpret_cast<float*>(o.pre) + F, 2 * F, pre_vec, up);
       }
     }
     auto value = [&](auto act) {
-      leave(std::integral_constant<int, OUT>{}, o.out, F, f0, F, vec, [&](int j, int v) {
-        return gated_one<decltype(act)::value>(acc[i][2 * j][v], acc[i][2 * j + 1][v]);
-      });
+      leave(std::integral_constant<int, OUT>{}, o.out, F, vec,
+            [&](int j, int v) { return gated_one<decltype(act)::value>(acc[i][2 * j][v], acc[i][2 * j + 1][v]); });
     };
     if (o.act == 1) value(std::integral_constant<int, 1>{});
     else if (o.act == 2) value(std::integral_constant<int, 2>{});
     else value(std::integral_constant<int, 3>{});
   }
+}
+
+template <int EB, int BM, int BF, int S, int WY, int NW, int OUT>
+__global__ __launch_bounds__(64 * NW) void gated_kernel(Operand x, Operand w, GatedOut o, int64_t M, int64_t F, int64_t K,
+                                                        int vec, int pre_vec) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  constexpr int BN = 2 * BF;
+  using AOp = RowsOperand<BM, NW, 2, PlainRows>;
+  using BOp = RowsOperand<BN, NW, EB, GatedRows>;
+  using L = ProductLayout<AOp, BOp, BM, BN, S, WY, NW>;
+  constexpr int kSlab = OutSlab<0, 16 * L::FN>::kBytes;  // the wider of the types that leave by it
+  static_assert(NW * kSlab <= L::kLds, "staging");
+  int64_t tm, tn;
+  tile_of_block(blockIdx.x, (M + BM - 1) / BM, (F + BF - 1) / BF, tm, tn);
+  AOp ao;
+  BOp bo;
+  ao.init(x, PlainRows{tm * BM, M}, K);
+  bo.init(w, GatedRows{tn * BF, F}, K);
+  v16f acc[L::FM][L::FN];
+  product_tile<AOp, BOp, BM, BN, S, WY, NW>(lds, ao, bo, K, 0, (K + kStripK - 1) / kStripK, acc);
+  const int wid = threadIdx.x >> 6;
+  block_barrier();  // every wave is done with the last strip
+  gated_out<OUT>(lds + wid * kSlab, acc, o, tm * BM + wid / L::WX * (BM / WY), tn * BF + wid % L::WX * (BF / L::WX), M, F,
+                 vec, pre_vec);
+}
+
+// The same at any address and size (K >= 8, 16 with FP8).
+template <int EB, int BM, int OUT>
+__global__ __launch_bounds__(256) void gated_staged_kernel(Operand x, Operand w, GatedOut o, int64_t M, int64_t F,
+                                                          int64_t K) {
+  constexpr int BF = 64, WY = 2, NW = 4, G = 16 / EB;
+  using AOp = StagedRows<BM, NW, 2, PlainRows, G>;
+  using BOp = StagedRows<2 * BF, NW, EB, GatedRows, G>;
+  constexpr int kSlab = OutSlab<0, 32>::kBytes, kTiles = AOp::kBytes + BOp::kBytes;
+  __shared__ __attribute__((aligned(16))) char lds[kTiles > NW * kSlab ? kTiles : NW * kSlab];
+  int64_t tm, tn;
+  tile_of_block(blockIdx.x, (M + BM - 1) / BM, (F + BF - 1) / BF, tm, tn);
+  AOp ao;
+  BOp bo;
+  ao.init(x, PlainRows{tm * BM, M}, K);
+  bo.init(w, GatedRows{tn * BF, F}, K);
+  v16f acc[BM / 64][2];
+  staged_tile<AOp, BOp, BM, 2 * BF, WY, NW>(lds, ao, bo, K, acc);
+  const int wid = threadIdx.x >> 6;
+  wait_lds();
+  block_barrier();
+  gated_out<OUT>(lds + wid * kSlab, acc, o, tm * BM + wid / 2 * (BM / 2), tn * BF + wid % 2 * 32, M, F, false, false);
 }
 
 // ---------------------------------------------------------------- gradient of the activation
@@ -523,30 +581,72 @@ bool tiled_rows(const void* p, int64_t row_bytes) {
   return aligned16(p) && row_bytes % 16 == 0 && row_bytes < (int64_t(1) << 23);
 }
 
+int64_t rounds(int64_t M, int64_t N, int64_t bm, int64_t bn, int64_t slots) {
+  return (((M + bm - 1) / bm) * ((N + bn - 1) / bn) + slots - 1) / slots;
+}
+
+// The products' tiles: 256 x 256 has a CU to itself, of the others two blocks share one and cover each
+// other's barriers.  Measured per strip of K and round over the card, us (8192 x 4096, K = 8192 and 4096 x 2048, K =
+// 11264): 1.7, 1.26 (192 x 128), 1.0 (128 x 128), and 8 more a round.  The one with the least time is taken.
+enum ProductTile { kTile256, kTile192, kTile128 };
+ProductTile product_tile_of(int64_t M, int64_t N, int64_t strips, int num_cus) {
+  const double t256 = rounds(M, N, 256, 256, num_cus) * (8 + 1.7 * strips);
+  const double t192 = rounds(M, N, 192, 128, 2 * num_cus) * (8 + 1.26 * strips);
+  const double t128 = rounds(M, N, 128, 128, 2 * num_cus) * (8 + 1.0 * strips);
+  return t256 <= t192 && t256 <= t128 ? kTile256 : t192 <= t128 ? kTile192 : kTile128;
+}
+
+// Parts of K where tiles of 128 x 128 leave more than half of the places for them empty: so many that they are
+// full, of 8 strips (512 values) at least.  4096 x 2048 never; M = N = 512, K = 11264 SPLITFIGURE
+int product_parts(int64_t M, int64_t N, int64_t K, int num_cus) {
+  const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128), strips = (K + kStripK - 1) / kStripK;
+  if (tiles * 2 > 2 * num_cus) return 1;
+  return int(std::max<int64_t>(1, std::min({int64_t(16), 2 * num_cus / tiles, strips / 8})));
+}
+
 template <bool TA, bool TB>
 hipError_t launch_product(const Operand& a, const Operand& b, void* out, int out_bf16, int64_t M, int64_t N, int64_t K,
-                          int num_cus, hipStream_t s) {
+                          int num_cus, float* ws, size_t ws_bytes, hipStream_t s) {
+  const int64_t strips = (K + kStripK - 1) / kStripK;
   const int vec = aligned16(out) && N * (out_bf16 ? 2 : 4) % 16 == 0;
-  auto go = [&](auto bm, auto bn, auto stages, auto wy, auto type) {
-    constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value, S = decltype(stages)::value;
-    constexpr int WY = decltype(wy)::value, OUT = decltype(type)::value;
+  auto go = [&](auto bm, auto bn, auto nw, auto type, void* to, int parts) {
+    constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value, NW = decltype(nw)::value, OUT = decltype(type)::value;
     const int64_t blocks = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
     if (blocks > kMaxGrid) return hipErrorInvalidValue;
-    return launch_big_lds<product_kernel<TA, TB, BM, BN, S, WY, 8, OUT>>(S * (BM + BN) * 128, blocks, 512, s, a, b, out, M,
-                                                                         N, K, vec);
+    constexpr int kLds = 2 * (BM + BN) * 128;
+    static std::atomic<uint64_t> lds_set{0};
+    constexpr auto kernel = product_kernel<TA, TB, BM, BN, 2, 2, NW, OUT>;
+    if (hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(kernel), kLds, lds_set)) return e;
+    return launch(kernel, dim3(unsigned(blocks), unsigned(parts)), dim3(64 * NW), kLds, s, a, b, to, M, N, K,
+                  (strips + parts - 1) / parts, parts > 1 ? int(N % 4 == 0) : vec);
   };
-  auto by_type = [&](auto bm, auto bn, auto stages, auto wy) {
-    return out_bf16 ? go(bm, bn, stages, wy, Int<1>{}) : go(bm, bn, stages, wy, Int<0>{});
+  int parts = product_parts(M, N, K, num_cus);
+  if (parts > 1 && ws && ws_bytes >= size_t(parts) * M * N * 4) {
+    parts = int((strips + (strips + parts - 1) / parts - 1) / ((strips + parts - 1) / parts));  // none of them empty
+    if (hipError_t e = go(Int<128>{}, Int<128>{}, Int<4>{}, Int<0>{}, ws, parts)) return e;
+    return launch_splitk_reduce(ws, out, out_bf16, M, N, parts, 1.f, s, Epilogue{});
+  }
+  auto by_type = [&](auto bm, auto bn, auto nw) {
+    return out_bf16 ? go(bm, bn, nw, Int<1>{}, out, 1) : go(bm, bn, nw, Int<0>{}, out, 1);
   };
-  if (((M + 255) / 256) * ((N + 255) / 256) >= num_cus) return by_type(Int<256>{}, Int<256>{}, Int<2>{}, Int<2>{});
-  return by_type(Int<128>{}, Int<256>{}, Int<3>{}, Int<2>{});
+  switch (product_tile_of(M, N, strips, num_cus)) {
+    case kTile256: return by_type(Int<256>{}, Int<256>{}, Int<8>{});
+    case kTile192: return by_type(Int<192>{}, Int<128>{}, Int<4>{});
+    default: return by_type(Int<128>{}, Int<128>{}, Int<4>{});
+  }
 }
 
 template <bool TA, bool TB>
 hipError_t launch_product_any(const uint16_t* a, int64_t lda, const uint16_t* b, int64_t ldb, void* out, int out_bf16,
                               int64_t M, int64_t N, int64_t K, hipStream_t s) {
-  const int64_t blocks = (M + kAnyTile - 1) / kAnyTile * ((N + kAnyTile - 1) / kAnyTile);
+  const int64_t tile = K >= 8 ? 128 : kAnyTile, blocks = (M + tile - 1) / tile * ((N + tile - 1) / tile);
   if (blocks > kMaxGrid) return hipErrorInvalidValue;
+  if (K >= 8) {
+    const Operand ao{reinterpret_cast<const char*>(a), 2 * lda, M}, bo{reinterpret_cast<const char*>(b), 2 * ldb, N};
+    if (out_bf16)
+      return launch(product_staged_kernel<TA, TB, 1>, dim3(unsigned(blocks)), dim3(256), 0, s, ao, bo, out, M, N, K);
+    return launch(product_staged_kernel<TA, TB, 0>, dim3(unsigned(blocks)), dim3(256), 0, s, ao, bo, out, M, N, K);
+  }
   return launch(product_any_kernel<TA, TB>, dim3(unsigned(blocks)), dim3(kThreads), 0, s, a, lda, b, ldb, out, out_bf16, M,
                 N, K);
 }
@@ -590,25 +690,40 @@ hipError_t launch_gated_gemm(const void* w, int fp8, const uint16_t* x, const Ga
     };
     return fp8 ? by_parts(Int<1>{}) : by_parts(Int<2>{});
   }
+  const Operand xo{reinterpret_cast<const char*>(x), 2 * K, M}, wo{static_cast<const char*>(w), K * eb, 2 * F};
   if (tiled_rows(x, K * 2) && tiled_rows(w, K * eb) && 2 * F * K * eb < kNowhere) {
-    const Operand xo{reinterpret_cast<const char*>(x), 2 * K, M}, wo{static_cast<const char*>(w), K * eb, 2 * F};
     const int vec = aligned16(o.out) && F * (o.out_bf16 ? 2 : 4) % 16 == 0;
     const int pre_vec = aligned16(o.pre) && F * (o.pre_bf16 ? 2 : 4) % 16 == 0;
-    auto go = [&](auto bytes, auto bm, auto bf, auto stages, auto wy, auto out) {
+    auto go = [&](auto bytes, auto bm, auto bf, auto stages, auto nw, auto out) {
       constexpr int EB = decltype(bytes)::value, BM = decltype(bm)::value, BF = decltype(bf)::value;
-      constexpr int S = decltype(stages)::value, WY = decltype(wy)::value, OUT = decltype(out)::value;
-      using L = ProductLayout<RowsOperand<BM, 8, 2, PlainRows>, RowsOperand<2 * BF, 8, EB, GatedRows>, BM, 2 * BF, S, WY, 8>;
+      constexpr int S = decltype(stages)::value, NW = decltype(nw)::value, OUT = decltype(out)::value;
+      using L = ProductLayout<RowsOperand<BM, NW, 2, PlainRows>, RowsOperand<2 * BF, NW, EB, GatedRows>, BM, 2 * BF, S, 2, NW>;
       const int64_t blocks = ((M + BM - 1) / BM) * ((F + BF - 1) / BF);
       if (blocks > kMaxGrid) return hipErrorInvalidValue;
-      return launch_big_lds<gated_kernel<EB, BM, BF, S, WY, 8, OUT>>(L::kLds, blocks, 512, s, xo, wo, o, M, F, K, vec,
+      return launch_big_lds<gated_kernel<EB, BM, BF, S, 2, NW, OUT>>(L::kLds, blocks, 64 * NW, s, xo, wo, o, M, F, K, vec,
                                                                      pre_vec);
     };
+    // Tiles of 256 x 128 columns with a CU to themselves, or of 128 x 64 of which two blocks share one, by the time of
+    // their rounds as for the products above: M = 256, F = 14336, K = 4096 91 and 70 us, M = 500 105 and 125.
+    const bool wide = 1.75 * rounds(M, F, 256, 128, num_cus) <= 1.05 * rounds(M, F, 128, 64, 2 * num_cus);
     auto by_tile = [&](auto bytes, auto out) {
-      if (M > 128) return go(bytes, Int<256>{}, Int<128>{}, Int<2>{}, Int<2>{}, out);
-      return go(bytes, Int<64>{}, Int<128>{}, Int<3>{}, Int<2>{}, out);
+      if (M <= 128) return go(bytes, Int<64>{}, Int<128>{}, Int<3>{}, Int<8>{}, out);
+      if (wide) return go(bytes, Int<256>{}, Int<128>{}, Int<2>{}, Int<8>{}, out);
+      return go(bytes, Int<128>{}, Int<64>{}, Int<2>{}, Int<4>{}, out);
     };
     auto by_out = [&](auto bytes) { return o.out_bf16 ? by_tile(bytes, Int<1>{}) : by_tile(bytes, Int<0>{}); };
     return fp8 ? by_out(Int<1>{}) : by_out(Int<2>{});
+  }
+  if (K >= 16 / eb) {
+    const int64_t bm = M <= 64 ? 64 : 128, blocks = (M + bm - 1) / bm * ((F + 63) / 64);
+    if (blocks > kMaxGrid) return hipErrorInvalidValue;
+    auto go = [&](auto kernel) { return launch(kernel, dim3(unsigned(blocks)), dim3(256), 0, s, xo, wo, o, M, F, K); };
+    auto by_out = [&](auto bytes, auto rows) {
+      constexpr int EB = decltype(bytes)::value, BM = decltype(rows)::value;
+      return o.out_bf16 ? go(gated_staged_kernel<EB, BM, 1>) : go(gated_staged_kernel<EB, BM, 0>);
+    };
+    auto by_rows = [&](auto bytes) { return bm == 64 ? by_out(bytes, Int<64>{}) : by_out(bytes, Int<128>{}); };
+    return fp8 ? by_rows(Int<1>{}) : by_rows(Int<2>{});
   }
   const int64_t blocks = (M + kAnyTile - 1) / kAnyTile * ((F + 31) / 32);
   if (blocks > kMaxGrid) return hipErrorInvalidValue;
@@ -637,21 +752,29 @@ hipError_t launch_gated_grad(const void* dy, int dy_bf16, const void* pre, int p
   });
 }
 
+// Bytes of workspace that the product of [M, K] and [N, K] takes, 0: none.
+size_t bf16_product_ws_bytes(int64_t M, int64_t N, int64_t K, int num_cus) {
+  const int parts = K >= 8 && N % 8 == 0 ? product_parts(M, N, K, num_cus) : 1;
+  return parts > 1 ? size_t(parts) * M * N * 4 : 0;
+}
+
 // dx[m, k] = sum_n dout[m, n] w[n, k]
 hipError_t launch_bf16_grad_x(const uint16_t* dout, const uint16_t* w, void* dx, int dx_bf16, int64_t M, int64_t N,
-                              int64_t K, int num_cus, hipStream_t s) {
+                              int64_t K, int num_cus, float* ws, size_t ws_bytes, hipStream_t s) {
   if (tiled_rows(dout, 2 * N) && tiled_rows(w, 2 * K))
     return launch_product<false, true>(Operand{reinterpret_cast<const char*>(dout), 2 * N, M},
-                                       Operand{reinterpret_cast<const char*>(w), 2 * K, N}, dx, dx_bf16, M, K, N, num_cus, s);
+                                       Operand{reinterpret_cast<const char*>(w), 2 * K, N}, dx, dx_bf16, M, K, N, num_cus,
+                                       ws, ws_bytes, s);
   return launch_product_any<false, true>(dout, N, w, K, dx, dx_bf16, M, K, N, s);
 }
 
 // dw[n, k] = sum_m dout[m, n] x[m, k]
 hipError_t launch_bf16_grad_w(const uint16_t* dout, const uint16_t* x, void* dw, int dw_bf16, int64_t M, int64_t N,
-                              int64_t K, int num_cus, hipStream_t s) {
+                              int64_t K, int num_cus, float* ws, size_t ws_bytes, hipStream_t s) {
   if (tiled_rows(dout, 2 * N) && tiled_rows(x, 2 * K))
     return launch_product<true, true>(Operand{reinterpret_cast<const char*>(dout), 2 * N, M},
-                                      Operand{reinterpret_cast<const char*>(x), 2 * K, M}, dw, dw_bf16, N, K, M, num_cus, s);
+                                      Operand{reinterpret_cast<const char*>(x), 2 * K, M}, dw, dw_bf16, N, K, M, num_cus,
+                                      ws, ws_bytes, s);
   return launch_product_any<true, true>(dout, N, x, K, dw, dw_bf16, N, K, M, s);
 }
 

@@ -202,10 +202,11 @@ hipError_t launch_gated_gemm(const void* w, int fp8, const uint16_t* x, const Ga
                              int num_cus, hipStream_t s);
 hipError_t launch_gated_grad(const void* dy, int dy_bf16, const void* pre, int pre_bf16, uint16_t* dpre, int act, int64_t M,
                              int64_t F, hipStream_t s);
+size_t bf16_product_ws_bytes(int64_t M, int64_t N, int64_t K, int num_cus);
 hipError_t launch_bf16_grad_x(const uint16_t* dout, const uint16_t* w, void* dx, int dx_bf16, int64_t M, int64_t N,
-                              int64_t K, int num_cus, hipStream_t s);
+                              int64_t K, int num_cus, float* ws, size_t ws_bytes, hipStream_t s);
 hipError_t launch_bf16_grad_w(const uint16_t* dout, const uint16_t* x, void* dw, int dw_bf16, int64_t M, int64_t N,
-                              int64_t K, int num_cus, hipStream_t s);
+                              int64_t K, int num_cus, float* ws, size_t ws_bytes, hipStream_t s);
 
 // lora.hip: low-rank adapters; the workspaces' sizes depend on the sizes alone.
 // Zeros over a whole number of 2-byte values.

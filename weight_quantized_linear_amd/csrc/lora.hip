@@ -251,6 +251,18 @@ __global__ __launch_bounds__(kThreads) void lora_shrink_kernel(const uint16_t* _
 // follow each other.  SMALL: R < 8.  TAIL: N % 8 != 0.
 constexpr int kSpan = 1024;
 
+// Even lanes' second against odd lanes' first pieces.  Lanes 2 j and 2 j + 1 that hold pieces (first, second) of their
+// own rows come to hold pieces 0 of both rows, and pieces 1 of both; and back.
+__device__ __forceinline__ void swap_pairs(Eight<1>& first, Eight<1>& second, bool odd) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t mine = odd ? first.v[0][w] : second.v[0][w];
+    const uint32_t other = __builtin_amdgcn_update_dpp(0, int(mine), 0xB1, 0xF, 0xF, false);  // the neighbour's
+    if (odd) first.v[0][w] = other;
+    else second.v[0][w] = other;
+  }
+}
+
 template <int BM, int OUT, bool WHOLE, bool SMALL, bool TAIL>
 __global__ __launch_bounds__(kThreads) void lora_expand_kernel(const float* __restrict__ plane, int splits,
                                                               const uint16_t* __restrict__ b, Groups g,
@@ -260,6 +272,7 @@ __global__ __launch_bounds__(kThreads) void lora_expand_kernel(const float* __re
                                                               int64_t span) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   constexpr int FM = BM / 16, P = pieces_of(OUT);
+  constexpr bool kPaired = OUT == 1;  // whole 128-byte lines a load and a store; float32 pieces are 32 bytes a lane
   const int R8 = int((R + 7) / 8), row_bytes = 16 * P * R8 + 16;
   char* const zs = lds;                                   // [BM][P R8 eights + 1 of padding]
   int* const cum = reinterpret_cast<int*>(lds + BM * row_bytes);
@@ -314,13 +327,16 @@ __global__ __launch_bounds__(kThreads) void lora_expand_kernel(const float* __re
     Eight<OUT> add[FM][2];
     if (base) {
 #pragma unroll
-      for (int m = 0; m < FM; ++m)
+      for (int m = 0; m < FM; ++m) {
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          const int64_t row = row0 + (16 * m + i < rows ? 16 * m + i : rows - 1), n = n0 + 32 * p + 8 * q;
+          const int r = 16 * m + (kPaired ? (i & ~1) + p : i);
+          const int64_t row = row0 + (r < rows ? r : rows - 1), n = n0 + 32 * (kPaired ? i & 1 : p) + 8 * q;
           if constexpr (TAIL) add[m][p].template load<true>(base, row * N + n, N - n);
           else add[m][p].get_at(base, row * N + (n < N ? n : N - 8));
         }
+        if constexpr (kPaired) swap_pairs(add[m][0], add[m][1], i & 1);
+      }
     }
     v4f acc[FM][2][2];
 #pragma unroll
@@ -369,10 +385,10 @@ __global__ __launch_bounds__(kThreads) void lora_expand_kernel(const float* __re
       }
     }
 #pragma unroll
-    for (int m = 0; m < FM; ++m)
+    for (int m = 0; m < FM; ++m) {
+      Eight<OUT> to[2];
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        const int64_t n = n0 + 32 * p + 8 * q;
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = acc[m][p][e / 4][e % 4];
@@ -382,10 +398,16 @@ __global__ __launch_bounds__(kThreads) void lora_expand_kernel(const float* __re
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] += o[e];
         }
-        Eight<OUT> to;
-        to.put(v);
-        if (16 * m + i < rows) to.template store<TAIL>(out, (row0 + 16 * m + i) * N + n, N - n);
+        to[p].put(v);
       }
+      if constexpr (kPaired) swap_pairs(to[0], to[1], i & 1);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int r = 16 * m + (kPaired ? (i & ~1) + p : i);
+        const int64_t n = n0 + 32 * (kPaired ? i & 1 : p) + 8 * q;
+        if (r < rows) to[p].template store<TAIL>(out, (row0 + r) * N + n, N - n);
+      }
+    }
   }
 }
 
@@ -578,10 +600,11 @@ bool tall(int64_t T, int64_t G) { return T > 16 * G; }
 
 int64_t tile_count(int64_t T, int64_t G, int bm) { return std::min(T, T / bm + G); }
 
-// Parts of the long axis: as many as fill the card twice (512 blocks), of 512 values at least.
+// Parts of the long axis: as many as make 128 blocks, of 512 values at least.  More blocks take the first product
+// less time and the second more, which adds the parts (4096 rows, R = 64, N = 14336: 97 us, 103 with 512 blocks).
 int shrink_splits(int64_t T, int64_t G, int64_t K, int64_t R) {
   const int64_t tiles = tile_count(T, G, tall(T, G) ? 64 : 16) * ((R + 63) / 64);
-  return int(std::max<int64_t>(1, std::min({int64_t(16), (512 + tiles - 1) / tiles, K / 512})));
+  return int(std::max<int64_t>(1, std::min({int64_t(16), (128 + tiles - 1) / tiles, K / 512})));
 }
 
 hipError_t launch_shrink(const uint16_t* x, const uint16_t* a, const Groups& g, float* plane, int splits, int64_t K,

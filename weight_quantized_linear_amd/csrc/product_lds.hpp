@@ -60,10 +60,10 @@ struct GatedRows {
 // ROWS rows of 64 values of k, EB bytes each (2: bfloat16, 1: FP8).
 template <int ROWS, int NW, int EB, class Map>
 struct RowsOperand {
+  using Layout = RowsOperand;
   static constexpr int kRowBytes = kStripK * EB, kCpr = kRowBytes / 16, kBytes = ROWS * kRowBytes;
   static constexpr int kInst = ROWS * kCpr / (64 * NW);
   static_assert(ROWS * kCpr % (64 * NW) == 0, "whole instructions");
-  static constexpr bool kPairs = EB == 1;  // one read serves two steps
   const char* base;
   int64_t bytes;  // from base to the operand's end
   uint32_t off[kInst], tail[kInst];
@@ -89,13 +89,22 @@ struct RowsOperand {
   }
 };
 
+// Where row k of a turned strip of CPR 16-byte pieces a row has its pieces: exchanged in groups of four (64 bytes), so
+// that a group's four rows k .. k + 3 lie in different quarters of the 64 banks.  Rows of 16 or 32 pieces all begin in
+// the same quarter; rows of 24 begin in quarters 0, 2, 0, 2.
+template <int CPR>
+__device__ __forceinline__ int turned_swz(int k) {
+  static_assert(CPR % 8 == 0 && CPR >= 16, "groups of four, in pairs");
+  return CPR % 16 == 0 ? (k & 3) << 2 : (k >> 1 & 1) << 2;
+}
+
 // 64 rows of k, COLS values (bfloat16) each.
 template <int COLS, int NW>
 struct TurnedOperand {
+  using Layout = TurnedOperand;
   static constexpr int kRowBytes = COLS * 2, kCpr = kRowBytes / 16, kBytes = kStripK * kRowBytes;
   static constexpr int kInst = kStripK * kCpr / (64 * NW);
-  static_assert(kStripK * kCpr % (64 * NW) == 0 && kCpr >= 16, "whole instructions");
-  static constexpr bool kPairs = false;
+  static_assert(kStripK * kCpr % (64 * NW) == 0, "whole instructions");
   const char* base;
   int64_t bytes, step;
   uint32_t off[kInst];
@@ -107,7 +116,7 @@ struct TurnedOperand {
     step = kStripK * o.ld;
 #pragma unroll
     for (int q = 0; q < kInst; ++q) {
-      const int c = (q * NW + wid) * 64 + lane, k = c / kCpr, g = (c % kCpr) ^ ((k & 3) << 2);
+      const int c = (q * NW + wid) * 64 + lane, k = c / kCpr, g = (c % kCpr) ^ turned_swz<kCpr>(k);
       off[q] = uint32_t(k * o.ld + 16 * g);
     }
   }
@@ -117,6 +126,107 @@ struct TurnedOperand {
     const __amdgpu_buffer_rsrc_t r = strip_rsrc(base + at, bytes - at, none);
 #pragma unroll
     for (int q = 0; q < kInst; ++q) bdma16(r, tile + (q * NW + wid) * 1024, off[q], 0);
+  }
+};
+
+// ---------------------------------------------------------------- operands at any address
+//
+// The same tiles through registers, for operands whose rows are not whole 16-byte pieces at aligned
+// addresses: 16-byte loads at any address, held inside the operand.  A row's last values, where it does
+// not end with a piece of G of them, are taken as the G values before its end, of which those that the piece before
+// had are zeroed, in both operands: G = 8, or 16 beside FP8 weights, so that k means the same in both.  K >= G.
+
+typedef u32x4 u32x4_loose1 __attribute__((aligned(1)));
+
+// Value index of slot k of the contraction, and whether it is a repetition.
+template <int G>
+__device__ __forceinline__ int64_t slot_value(int64_t k, int64_t K) {
+  const int64_t first = k & ~int64_t(G - 1);
+  return first > K - G ? K - G + (k - first) : k;
+}
+
+template <int ROWS, int NW, int EB, class Map, int G>
+struct StagedRows {
+  using Layout = RowsOperand<ROWS, NW, EB, Map>;
+  static constexpr int kBytes = Layout::kBytes, kInst = Layout::kInst, kCpr = Layout::kCpr, kValues = 16 / EB;
+  const char* row[kInst];
+  int64_t K;
+  u32x4 held[kInst];
+  __device__ __forceinline__ void init(const Operand& o, const Map& map, int64_t k) {
+    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+    K = k;
+#pragma unroll
+    for (int q = 0; q < kInst; ++q) {
+      const int r = ((q * NW + wid) * 64 + lane) / kCpr;
+      row[q] = o.p + (map.first + (map.in(r) ? map.at(r) : 0)) * o.ld;  // rows past the end: any, not stored
+    }
+  }
+  __device__ __forceinline__ void load(int64_t strip) {
+    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+    const bool ends = (strip + 1) * kStripK > K;
+#pragma unroll
+    for (int q = 0; q < kInst; ++q) {
+      const int c = (q * NW + wid) * 64 + lane, g = (c % kCpr) ^ swz<kCpr>(c / kCpr);
+      const int64_t k = strip * kStripK + g * kValues;
+      held[q] = *reinterpret_cast<const u32x4_loose1*>(row[q] + (ends ? slot_value<G>(k, K) : k) * EB);
+    }
+  }
+  __device__ __forceinline__ void store(char* tile, int64_t strip) {
+    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+#pragma unroll
+    for (int q = 0; q < kInst; ++q) {
+      const int c = (q * NW + wid) * 64 + lane, g = (c % kCpr) ^ swz<kCpr>(c / kCpr);
+      if ((strip + 1) * kStripK > K) {
+        const int64_t k = strip * kStripK + g * kValues, first = k & ~int64_t(G - 1), v = slot_value<G>(k, K);
+#pragma unroll
+        for (int e = 0; e < kValues; ++e)
+          if (v + e < first) held[q][e * EB / 4] &= ~((EB == 2 ? 0xFFFFu : 0xFFu) << (e * EB % 4 * 8));
+      }
+      *reinterpret_cast<u32x4*>(tile + c * 16) = held[q];
+    }
+  }
+};
+
+template <int COLS, int NW, int G>
+struct StagedTurned {
+  using Layout = TurnedOperand<COLS, NW>;
+  static constexpr int kBytes = Layout::kBytes, kInst = Layout::kInst, kCpr = Layout::kCpr;
+  const char* base;
+  int64_t ld, K, left;  // left: columns from the tile's first on
+  u32x4 held[kInst];
+  __device__ __forceinline__ void init(const Operand& o, const PlainRows& map, int64_t k) {
+    base = o.p + map.first * 2;
+    ld = o.ld;
+    K = k;
+    left = map.rows - map.first;
+  }
+  __device__ __forceinline__ void load(int64_t strip) {
+    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+#pragma unroll
+    for (int q = 0; q < kInst; ++q) {
+      const int c = (q * NW + wid) * 64 + lane, kk = c / kCpr, g = (c % kCpr) ^ turned_swz<kCpr>(kk);
+      const char* const p = base + slot_value<G>(strip * kStripK + kk, K) * ld;
+      if (left >= COLS) {
+        held[q] = *reinterpret_cast<const u32x4_loose1*>(p + 16 * g);
+      } else {  // the last columns' tile: value by value, held inside the row
+        held[q] = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int64_t col = 8 * g + e < left ? 8 * g + e : left - 1;
+          held[q][e / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(p)[col]) << (16 * (e % 2));
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void store(char* tile, int64_t strip) {
+    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+#pragma unroll
+    for (int q = 0; q < kInst; ++q) {
+      const int c = (q * NW + wid) * 64 + lane, kk = c / kCpr;
+      const int64_t k = strip * kStripK + kk;
+      const bool repeated = slot_value<G>(k, K) < (k & ~int64_t(G - 1));
+      *reinterpret_cast<u32x4*>(tile + c * 16) = repeated ? u32x4{0, 0, 0, 0} : held[q];
+    }
   }
 };
 
@@ -169,7 +279,7 @@ struct Fragments<TurnedOperand<COLS, NW>, NF> {
 #pragma unroll
     for (int n = 0; n < NF; ++n) {
       const int byte = (row0 + 32 * n + 16 * (lane / 16 % 2) + 4 * (lane % 4)) * 2;
-      at[n] = uint32_t((16 * h + j) * COLS * 2 + (byte ^ (j << 6)));
+      at[n] = uint32_t((16 * h + j) * COLS * 2 + (byte ^ (turned_swz<COLS / 8>(j) << 4)));
     }
   }
   template <int U>
@@ -193,11 +303,11 @@ struct ProductLayout {
   static_assert(kLds <= 160 * 1024 && (S - 1) * kLoads < 64 && S >= 2, "ring");
 };
 
-// The sums of the tile whose operands `a` and `b` were set to: acc[i][j][v] belongs to row
+// The sums of the tile whose operands `a` and `b` were set to, over the strips s0 .. s0 + nk - 1 of K (nk >= 1): acc[i][j][v] belongs to row
 // 32 i + 8 (v / 4) + 4 h + v % 4 and column 32 j + lane % 32 of the wave's part.
 template <class AOp, class BOp, int BM, int BN, int S, int WY, int NW>
 __device__ __forceinline__ void product_tile(
-    char* lds, const AOp& a, const BOp& b, int64_t K,
+    char* lds, const AOp& a, const BOp& b, int64_t K, int64_t s0, int64_t nk,
     v16f (&acc)[ProductLayout<AOp, BOp, BM, BN, S, WY, NW>::FM][ProductLayout<AOp, BOp, BM, BN, S, WY, NW>::FN]) {
   using L = ProductLayout<AOp, BOp, BM, BN, S, WY, NW>;
   constexpr int FM = L::FM, FN = L::FN, NM = FM * FN;
@@ -206,12 +316,11 @@ __device__ __forceinline__ void product_tile(
   Fragments<BOp, FN> fb;
   fa.init(wid / L::WX * (BM / WY));
   fb.init(wid % L::WX * (BN / L::WX));
-  const int64_t nk = (K + kStripK - 1) / kStripK;
   auto fetch = [&](int64_t s) {
     char* st = lds + int(s % S) * L::kStage;
-    const bool last = s == nk - 1, none = s >= nk;
-    a.fetch(st, none ? 0 : s, last, none);
-    b.fetch(st + AOp::kBytes, none ? 0 : s, last, none);
+    const bool last = (s0 + s + 1) * kStripK >= K, none = s >= nk;
+    a.fetch(st, none ? 0 : s0 + s, last, none);
+    b.fetch(st + AOp::kBytes, none ? 0 : s0 + s, last, none);
   };
 #pragma unroll
   for (int i = 0; i < FM; ++i)
@@ -263,6 +372,51 @@ __device__ __forceinline__ void product_tile(
   inner(lds + int((nk - 1) % S) * L::kStage);
   mma(aY, bY);
   wait_vm<0>();  // no LDS write may land after the block ends
+}
+
+// The same with staged operands and one stage: a strip's values wait in registers while the strip before
+// is multiplied.  With few registers and little LDS a block, others on its CU cover its barriers.
+template <class AOp, class BOp, int BM, int BN, int WY, int NW>
+__device__ __forceinline__ void staged_tile(char* lds, AOp& a, BOp& b, int64_t K,
+                                            v16f (&acc)[BM / WY / 32][BN / (NW / WY) / 32]) {
+  constexpr int WX = NW / WY, FM = BM / WY / 32, FN = BN / WX / 32;
+  const int wid = threadIdx.x >> 6;
+  Fragments<typename AOp::Layout, FM> fa;
+  Fragments<typename BOp::Layout, FN> fb;
+  fa.init(wid / WX * (BM / WY));
+  fb.init(wid % WX * (BN / WX));
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = v16f{};
+  const int64_t nk = (K + kStripK - 1) / kStripK;
+  a.load(0);
+  b.load(0);
+  for (int64_t s = 0; s < nk; ++s) {
+    if (s > 0) {
+      wait_lds();
+      block_barrier();  // every wave has read the strip before
+    }
+    a.store(lds, s);
+    b.store(lds + AOp::kBytes, s);
+    if (s + 1 < nk) {
+      a.load(s + 1);
+      b.load(s + 1);
+    }
+    wait_lds();
+    block_barrier();
+    v8bf af[FM], bf[FN];
+    static_for<4>([&](auto uc) {
+      constexpr int U = decltype(uc)::value;
+      fa.template read<U>(lds, af);
+      fb.template read<U>(lds + AOp::kBytes, bf);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[i], bf[j], acc[i][j], 0, 0, 0);
+    });
+  }
 }
 
 }  // namespace qlinear

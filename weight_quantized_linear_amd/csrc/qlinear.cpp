@@ -799,24 +799,40 @@ int qlinear_gated_backward(const void* grad_out, int grad_dtype, const void* pre
                                   static_cast<uint16_t*>(grad_pre), activation, M, F, static_cast<hipStream_t>(stream)));
 }
 
+int qlinear_bf16_gemm_grad_workspace_size(int64_t M, int64_t N, int64_t K, int64_t* x_bytes, int64_t* w_bytes) {
+  if (x_bytes) *x_bytes = 0;
+  if (w_bytes) *w_bytes = 0;
+  if ((!x_bytes && !w_bytes) || M < 0 || N <= 0 || K <= 0 || !fits(M ? M : 1, N) || !fits(M ? M : 1, K) || !fits(N, K))
+    return QLINEAR_ERR_INVALID_ARG;
+  int num_cus = 0;
+  if (int st = current_device(&num_cus)) return st;
+  if (x_bytes && M) *x_bytes = int64_t(bf16_product_ws_bytes(M, K, N, num_cus));
+  if (w_bytes && M) *w_bytes = int64_t(bf16_product_ws_bytes(N, K, M, num_cus));
+  return QLINEAR_OK;
+}
+
 int qlinear_bf16_gemm_grad_x(const void* grad_out, const void* w, void* grad_x, int dtype, int64_t M, int64_t N, int64_t K,
-                             void* stream) {
+                             void* workspace, int64_t workspace_bytes, void* stream) {
   if (!linear_grad_ok(grad_out, w, grad_x, dtype, M, N, K)) return QLINEAR_ERR_INVALID_ARG;
+  if (int st = check_workspace(workspace, workspace_bytes)) return st;
   int num_cus = 0;
   if (int st = current_device(&num_cus)) return st;
   if (M == 0) return QLINEAR_OK;
   return finish(launch_bf16_grad_x(static_cast<const uint16_t*>(grad_out), static_cast<const uint16_t*>(w), grad_x,
-                                   dtype == QLINEAR_BF16, M, N, K, num_cus, static_cast<hipStream_t>(stream)));
+                                   dtype == QLINEAR_BF16, M, N, K, num_cus, static_cast<float*>(workspace),
+                                   size_t(workspace_bytes), static_cast<hipStream_t>(stream)));
 }
 
 int qlinear_bf16_gemm_grad_w(const void* grad_out, const void* x, void* grad_w, int dtype, int64_t M, int64_t N, int64_t K,
-                             void* stream) {
+                             void* workspace, int64_t workspace_bytes, void* stream) {
   if (!linear_grad_ok(grad_out, x, grad_w, dtype, M, N, K)) return QLINEAR_ERR_INVALID_ARG;
+  if (int st = check_workspace(workspace, workspace_bytes)) return st;
   int num_cus = 0;
   if (int st = current_device(&num_cus)) return st;
   if (M == 0) return finish(launch_clear(grad_w, N * K * int64_t(out_size(dtype)), static_cast<hipStream_t>(stream)));
   return finish(launch_bf16_grad_w(static_cast<const uint16_t*>(grad_out), static_cast<const uint16_t*>(x), grad_w,
-                                   dtype == QLINEAR_BF16, M, N, K, num_cus, static_cast<hipStream_t>(stream)));
+                                   dtype == QLINEAR_BF16, M, N, K, num_cus, static_cast<float*>(workspace),
+                                   size_t(workspace_bytes), static_cast<hipStream_t>(stream)));
 }
 
 int qlinear_lora_workspace_size(int64_t num_groups, int64_t T, int64_t K, int64_t R, int64_t* bytes) {
