@@ -117,32 +117,6 @@ struct Eight {
   }
 };
 
-// Eight values at p + i (16-byte aligned) to and from float32.
-template <int BF16>
-__device__ __forceinline__ void load_eight(const void* p, int64_t i, float (&f)[8]) {
-  if constexpr (BF16) {
-    Elem<1>::unpack(ld16(reinterpret_cast<const uint16_t*>(p) + i), f);
-  } else {
-    const u32x4 a = ld16(reinterpret_cast<const float*>(p) + i), b = ld16(reinterpret_cast<const float*>(p) + i + 4);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      f[e] = __uint_as_float(a[e]);
-      f[4 + e] = __uint_as_float(b[e]);
-    }
-  }
-}
-
-template <int BF16>
-__device__ __forceinline__ void store_eight(void* p, int64_t i, const float (&f)[8]) {
-  if constexpr (BF16) {
-    *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(p) + i) = Elem<1>::pack(f);
-  } else {
-    const float a[4] = {f[0], f[1], f[2], f[3]}, b[4] = {f[4], f[5], f[6], f[7]};
-    *reinterpret_cast<u32x4*>(reinterpret_cast<float*>(p) + i) = Elem<0>::pack(a);
-    *reinterpret_cast<u32x4*>(reinterpret_cast<float*>(p) + i + 4) = Elem<0>::pack(b);
-  }
-}
-
 // One value at p[at].
 __device__ __forceinline__ void put_float(void* p, int64_t at, float v, int bf16) {
   if (bf16) reinterpret_cast<uint16_t*>(p)[at] = Elem<1>::put(v);

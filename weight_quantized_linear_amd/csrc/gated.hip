@@ -402,10 +402,10 @@ __global__ __launch_bounds__(64 * NW) void product_kernel(Operand a, Operand b, 
                    tn * BN + wid % L::WX * (BN / L::WX), M, N, vec);
 }
 
-// The same at any address and size (K >= 8), 128 x 128.
+// The same at any address, 128 x 128; K and the widths of turned operands are 8 at least.
 template <bool TA, bool TB, int OUT>
 __global__ __launch_bounds__(256) void product_staged_kernel(Operand a, Operand b, void* __restrict__ out, int64_t M,
-                                                            int64_t N, int64_t K) {
+                                                            int64_t N, int64_t K, int64_t strips) {
   constexpr int BM = 128, BN = 128, WY = 2, NW = 4;
   using AOp = std::conditional_t<TA, StagedTurned<BM, NW, 8>, StagedRows<BM, NW, 2, PlainRows, 8>>;
   using BOp = std::conditional_t<TB, StagedTurned<BN, NW, 8>, StagedRows<BN, NW, 2, PlainRows, 8>>;
@@ -418,11 +418,12 @@ __global__ __launch_bounds__(256) void product_staged_kernel(Operand a, Operand 
   ao.init(a, PlainRows{tm * BM, M}, K);
   bo.init(b, PlainRows{tn * BN, N}, K);
   v16f acc[2][2];
-  staged_tile<AOp, BOp, BM, BN, WY, NW>(lds, ao, bo, K, acc);
+  const int64_t all = (K + kStripK - 1) / kStripK, s0 = blockIdx.y * strips;
+  staged_tile<AOp, BOp, BM, BN, WY, NW>(lds, ao, bo, s0, all - s0 < strips ? all - s0 : strips, acc);
   const int wid = threadIdx.x >> 6;
   wait_lds();
   block_barrier();
-  product_out<OUT>(lds + wid * kSlab, acc, out, tm * BM + wid / 2 * 64, tn * BN + wid % 2 * 64, M, N, false);
+  product_out<OUT>(lds + wid * kSlab, acc, reinterpret_cast<char*>(out) + blockIdx.y * M * N * (OUT ? 2 : 4), tm * BM + wid / 2 * 64, tn * BN + wid % 2 * 64, M, N, false);
 }
 
 // A wave's part of a gated product: its columns are FN / 2 times 32 gate and the 32 up columns beside them.
@@ -518,7 +519,7 @@ __global__ __launch_bounds__(256) void gated_staged_kernel(Operand x, Operand w,
   ao.init(x, PlainRows{tm * BM, M}, K);
   bo.init(w, GatedRows{tn * BF, F}, K);
   v16f acc[BM / 64][2];
-  staged_tile<AOp, BOp, BM, 2 * BF, WY, NW>(lds, ao, bo, K, acc);
+  staged_tile<AOp, BOp, BM, 2 * BF, WY, NW>(lds, ao, bo, 0, (K + kStripK - 1) / kStripK, acc);
   const int wid = threadIdx.x >> 6;
   wait_lds();
   block_barrier();
@@ -527,39 +528,35 @@ __global__ __launch_bounds__(256) void gated_staged_kernel(Operand x, Operand w,
 
 // ---------------------------------------------------------------- gradient of the activation
 
-// dpre of kPer values a thread; VEC: 16-byte aligned rows, whole pieces.
-template <int ACT, int DY, int PRE, bool VEC>
+// Eight columns of a row a thread, at any address; TAIL: F % 8 != 0.  Bound by HBM: 4096 x 5632 from float32 pre-activations
+// 54 us, 6.0 TB/s.
+template <int ACT, int DY, int PRE, bool TAIL>
 __global__ __launch_bounds__(kThreads) void gated_grad_kernel(const void* __restrict__ dy, const void* __restrict__ pre,
                                                              uint16_t* __restrict__ dpre, int64_t M, int64_t F) {
-  constexpr int P = VEC ? 8 : 1;
-  const int64_t per = (F + P - 1) / P;
+  const int64_t per = (F + 7) / 8;
   for (int64_t at = int64_t(blockIdx.x) * kThreads + threadIdx.x; at < M * per; at += int64_t(gridDim.x) * kThreads) {
-    const int64_t m = at / per, f = at % per * P;
-    float d[P], g[P], u[P];
-    if constexpr (VEC) {
-      load_eight<DY>(dy, m * F + f, d);
-      load_eight<PRE>(pre, m * 2 * F + f, g);
-      load_eight<PRE>(pre, m * 2 * F + F + f, u);
-    } else {
-      d[0] = Elem<DY>::get(reinterpret_cast<const typename Elem<DY>::T*>(dy)[m * F + f]);
-      g[0] = Elem<PRE>::get(reinterpret_cast<const typename Elem<PRE>::T*>(pre)[m * 2 * F + f]);
-      u[0] = Elem<PRE>::get(reinterpret_cast<const typename Elem<PRE>::T*>(pre)[m * 2 * F + F + f]);
-    }
+    const int64_t m = at / per, f = at % per * 8, left = F - f;
+    Eight<DY> d8;
+    Eight<PRE> g8, u8;
+    d8.template load<TAIL>(dy, m * F + f, left);
+    g8.template load<TAIL>(pre, m * 2 * F + f, left);
+    u8.template load<TAIL>(pre, m * 2 * F + F + f, left);
+    float d[8], g[8], u[8];
+    d8.get(d);
+    g8.get(g);
+    u8.get(u);
 #pragma unroll
-    for (int e = 0; e < P; ++e) {
+    for (int e = 0; e < 8; ++e) {
       float dg, du;
       gated_grad<ACT>(g[e], u[e], d[e], dg, du);
       g[e] = dg;
       u[e] = du;
     }
-    uint16_t* const o = dpre + m * 2 * F + f;
-    if constexpr (VEC) {
-      *reinterpret_cast<u32x4*>(o) = Elem<1>::pack(g);
-      *reinterpret_cast<u32x4*>(o + F) = Elem<1>::pack(u);
-    } else {
-      o[0] = Elem<1>::put(g[0]);
-      o[F] = Elem<1>::put(u[0]);
-    }
+    Eight<1> o;
+    o.put(g);
+    o.template store<TAIL>(dpre, m * 2 * F + f, left);
+    o.put(u);
+    o.template store<TAIL>(dpre, m * 2 * F + F + f, left);
   }
 }
 
@@ -597,58 +594,56 @@ ProductTile product_tile_of(int64_t M, int64_t N, int64_t strips, int num_cus) {
 }
 
 // Parts of K where tiles of 128 x 128 leave more than half of the places for them empty: so many that they are
-// full, of 8 strips (512 values) at least.  4096 x 2048 never; M = N = 512, K = 11264 SPLITFIGURE
+// full, of 8 strips (512 values) at least.  4096 x 2048 never; 512 x 2048, K = 11264 148 us whole, 41 split.
 int product_parts(int64_t M, int64_t N, int64_t K, int num_cus) {
   const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128), strips = (K + kStripK - 1) / kStripK;
   if (tiles * 2 > 2 * num_cus) return 1;
   return int(std::max<int64_t>(1, std::min({int64_t(16), 2 * num_cus / tiles, strips / 8})));
 }
 
+// The product of [M, K] and [N, K], either of them stored across k, in the workspace's planes where it is split.
 template <bool TA, bool TB>
-hipError_t launch_product(const Operand& a, const Operand& b, void* out, int out_bf16, int64_t M, int64_t N, int64_t K,
+hipError_t launch_product(const uint16_t* a, const uint16_t* b, void* out, int out_bf16, int64_t M, int64_t N, int64_t K,
                           int num_cus, float* ws, size_t ws_bytes, hipStream_t s) {
-  const int64_t strips = (K + kStripK - 1) / kStripK;
-  const int vec = aligned16(out) && N * (out_bf16 ? 2 : 4) % 16 == 0;
+  const int64_t lda = TA ? M : K, ldb = TB ? N : K, strips = (K + kStripK - 1) / kStripK;
+  const Operand ao{reinterpret_cast<const char*>(a), 2 * lda, TA ? K : M};
+  const Operand bo{reinterpret_cast<const char*>(b), 2 * ldb, TB ? K : N};
+  if (K < 8 || (TA && M < 8) || (TB && N < 8)) {
+    const int64_t blocks = (M + kAnyTile - 1) / kAnyTile * ((N + kAnyTile - 1) / kAnyTile);
+    if (blocks > kMaxGrid) return hipErrorInvalidValue;
+    return launch(product_any_kernel<TA, TB>, dim3(unsigned(blocks)), dim3(kThreads), 0, s, a, lda, b, ldb, out, out_bf16,
+                  M, N, K);
+  }
+  const bool aligned = tiled_rows(a, 2 * lda) && tiled_rows(b, 2 * ldb);
   auto go = [&](auto bm, auto bn, auto nw, auto type, void* to, int parts) {
     constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value, NW = decltype(nw)::value, OUT = decltype(type)::value;
-    const int64_t blocks = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
+    const int64_t blocks = ((M + BM - 1) / BM) * ((N + BN - 1) / BN), per = (strips + parts - 1) / parts;
     if (blocks > kMaxGrid) return hipErrorInvalidValue;
+    const dim3 grid{unsigned(blocks), unsigned((strips + per - 1) / per)};  // no part is empty
+    if constexpr (BM == 128) {
+      if (!aligned) return launch(product_staged_kernel<TA, TB, OUT>, grid, dim3(256), 0, s, ao, bo, to, M, N, K, per);
+    }
     constexpr int kLds = 2 * (BM + BN) * 128;
     static std::atomic<uint64_t> lds_set{0};
     constexpr auto kernel = product_kernel<TA, TB, BM, BN, 2, 2, NW, OUT>;
     if (hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(kernel), kLds, lds_set)) return e;
-    return launch(kernel, dim3(unsigned(blocks), unsigned(parts)), dim3(64 * NW), kLds, s, a, b, to, M, N, K,
-                  (strips + parts - 1) / parts, parts > 1 ? int(N % 4 == 0) : vec);
+    const int vec = aligned16(to) && N * (OUT ? 2 : 4) % 16 == 0;
+    return launch(kernel, grid, dim3(64 * NW), kLds, s, ao, bo, to, M, N, K, per, vec);
   };
-  int parts = product_parts(M, N, K, num_cus);
+  const int parts = product_parts(M, N, K, num_cus);
   if (parts > 1 && ws && ws_bytes >= size_t(parts) * M * N * 4) {
-    parts = int((strips + (strips + parts - 1) / parts - 1) / ((strips + parts - 1) / parts));  // none of them empty
     if (hipError_t e = go(Int<128>{}, Int<128>{}, Int<4>{}, Int<0>{}, ws, parts)) return e;
-    return launch_splitk_reduce(ws, out, out_bf16, M, N, parts, 1.f, s, Epilogue{});
+    const int64_t per = (strips + parts - 1) / parts;
+    return launch_splitk_reduce(ws, out, out_bf16, M, N, int((strips + per - 1) / per), 1.f, s, Epilogue{});
   }
   auto by_type = [&](auto bm, auto bn, auto nw) {
     return out_bf16 ? go(bm, bn, nw, Int<1>{}, out, 1) : go(bm, bn, nw, Int<0>{}, out, 1);
   };
-  switch (product_tile_of(M, N, strips, num_cus)) {
+  switch (aligned ? product_tile_of(M, N, strips, num_cus) : kTile128) {
     case kTile256: return by_type(Int<256>{}, Int<256>{}, Int<8>{});
     case kTile192: return by_type(Int<192>{}, Int<128>{}, Int<4>{});
     default: return by_type(Int<128>{}, Int<128>{}, Int<4>{});
   }
-}
-
-template <bool TA, bool TB>
-hipError_t launch_product_any(const uint16_t* a, int64_t lda, const uint16_t* b, int64_t ldb, void* out, int out_bf16,
-                              int64_t M, int64_t N, int64_t K, hipStream_t s) {
-  const int64_t tile = K >= 8 ? 128 : kAnyTile, blocks = (M + tile - 1) / tile * ((N + tile - 1) / tile);
-  if (blocks > kMaxGrid) return hipErrorInvalidValue;
-  if (K >= 8) {
-    const Operand ao{reinterpret_cast<const char*>(a), 2 * lda, M}, bo{reinterpret_cast<const char*>(b), 2 * ldb, N};
-    if (out_bf16)
-      return launch(product_staged_kernel<TA, TB, 1>, dim3(unsigned(blocks)), dim3(256), 0, s, ao, bo, out, M, N, K);
-    return launch(product_staged_kernel<TA, TB, 0>, dim3(unsigned(blocks)), dim3(256), 0, s, ao, bo, out, M, N, K);
-  }
-  return launch(product_any_kernel<TA, TB>, dim3(unsigned(blocks)), dim3(kThreads), 0, s, a, lda, b, ldb, out, out_bf16, M,
-                N, K);
 }
 
 }  // namespace
@@ -736,46 +731,37 @@ hipError_t launch_gated_gemm(const void* w, int fp8, const uint16_t* x, const Ga
 
 hipError_t launch_gated_grad(const void* dy, int dy_bf16, const void* pre, int pre_bf16, uint16_t* dpre, int act, int64_t M,
                              int64_t F, hipStream_t s) {
-  const bool vec = F % 8 == 0 && aligned16(dy) && aligned16(pre) && aligned16(dpre);
-  const int64_t items = M * (vec ? F / 8 : F), blocks = (items + kThreads - 1) / kThreads;
+  const int64_t blocks = (M * ((F + 7) / 8) + kThreads - 1) / kThreads;
   return by_act(act, [&](auto a) {
     constexpr int ACT = decltype(a)::value;
     auto go = [&](auto kernel) {
       return launch(kernel, dim3(unsigned(blocks < 65536 ? blocks : 65536)), dim3(kThreads), 0, s, dy, pre, dpre, M, F);
     };
-    auto by_vec = [&](auto v) {
-      constexpr bool VEC = decltype(v)::value;
-      if (dy_bf16) return pre_bf16 ? go(gated_grad_kernel<ACT, 1, 1, VEC>) : go(gated_grad_kernel<ACT, 1, 0, VEC>);
-      return pre_bf16 ? go(gated_grad_kernel<ACT, 0, 1, VEC>) : go(gated_grad_kernel<ACT, 0, 0, VEC>);
+    auto by_tail = [&](auto tail) {
+      constexpr bool TAIL = decltype(tail)::value;
+      if (dy_bf16) return pre_bf16 ? go(gated_grad_kernel<ACT, 1, 1, TAIL>) : go(gated_grad_kernel<ACT, 1, 0, TAIL>);
+      return pre_bf16 ? go(gated_grad_kernel<ACT, 0, 1, TAIL>) : go(gated_grad_kernel<ACT, 0, 0, TAIL>);
     };
-    return vec ? by_vec(std::true_type{}) : by_vec(std::false_type{});
+    return F % 8 ? by_tail(std::true_type{}) : by_tail(std::false_type{});
   });
 }
 
 // Bytes of workspace that the product of [M, K] and [N, K] takes, 0: none.
 size_t bf16_product_ws_bytes(int64_t M, int64_t N, int64_t K, int num_cus) {
-  const int parts = K >= 8 && N % 8 == 0 ? product_parts(M, N, K, num_cus) : 1;
+  const int parts = product_parts(M, N, K, num_cus);
   return parts > 1 ? size_t(parts) * M * N * 4 : 0;
 }
 
 // dx[m, k] = sum_n dout[m, n] w[n, k]
 hipError_t launch_bf16_grad_x(const uint16_t* dout, const uint16_t* w, void* dx, int dx_bf16, int64_t M, int64_t N,
                               int64_t K, int num_cus, float* ws, size_t ws_bytes, hipStream_t s) {
-  if (tiled_rows(dout, 2 * N) && tiled_rows(w, 2 * K))
-    return launch_product<false, true>(Operand{reinterpret_cast<const char*>(dout), 2 * N, M},
-                                       Operand{reinterpret_cast<const char*>(w), 2 * K, N}, dx, dx_bf16, M, K, N, num_cus,
-                                       ws, ws_bytes, s);
-  return launch_product_any<false, true>(dout, N, w, K, dx, dx_bf16, M, K, N, s);
+  return launch_product<false, true>(dout, w, dx, dx_bf16, M, K, N, num_cus, ws, ws_bytes, s);
 }
 
 // dw[n, k] = sum_m dout[m, n] x[m, k]
 hipError_t launch_bf16_grad_w(const uint16_t* dout, const uint16_t* x, void* dw, int dw_bf16, int64_t M, int64_t N,
                               int64_t K, int num_cus, float* ws, size_t ws_bytes, hipStream_t s) {
-  if (tiled_rows(dout, 2 * N) && tiled_rows(x, 2 * K))
-    return launch_product<true, true>(Operand{reinterpret_cast<const char*>(dout), 2 * N, M},
-                                      Operand{reinterpret_cast<const char*>(x), 2 * K, M}, dw, dw_bf16, N, K, M, num_cus,
-                                      ws, ws_bytes, s);
-  return launch_product_any<true, true>(dout, N, x, K, dw, dw_bf16, N, K, M, s);
+  return launch_product<true, true>(dout, x, dw, dw_bf16, N, K, M, num_cus, ws, ws_bytes, s);
 }
 
 }  // namespace qlinear

@@ -134,7 +134,8 @@ struct TurnedOperand {
 // The same tiles through registers, for operands whose rows are not whole 16-byte pieces at aligned
 // addresses: 16-byte loads at any address, held inside the operand.  A row's last values, where it does
 // not end with a piece of G of them, are taken as the G values before its end, of which those that the piece before
-// had are zeroed, in both operands: G = 8, or 16 beside FP8 weights, so that k means the same in both.  K >= G.
+// had are zeroed, in both operands: G = 8, or 16 beside FP8 weights, so that k means the same in both.  K >= G, and
+// turned operands have 8 columns at least.
 
 typedef u32x4 u32x4_loose1 __attribute__((aligned(1)));
 
@@ -206,23 +207,24 @@ struct StagedTurned {
     for (int q = 0; q < kInst; ++q) {
       const int c = (q * NW + wid) * 64 + lane, kk = c / kCpr, g = (c % kCpr) ^ turned_swz<kCpr>(kk);
       const char* const p = base + slot_value<G>(strip * kStripK + kk, K) * ld;
-      if (left >= COLS) {
-        held[q] = *reinterpret_cast<const u32x4_loose1*>(p + 16 * g);
-      } else {  // the last columns' tile: value by value, held inside the row
-        held[q] = u32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int64_t col = 8 * g + e < left ? 8 * g + e : left - 1;
-          held[q][e / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(p)[col]) << (16 * (e % 2));
-        }
-      }
+      // Eight columns that the row's end cuts are the row's last eight, moved to their places in store().
+      const int64_t col = 8 * g < left - 8 ? 8 * g : left - 8;
+      held[q] = *reinterpret_cast<const u32x4_loose1*>(p + 2 * col);
     }
   }
   __device__ __forceinline__ void store(char* tile, int64_t strip) {
     const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
 #pragma unroll
     for (int q = 0; q < kInst; ++q) {
-      const int c = (q * NW + wid) * 64 + lane, kk = c / kCpr;
+      const int c = (q * NW + wid) * 64 + lane, kk = c / kCpr, g = (c % kCpr) ^ turned_swz<kCpr>(kk);
+      if (left < COLS) {
+        const int over = 8 * g > left - 8 ? int(8 * g - (left - 8)) : 0, by = 16 * (over < 7 ? over : 7);
+        uint64_t lo = held[q].x | uint64_t(held[q].y) << 32;
+        const uint64_t hi = held[q].z | uint64_t(held[q].w) << 32;
+        lo = by >= 64 ? hi >> (by - 64) : by ? lo >> by | hi << (64 - by) : lo;
+        const uint64_t up = by >= 64 ? 0 : hi >> by;
+        held[q] = u32x4{uint32_t(lo), uint32_t(lo >> 32), uint32_t(up), uint32_t(up >> 32)};
+      }
       const int64_t k = strip * kStripK + kk;
       const bool repeated = slot_value<G>(k, K) < (k & ~int64_t(G - 1));
       *reinterpret_cast<u32x4*>(tile + c * 16) = repeated ? u32x4{0, 0, 0, 0} : held[q];
@@ -377,7 +379,7 @@ __device__ __forceinline__ void product_tile(
 // The same with staged operands and one stage: a strip's values wait in registers while the strip before
 // is multiplied.  With few registers and little LDS a block, others on its CU cover its barriers.
 template <class AOp, class BOp, int BM, int BN, int WY, int NW>
-__device__ __forceinline__ void staged_tile(char* lds, AOp& a, BOp& b, int64_t K,
+__device__ __forceinline__ void staged_tile(char* lds, AOp& a, BOp& b, int64_t s0, int64_t nk,
                                             v16f (&acc)[BM / WY / 32][BN / (NW / WY) / 32]) {
   constexpr int WX = NW / WY, FM = BM / WY / 32, FN = BN / WX / 32;
   const int wid = threadIdx.x >> 6;
@@ -389,19 +391,18 @@ __device__ __forceinline__ void staged_tile(char* lds, AOp& a, BOp& b, int64_t K
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = v16f{};
-  const int64_t nk = (K + kStripK - 1) / kStripK;
-  a.load(0);
-  b.load(0);
+  a.load(s0);
+  b.load(s0);
   for (int64_t s = 0; s < nk; ++s) {
     if (s > 0) {
       wait_lds();
       block_barrier();  // every wave has read the strip before
     }
-    a.store(lds, s);
-    b.store(lds + AOp::kBytes, s);
+    a.store(lds, s0 + s);
+    b.store(lds + AOp::kBytes, s0 + s);
     if (s + 1 < nk) {
-      a.load(s + 1);
-      b.load(s + 1);
+      a.load(s0 + s + 1);
+      b.load(s0 + s + 1);
     }
     wait_lds();
     block_barrier();
