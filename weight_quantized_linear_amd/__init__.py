@@ -685,13 +685,13 @@ def _float_tensor(t: torch.Tensor, what: str, shape=None):
     _require(t, what)
     if t.dtype not in _OUT_CODES:
         raise TypeError(f"{what} must be float32 or bfloat16, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what} must be {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _typed(t: torch.Tensor, what: str, dtype: torch.dtype, shape):
     _require(t, what)
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{what} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
 
 
@@ -874,7 +874,7 @@ def swiglu_backward(grad_y: torch.Tensor, x: torch.Tensor, grad_x: torch.Tensor 
 def _call(name: str, at: torch.Tensor, *args):
     """The C call ``name`` on the current stream of ``at``'s device, made current for the
     call where it is not."""
-    if at.is_cuda and at.get_device() != torch.cuda.current_device():
+    if at.is_cuda and at.get_device() != torch._C._cuda_getDevice():
         with torch.cuda.device(at.device):
             st = getattr(lib, name)(*args, _stream(at))
     else:
@@ -884,9 +884,10 @@ def _call(name: str, at: torch.Tensor, *args):
 
 def _together(first: torch.Tensor, *others):
     """Every given tensor on the first one's device."""
+    at = first.device
     for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"all tensors must be on one device, got {first.device} and {t.device}")
+        if t is not None and t.device != at:
+            raise ValueError(f"all tensors must be on one device, got {at} and {t.device}")
 
 
 def _opt(t):
@@ -898,9 +899,10 @@ def _code(t):
 
 
 def _bf16_matrix(t: torch.Tensor, what: str, shape=None) -> torch.Tensor:
-    t = _as_bf16(t, what)
+    if t.dtype != torch.bfloat16:
+        t = _as_bf16(t, what)
     _require(t, what)
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
         raise ValueError(f"{what} must be {'a matrix' if shape is None else tuple(shape)}, got {tuple(t.shape)}")
     return t
 
@@ -1057,7 +1059,6 @@ def _adapters(x, a, b, a_offsets, adapter_ids, scale):
     l, r = a.shape[0], a.shape[1]
     if scale is not None:
         _typed(scale, "scale", torch.float32, (l,))
-    _together(x, a, b, a_offsets, adapter_ids, scale)
     return x, a, b, t, k, b.shape[1], r, g, l
 
 
@@ -1077,7 +1078,7 @@ def lora_gemm(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, a_offsets: torc
     out = _out(out, (t, n), out_dtype, x.device)
     z = _out(None, (t, r), torch.float32, x.device) if return_z else None
     ws = _bytes(workspace, _bytes_of("qlinear_lora_workspace_size", g, t, k, r), x.device)
-    _together(x, base, out, ws)
+    _together(x, a, b, a_offsets, adapter_ids, scale, base, out, ws)
     if t > 0:
         _call("qlinear_lora_gemm", x, _ptr(x), _ptr(a), _ptr(b), _ptr(a_offsets), _ptr(adapter_ids), _opt(scale),
               _opt(base), _ptr(out), code, _opt(z), g, l, t, n, k, r, _opt(ws), _size_of(ws))
@@ -1103,7 +1104,7 @@ def lora_gemm_backward(grad_out: torch.Tensor, x: torch.Tensor, z: torch.Tensor,
     grad_a = torch.empty((l, r, k), dtype=param_dtype, device=x.device)
     grad_b = torch.empty((l, n, r), dtype=param_dtype, device=x.device)
     ws = _bytes(workspace, _bytes_of("qlinear_lora_backward_workspace_size", g, l, t, n, k, r), x.device)
-    _together(x, grad_out, z, base, grad_x, ws)
+    _together(x, a, b, a_offsets, adapter_ids, scale, grad_out, z, base, grad_x, ws)
     if t == 0:
         return grad_x, grad_a.zero_(), grad_b.zero_()
     _call("qlinear_lora_gemm_backward", x, _ptr(grad_out), _ptr(x), _ptr(z), _ptr(a), _ptr(b), _ptr(a_offsets),
@@ -1113,28 +1114,25 @@ def lora_gemm_backward(grad_out: torch.Tensor, x: torch.Tensor, z: torch.Tensor,
 
 
 def _norm_operands(residual, weight, block, block_weight, gate):
-    """The checked inputs of the norm calls -> (T, H, the rows of the gate, block and out's dtype)."""
+    """The checked inputs of the norm calls -> (T, H, the rows of the gate)."""
     _float_tensor(residual, "residual")
     if residual.dim() != 2:
         raise ValueError("residual must be [T, H]")
-    t, h = residual.shape
+    t, h = shape = residual.shape
     _float_tensor(weight, "weight", (h,))
     if block is None:
         if block_weight is not None or gate is not None:
             raise ValueError("block_weight and gate need a block")
         return t, h, 0
-    _float_tensor(block, "block", (t, h))
+    _float_tensor(block, "block", shape)
     if block_weight is not None:
         _typed(block_weight, "block_weight", weight.dtype, (h,))
     gates = 0
     if gate is not None:
-        if gate.dim() == 1:
-            gate = gate.unsqueeze(0)
-        gates = gate.shape[0]
-        _typed(gate, "gate", weight.dtype, (gates, h))
+        gates = gate.shape[0] if gate.dim() == 2 else 1
+        _typed(gate, "gate", weight.dtype, (gates, h) if gate.dim() == 2 else (h,))
         if gates == 0 or t % gates != 0:
             raise ValueError("gate must be [G, H] with G dividing T")
-    _together(residual, weight, block, block_weight, gate)
     return t, h, gates
 
 
@@ -1164,7 +1162,7 @@ def block_norm(residual: torch.Tensor, weight: torch.Tensor, block: torch.Tensor
         residual_out = _out(residual_out, (t, h), residual.dtype, residual.device)
     code = _float_code(out_dtype, "out_dtype")
     out = _out(out, (t, h), out_dtype, residual.device)
-    _together(residual, weight, out, residual_out)
+    _together(residual, weight, block, block_weight, gate, out, residual_out)
     if t > 0:
         _call("qlinear_block_norm", residual, _ptr(residual), _code(residual), _ptr(weight), _code(weight), _opt(block),
               code, _opt(block_weight), _opt(gate), gates, _opt(residual_out), _ptr(out), t, h, float(residual_scale),
@@ -1202,7 +1200,7 @@ def block_norm_backward(grad_out: torch.Tensor, grad_residual_out: torch.Tensor 
     need = _bytes_of("qlinear_block_norm_backward_workspace_size", t, h, int(block_weight is not None),
                      int(gate is not None))
     ws = _bytes(workspace, need, dev)
-    _together(residual_out, weight, grad_out, grad_residual_out, grad_residual, ws)
+    _together(residual_out, weight, block, block_weight, gate, grad_out, grad_residual_out, grad_residual, ws)
     if t == 0:
         for p in (g.weight, g.block_weight, g.gate):
             if p is not None:
