@@ -364,10 +364,10 @@ __device__ __forceinline__ void product_tile(
     wait_lds();
     wait_vm<(S - 2) * L::kLoads>();
     block_barrier();
-    fetch(kt + S);
     const char* sn = lds + int((kt + 1) % S) * L::kStage;
     fa.template read<0>(sn, aX);
     fb.template read<0>(sn + AOp::kBytes, bX);
+    fetch(kt + S);  // behind the reads: 3 to 5 % less time than in front of them
     mma(aY, bY);
     interleave<NM, L::kLoads, kReads, 0>();
   }
