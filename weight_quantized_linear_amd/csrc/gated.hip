@@ -217,8 +217,8 @@ __global__ __launch_bounds__(256) void gated_gemv_kernel(const char* __restrict_
 // stages a row), and the waves' sums meet in LDS at a tile's end.  MFMA 16x16x32: the weights' rows are the
 // result's rows and the tokens its columns: lanes 0 .. 31 end with four gate columns of a token, lanes 32 .. 63
 // with the up ones.  FP8: a lane's 16 bytes are the operands of two steps, and x is held in that order.
-// M = 13, K = 4096, F = 14336: 28 us FP8 (4.2 TB/s), 43 bfloat16 (5.5); K = 2048, F = 5504, bfloat16 13 (3.4: three tiles a
-// block, the first loads' and the last sums' latency shows).  Weights kept in the caches: 1 to 2 us more.
+// M = 13, K = 4096, F = 14336: 28 us FP8 (4.2 TB/s), 43 bfloat16 (5.5); K = 2048, F = 5504, bfloat16 13 (3.4: of its three
+// tiles a CU the first loads' and the last sums' latency shows).  Weights kept in the caches: 1 to 2 us more.
 template <int EB, int KS, int S>
 __global__ __launch_bounds__(512) void gated_rows_kernel(const char* __restrict__ w, const uint16_t* __restrict__ x,
                                                         GatedOut o, int M, int64_t F, int64_t K) {
@@ -273,7 +273,7 @@ __global__ __launch_bounds__(512) void gated_rows_kernel(const char* __restrict_
   for (int j = 0; j < stages; ++j) {
     const int ahead = stages - 1 - j;  // later stages, of which at most S - 1 are on their way
     if (ahead >= S - 1) wait_vm<(S - 1) * kDma>();
-    else if (S > 3 && ahead == 2) wait_vm<2 * kDma>();
+    else if (ahead == 2) wait_vm<2 * kDma>();
     else if (ahead == 1) wait_vm<kDma>();
     else wait_vm<0>();
     block_barrier();
@@ -672,16 +672,19 @@ hipError_t launch_gated_gemm(const void* w, int fp8, const uint16_t* x, const Ga
                     : go(gated_gemv_kernel<2, 4, 2>);
   }
   if (M <= 16 && in_stages) {
-    auto go = [&](auto bytes, auto parts) {
-      constexpr int S = 4, kLds = S * 16 * kRowsSpan + 8 * kWave * 16;
+    // Two blocks a CU with two stages each cover each other's barriers and ends (M = 5 and 13 with an addend, K = 4096, F =
+    // 14336: FP8 30 us, one block with four stages 37; bfloat16 44 and 49); K = 8192 in bfloat16 56 and 51.
+    auto go = [&](auto bytes, auto parts, auto stages) {
+      constexpr int S = decltype(stages)::value, kLds = S * 16 * kRowsSpan + 8 * kWave * 16;
       return launch_big_lds<gated_rows_kernel<decltype(bytes)::value, decltype(parts)::value, S>>(
-          kLds, std::min<int64_t>((F + 7) / 8, num_cus), 512, s, static_cast<const char*>(w), x, o, int(M), F, K);
+          kLds, std::min<int64_t>((F + 7) / 8, (S == 2 ? 2 : 1) * num_cus), 512, s, static_cast<const char*>(w), x, o, int(M),
+          F, K);
     };
     auto by_parts = [&](auto bytes) {
-      if (K * eb <= kRowsSpan) return go(bytes, Int<1>{});
-      if (K * eb <= 2 * kRowsSpan) return go(bytes, Int<2>{});
-      if (K * eb <= 4 * kRowsSpan) return go(bytes, Int<4>{});
-      return go(Int<2>{}, Int<8>{});
+      if (K * eb <= kRowsSpan) return go(bytes, Int<1>{}, Int<2>{});
+      if (K * eb <= 2 * kRowsSpan) return go(bytes, Int<2>{}, Int<2>{});
+      if (K * eb <= 4 * kRowsSpan) return go(bytes, Int<4>{}, Int<2>{});
+      return go(Int<2>{}, Int<8>{}, Int<4>{});
     };
     return fp8 ? by_parts(Int<1>{}) : by_parts(Int<2>{});
   }
@@ -710,7 +713,9 @@ hipError_t launch_gated_gemm(const void* w, int fp8, const uint16_t* x, const Ga
     return fp8 ? by_out(Int<1>{}) : by_out(Int<2>{});
   }
   if (K >= 16 / eb) {
-    const int64_t bm = M <= 64 ? 64 : 128, blocks = (M + bm - 1) / bm * ((F + 63) / 64);
+    // 64 rows a tile also where tiles of 128 leave CUs idle (515 x 1365, K = 1023: 17 us, 23 with 128).
+    const int64_t bm = M <= 64 || (M + 127) / 128 * ((F + 63) / 64) <= num_cus ? 64 : 128;
+    const int64_t blocks = (M + bm - 1) / bm * ((F + 63) / 64);
     if (blocks > kMaxGrid) return hipErrorInvalidValue;
     auto go = [&](auto kernel) { return launch(kernel, dim3(unsigned(blocks)), dim3(256), 0, s, xo, wo, o, M, F, K); };
     auto by_out = [&](auto bytes, auto rows) {
