@@ -413,12 +413,12 @@ __global__ __launch_bounds__(256) void product_staged_kernel(Operand a, Operand 
   __shared__ __attribute__((aligned(16))) char lds[kTiles > NW * kSlab ? kTiles : NW * kSlab];
   int64_t tm, tn;
   tile_of_block(blockIdx.x, (M + BM - 1) / BM, (N + BN - 1) / BN, tm, tn);
+  const int64_t all = (K + kStripK - 1) / kStripK, s0 = blockIdx.y * strips;
   AOp ao;
   BOp bo;
-  ao.init(a, PlainRows{tm * BM, M}, K);
-  bo.init(b, PlainRows{tn * BN, N}, K);
+  ao.init(a, PlainRows{tm * BM, M}, K, s0);
+  bo.init(b, PlainRows{tn * BN, N}, K, s0);
   v16f acc[2][2];
-  const int64_t all = (K + kStripK - 1) / kStripK, s0 = blockIdx.y * strips;
   staged_tile<AOp, BOp, BM, BN, WY, NW>(lds, ao, bo, s0, all - s0 < strips ? all - s0 : strips, acc);
   const int wid = threadIdx.x >> 6;
   wait_lds();
@@ -516,8 +516,8 @@ __global__ __launch_bounds__(256) void gated_staged_kernel(Operand x, Operand w,
   tile_of_block(blockIdx.x, (M + BM - 1) / BM, (F + BF - 1) / BF, tm, tn);
   AOp ao;
   BOp bo;
-  ao.init(x, PlainRows{tm * BM, M}, K);
-  bo.init(w, GatedRows{tn * BF, F}, K);
+  ao.init(x, PlainRows{tm * BM, M}, K, 0);
+  bo.init(w, GatedRows{tn * BF, F}, K, 0);
   v16f acc[BM / 64][2];
   staged_tile<AOp, BOp, BM, 2 * BF, WY, NW>(lds, ao, bo, 0, (K + kStripK - 1) / kStripK, acc);
   const int wid = threadIdx.x >> 6;

@@ -146,44 +146,49 @@ __device__ __forceinline__ int64_t slot_value(int64_t k, int64_t K) {
   return first > K - G ? K - G + (k - first) : k;
 }
 
+// The pieces' addresses move on from strip to strip; only the last strip, where the row or the operand ends, works them
+// out anew.
 template <int ROWS, int NW, int EB, class Map, int G>
 struct StagedRows {
   using Layout = RowsOperand<ROWS, NW, EB, Map>;
   static constexpr int kBytes = Layout::kBytes, kInst = Layout::kInst, kCpr = Layout::kCpr, kValues = 16 / EB;
-  const char* row[kInst];
+  const char* at[kInst];  // of the next strip's pieces
   int64_t K;
   u32x4 held[kInst];
-  __device__ __forceinline__ void init(const Operand& o, const Map& map, int64_t k) {
-    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+  static __device__ __forceinline__ int chunk(int q) { return (q * NW + (threadIdx.x >> 6)) * 64 + (threadIdx.x & 63); }
+  static __device__ __forceinline__ int place(int q) { return (chunk(q) % kCpr) ^ swz<kCpr>(chunk(q) / kCpr); }
+  __device__ __forceinline__ void init(const Operand& o, const Map& map, int64_t k, int64_t s0) {
     K = k;
 #pragma unroll
     for (int q = 0; q < kInst; ++q) {
-      const int r = ((q * NW + wid) * 64 + lane) / kCpr;
-      row[q] = o.p + (map.first + (map.in(r) ? map.at(r) : 0)) * o.ld;  // rows past the end: any, not stored
+      const int r = chunk(q) / kCpr;  // rows past the end: any, not stored
+      at[q] = o.p + (map.first + (map.in(r) ? map.at(r) : 0)) * o.ld + s0 * kStripK * EB + 16 * place(q);
     }
   }
   __device__ __forceinline__ void load(int64_t strip) {
-    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
     const bool ends = (strip + 1) * kStripK > K;
 #pragma unroll
     for (int q = 0; q < kInst; ++q) {
-      const int c = (q * NW + wid) * 64 + lane, g = (c % kCpr) ^ swz<kCpr>(c / kCpr);
-      const int64_t k = strip * kStripK + g * kValues;
-      held[q] = *reinterpret_cast<const u32x4_loose1*>(row[q] + (ends ? slot_value<G>(k, K) : k) * EB);
+      const char* p = at[q];
+      if (ends) {
+        const int64_t slot = strip * kStripK + place(q) * kValues;
+        p += (slot_value<G>(slot, K) - slot) * EB;
+      }
+      held[q] = *reinterpret_cast<const u32x4_loose1*>(p);
+      at[q] += kStripK * EB;
     }
   }
   __device__ __forceinline__ void store(char* tile, int64_t strip) {
-    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
 #pragma unroll
     for (int q = 0; q < kInst; ++q) {
-      const int c = (q * NW + wid) * 64 + lane, g = (c % kCpr) ^ swz<kCpr>(c / kCpr);
       if ((strip + 1) * kStripK > K) {
-        const int64_t k = strip * kStripK + g * kValues, first = k & ~int64_t(G - 1), v = slot_value<G>(k, K);
+        const int64_t slot = strip * kStripK + place(q) * kValues, first = slot & ~int64_t(G - 1);
+        const int64_t value = slot_value<G>(slot, K);
 #pragma unroll
         for (int e = 0; e < kValues; ++e)
-          if (v + e < first) held[q][e * EB / 4] &= ~((EB == 2 ? 0xFFFFu : 0xFFu) << (e * EB % 4 * 8));
+          if (value + e < first) held[q][e * EB / 4] &= ~((EB == 2 ? 0xFFFFu : 0xFFu) << (e * EB % 4 * 8));
       }
-      *reinterpret_cast<u32x4*>(tile + c * 16) = held[q];
+      *reinterpret_cast<u32x4*>(tile + chunk(q) * 16) = held[q];
     }
   }
 };
@@ -192,42 +197,53 @@ template <int COLS, int NW, int G>
 struct StagedTurned {
   using Layout = TurnedOperand<COLS, NW>;
   static constexpr int kBytes = Layout::kBytes, kInst = Layout::kInst, kCpr = Layout::kCpr;
-  const char* base;
-  int64_t ld, K, left;  // left: columns from the tile's first on
+  const char* at[kInst];
+  int64_t ld, K;
+  int over[kInst];  // columns of a piece past the row's end (7: all); the row's last eight are loaded then and moved in store()
   u32x4 held[kInst];
-  __device__ __forceinline__ void init(const Operand& o, const PlainRows& map, int64_t k) {
-    base = o.p + map.first * 2;
+  static __device__ __forceinline__ int chunk(int q) { return (q * NW + (threadIdx.x >> 6)) * 64 + (threadIdx.x & 63); }
+  __device__ __forceinline__ void init(const Operand& o, const PlainRows& map, int64_t k, int64_t s0) {
     ld = o.ld;
     K = k;
-    left = map.rows - map.first;
-  }
-  __device__ __forceinline__ void load(int64_t strip) {
-    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+    const int64_t left = map.rows - map.first;
 #pragma unroll
     for (int q = 0; q < kInst; ++q) {
-      const int c = (q * NW + wid) * 64 + lane, kk = c / kCpr, g = (c % kCpr) ^ turned_swz<kCpr>(kk);
-      const char* const p = base + slot_value<G>(strip * kStripK + kk, K) * ld;
-      // Eight columns that the row's end cuts are the row's last eight, moved to their places in store().
-      const int64_t col = 8 * g < left - 8 ? 8 * g : left - 8;
-      held[q] = *reinterpret_cast<const u32x4_loose1*>(p + 2 * col);
+      const int kk = chunk(q) / kCpr, col = 8 * ((chunk(q) % kCpr) ^ turned_swz<kCpr>(kk));
+      const int64_t from = col < left - 8 ? col : left - 8;
+      over[q] = col - from < 7 ? int(col - from) : 7;
+      at[q] = o.p + (s0 * kStripK + kk) * ld + 2 * (map.first + from);
+    }
+  }
+  __device__ __forceinline__ void load(int64_t strip) {
+    const bool ends = (strip + 1) * kStripK > K;
+#pragma unroll
+    for (int q = 0; q < kInst; ++q) {
+      const char* p = at[q];
+      if (ends) {
+        const int64_t slot = strip * kStripK + chunk(q) / kCpr;
+        p += (slot_value<G>(slot, K) - slot) * ld;
+      }
+      held[q] = *reinterpret_cast<const u32x4_loose1*>(p);
+      at[q] += kStripK * ld;
     }
   }
   __device__ __forceinline__ void store(char* tile, int64_t strip) {
-    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
 #pragma unroll
     for (int q = 0; q < kInst; ++q) {
-      const int c = (q * NW + wid) * 64 + lane, kk = c / kCpr, g = (c % kCpr) ^ turned_swz<kCpr>(kk);
-      if (left < COLS) {
-        const int over = 8 * g > left - 8 ? int(8 * g - (left - 8)) : 0, by = 16 * (over < 7 ? over : 7);
-        uint64_t lo = held[q].x | uint64_t(held[q].y) << 32;
-        const uint64_t hi = held[q].z | uint64_t(held[q].w) << 32;
-        lo = by >= 64 ? hi >> (by - 64) : by ? lo >> by | hi << (64 - by) : lo;
+      u32x4 v = held[q];
+      if (over[q]) {
+        const int by = 16 * over[q];
+        uint64_t lo = v.x | uint64_t(v.y) << 32;
+        const uint64_t hi = v.z | uint64_t(v.w) << 32;
+        lo = by >= 64 ? hi >> (by - 64) : lo >> by | hi << (64 - by);
         const uint64_t up = by >= 64 ? 0 : hi >> by;
-        held[q] = u32x4{uint32_t(lo), uint32_t(lo >> 32), uint32_t(up), uint32_t(up >> 32)};
+        v = u32x4{uint32_t(lo), uint32_t(lo >> 32), uint32_t(up), uint32_t(up >> 32)};
       }
-      const int64_t k = strip * kStripK + kk;
-      const bool repeated = slot_value<G>(k, K) < (k & ~int64_t(G - 1));
-      *reinterpret_cast<u32x4*>(tile + c * 16) = repeated ? u32x4{0, 0, 0, 0} : held[q];
+      if ((strip + 1) * kStripK > K) {
+        const int64_t slot = strip * kStripK + chunk(q) / kCpr;
+        if (slot_value<G>(slot, K) < (slot & ~int64_t(G - 1))) v = u32x4{0, 0, 0, 0};
+      }
+      *reinterpret_cast<u32x4*>(tile + chunk(q) * 16) = v;
     }
   }
 };
