@@ -160,15 +160,25 @@ __global__ __launch_bounds__(256) void gated_gemv_kernel(const char* __restrict_
     u32x4 wv[U][2], xv[U][M][X];
 #pragma unroll
     for (int n = 0; n < U; ++n) {
-      const int64_t c = c0 + n * kWave + lane;
-      const bool ok = c < whole;
+      const int64_t c = c0 + n * kWave + lane, at = c < whole ? c : whole - 1;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) wv[n][r] = ok ? ld16_loose_stream(rows[r] + 16 * c) : u32x4{0, 0, 0, 0};
+      for (int r = 0; r < 2; ++r) wv[n][r] = ld16_loose_stream(rows[r] + 16 * at);
 #pragma unroll
       for (int m = 0; m < M; ++m)
 #pragma unroll
-        for (int e = 0; e < X; ++e)
-          xv[n][m][e] = ok ? ld16_loose(x + m * K + c * kValues + 8 * e) : u32x4{0, 0, 0, 0};
+        for (int e = 0; e < X; ++e) xv[n][m][e] = ld16_loose(x + m * K + at * kValues + 8 * e);
+    }
+    if (c0 + kWave * U > whole) {  // loads are never conditional: what lies past the row's end is dropped here
+#pragma unroll
+      for (int n = 0; n < U; ++n) {
+        if (c0 + n * kWave + lane < whole) continue;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) wv[n][r] = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+          for (int e = 0; e < X; ++e) xv[n][m][e] = u32x4{0, 0, 0, 0};
+      }
     }
 #pragma unroll
     for (int n = 0; n < U; ++n)
