@@ -137,6 +137,15 @@ def test_gated_large(q, m, f, k, fp8):
     check_forward(q, np.random.default_rng([4, m, f, k]), m, f, k, fp8, "silu", torch.bfloat16)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("m,f,k", [(17, 8300, 96), (64, 8256, 336), (33, 8193, 1040), (20, 8200, 128), (96, 130, 1040), (128, 200, 528),
+                                   (65, 4099, 400), (64, 8192, 144)])
+def test_gated_to_128_rows(q, fp8, m, f, k):
+    """One tile of rows over wide and narrow layers, rows of k that end inside a strip."""
+    check_forward(q, np.random.default_rng([12, m, f, k]), m, f, k, fp8, "silu", torch.bfloat16)
+    check_forward(q, np.random.default_rng([13, m, f, k]), m, f, k, fp8, "relu", torch.float32, torch.bfloat16)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("grad_dtype,pre_dtype", [(torch.bfloat16, torch.float32), (torch.float32, torch.float32),
                                                   (torch.bfloat16, torch.bfloat16), (torch.float32, torch.bfloat16)])

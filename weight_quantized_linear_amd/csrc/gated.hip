@@ -489,13 +489,13 @@ __device__ __forceinline__ void gated_out(char* mine, v16f (&acc)[FM][FN], const
   }
 }
 
-template <int EB, int BM, int BF, int S, int WY, int NW, int OUT>
+template <int EB, int BM, int BF, int SK, int S, int NW, bool NT, int OUT>
 __global__ __launch_bounds__(64 * NW) void gated_kernel(Operand x, Operand w, GatedOut o, int64_t M, int64_t F, int64_t K,
                                                         int vec, int pre_vec) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  constexpr int BN = 2 * BF;
-  using AOp = RowsOperand<BM, NW, 2, PlainRows>;
-  using BOp = RowsOperand<BN, NW, EB, GatedRows>;
+  constexpr int BN = 2 * BF, WY = 2;
+  using AOp = RowsOperand<BM, NW, 2, PlainRows, SK>;
+  using BOp = RowsOperand<BN, NW, EB, GatedRows, SK, NT>;
   using L = ProductLayout<AOp, BOp, BM, BN, S, WY, NW>;
   constexpr int kSlab = OutSlab<0, 16 * L::FN>::kBytes;  // the wider of the types that leave by it
   static_assert(NW * kSlab <= L::kLds, "staging");
@@ -506,7 +506,7 @@ __global__ __launch_bounds__(64 * NW) void gated_kernel(Operand x, Operand w, Ga
   ao.init(x, PlainRows{tm * BM, M}, K);
   bo.init(w, GatedRows{tn * BF, F}, K);
   v16f acc[L::FM][L::FN];
-  product_tile<AOp, BOp, BM, BN, S, WY, NW>(lds, ao, bo, K, 0, (K + kStripK - 1) / kStripK, acc);
+  product_tile<AOp, BOp, BM, BN, S, WY, NW>(lds, ao, bo, K, 0, (K + SK - 1) / SK, acc);
   const int wid = threadIdx.x >> 6;
   block_barrier();  // every wave is done with the last strip
   gated_out<OUT>(lds + wid * kSlab, acc, o, tm * BM + wid / L::WX * (BM / WY), tn * BF + wid % L::WX * (BF / L::WX), M, F,
@@ -702,22 +702,33 @@ hipError_t launch_gated_gemm(const void* w, int fp8, const uint16_t* x, const Ga
   if (tiled_rows(x, K * 2) && tiled_rows(w, K * eb) && 2 * F * K * eb < kNowhere) {
     const int vec = aligned16(o.out) && F * (o.out_bf16 ? 2 : 4) % 16 == 0;
     const int pre_vec = aligned16(o.pre) && F * (o.pre_bf16 ? 2 : 4) % 16 == 0;
-    auto go = [&](auto bytes, auto bm, auto bf, auto stages, auto nw, auto out) {
+    auto go = [&](auto bytes, auto bm, auto bf, auto strip, auto stages, auto nw, auto nt, auto out) {
       constexpr int EB = decltype(bytes)::value, BM = decltype(bm)::value, BF = decltype(bf)::value;
-      constexpr int S = decltype(stages)::value, NW = decltype(nw)::value, OUT = decltype(out)::value;
-      using L = ProductLayout<RowsOperand<BM, NW, 2, PlainRows>, RowsOperand<2 * BF, NW, EB, GatedRows>, BM, 2 * BF, S, 2, NW>;
+      constexpr int SK = decltype(strip)::value, S = decltype(stages)::value, NW = decltype(nw)::value;
+      constexpr int OUT = decltype(out)::value;
+      constexpr bool NT = decltype(nt)::value;
+      using L = ProductLayout<RowsOperand<BM, NW, 2, PlainRows, SK>, RowsOperand<2 * BF, NW, EB, GatedRows, SK>, BM, 2 * BF, S,
+                              2, NW>;
       const int64_t blocks = ((M + BM - 1) / BM) * ((F + BF - 1) / BF);
       if (blocks > kMaxGrid) return hipErrorInvalidValue;
-      return launch_big_lds<gated_kernel<EB, BM, BF, S, 2, NW, OUT>>(L::kLds, blocks, 64 * NW, s, xo, wo, o, M, F, K, vec,
+      return launch_big_lds<gated_kernel<EB, BM, BF, SK, S, NW, NT, OUT>>(L::kLds, blocks, 64 * NW, s, xo, wo, o, M, F, K, vec,
                                                                      pre_vec);
     };
-    // Tiles of 256 x 128 columns with a CU to themselves, or of 128 x 64 of which two blocks share one, by the time of
+    // To 128 rows one tile has them all and the weights are read once, past the caches where a strip's rows are whole
+    // 128-byte lines (F = 14336, K = 4096, M = 64: bfloat16 48 us, 54 through them), as many bytes of them on their way as
+    // LDS holds.  32 columns where tiles of 64 leave half the CUs idle (F = 5504, K = 2048, M = 64: 16 us, 17 FP8 and 20
+    // bfloat16 with 64; F = 14336 40 us FP8, 32 with 64).  Strips of 128: FP8 M = 64 32 us, 34 in strips of 64; M = 128 46, 48.
+    const bool narrow = 2 * ((F + 63) / 64) <= num_cus;
+    // Beyond, tiles of 256 x 128 columns with a CU to themselves, or of 128 x 64 of which two blocks share one, by the time of
     // their rounds as for the products above: M = 256, F = 14336, K = 4096 91 and 70 us, M = 500 105 and 125.
     const bool wide = 1.75 * rounds(M, F, 256, 128, num_cus) <= 1.05 * rounds(M, F, 128, 64, 2 * num_cus);
     auto by_tile = [&](auto bytes, auto out) {
-      if (M <= 128) return go(bytes, Int<64>{}, Int<128>{}, Int<3>{}, Int<8>{}, out);
-      if (wide) return go(bytes, Int<256>{}, Int<128>{}, Int<2>{}, Int<8>{}, out);
-      return go(bytes, Int<128>{}, Int<64>{}, Int<2>{}, Int<4>{}, out);
+      constexpr bool kFp8 = decltype(bytes)::value == 1;
+      if (M <= 64 && narrow) return go(bytes, Int<64>{}, Int<32>{}, Int<64>{}, Int<4>{}, Int<2>{}, Int<!kFp8>{}, out);
+      if (M <= 64) return go(bytes, Int<64>{}, Int<64>{}, Int<128>{}, Int<3>{}, Int<4>{}, Int<1>{}, out);
+      if (M <= 128) return go(bytes, Int<128>{}, Int<64>{}, Int<kFp8 ? 128 : 64>{}, Int<kFp8 ? 3 : 4>{}, Int<4>{}, Int<1>{}, out);
+      if (wide) return go(bytes, Int<256>{}, Int<128>{}, Int<64>{}, Int<2>{}, Int<8>{}, Int<0>{}, out);
+      return go(bytes, Int<128>{}, Int<64>{}, Int<64>{}, Int<2>{}, Int<4>{}, Int<0>{}, out);
     };
     auto by_out = [&](auto bytes) { return o.out_bf16 ? by_tile(bytes, Int<1>{}) : by_tile(bytes, Int<0>{}); };
     return fp8 ? by_out(Int<1>{}) : by_out(Int<2>{});

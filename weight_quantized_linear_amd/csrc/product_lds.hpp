@@ -1,10 +1,10 @@
 // A tile of C[m, n] = sum_k A[m, k] B[n, k] on the matrix cores, with either operand stored
 // along k ("rows": [M, K], bfloat16 or FP8) or across it ("turned": [K, M], bfloat16).
 //
-// * A block of NW waves owns BM x BN, a wave (BM / WY) x (BN / WX) of 32 x 32 MFMA blocks. K goes in strips of 64
-//   through a ring of S LDS stages, filled by loads that write LDS directly; a strip is four
+// * A block of NW waves owns BM x BN, a wave (BM / WY) x (BN / WX) of 32 x 32 MFMA blocks. K goes in strips of 64 (or 128)
+//   through a ring of S LDS stages, filled by loads that write LDS directly; a strip is
 //   steps of 16, and while the matrix cores work on one, the operands of the next are read.
-// * Rows operands lie in LDS as 128-byte rows (FP8: 64) with their 16-byte pieces permuted; a lane
+// * Rows operands lie in LDS as 128-byte rows (FP8: 64; twice that in strips of 128) with their 16-byte pieces permuted; a lane
 //   reads the 8 values of its row with one load (FP8: 16 values for two steps, widened exactly).
 // * Turned operands lie as 64 rows of k.  The transposing LDS read hands lane l of 16 the values k .. k + 3
 //   of column l from four rows: two reads give the 8 values that the MFMA wants.  Their 64-byte pieces
@@ -57,11 +57,11 @@ struct GatedRows {
   __device__ __forceinline__ bool in(int r) const { return first + r / 64 * 32 + r % 32 < rows; }
 };
 
-// ROWS rows of 64 values of k, EB bytes each (2: bfloat16, 1: FP8).
-template <int ROWS, int NW, int EB, class Map>
+// ROWS rows of SK values of k, EB bytes each (2: bfloat16, 1: FP8).  NT: past the caches.
+template <int ROWS, int NW, int EB, class Map, int SK = kStripK, bool NT = false>
 struct RowsOperand {
   using Layout = RowsOperand;
-  static constexpr int kRowBytes = kStripK * EB, kCpr = kRowBytes / 16, kBytes = ROWS * kRowBytes;
+  static constexpr int kStrip = SK, kRowBytes = SK * EB, kCpr = kRowBytes / 16, kBytes = ROWS * kRowBytes;
   static constexpr int kInst = ROWS * kCpr / (64 * NW);
   static_assert(ROWS * kCpr % (64 * NW) == 0, "whole instructions");
   const char* base;
@@ -76,7 +76,7 @@ struct RowsOperand {
     for (int q = 0; q < kInst; ++q) {
       const int c = (q * NW + wid) * 64 + lane, r = c / kCpr, g = (c % kCpr) ^ swz<kCpr>(r);
       off[q] = map.in(r) ? uint32_t(map.at(r) * o.ld + 16 * g) : kNowhere;
-      const int left = int(K % kStripK) * EB;  // bytes of a row in the last strip, 0: all
+      const int left = int(K % SK) * EB;  // bytes of a row in the last strip, 0: all
       tail[q] = left && 16 * g >= left ? kNowhere : off[q];
     }
   }
@@ -85,7 +85,11 @@ struct RowsOperand {
     const int64_t at = strip * kRowBytes;
     const __amdgpu_buffer_rsrc_t r = strip_rsrc(base + at, bytes - at, none);
 #pragma unroll
-    for (int q = 0; q < kInst; ++q) bdma16(r, tile + (q * NW + wid) * 1024, last ? tail[q] : off[q], 0);
+    for (int q = 0; q < kInst; ++q) {
+      char* const to = tile + (q * NW + wid) * 1024;
+      if constexpr (NT) bdma16_nt(r, to, last ? tail[q] : off[q]);
+      else bdma16(r, to, last ? tail[q] : off[q], 0);
+    }
   }
 };
 
@@ -102,7 +106,7 @@ __device__ __forceinline__ int turned_swz(int k) {
 template <int COLS, int NW>
 struct TurnedOperand {
   using Layout = TurnedOperand;
-  static constexpr int kRowBytes = COLS * 2, kCpr = kRowBytes / 16, kBytes = kStripK * kRowBytes;
+  static constexpr int kStrip = kStripK, kRowBytes = COLS * 2, kCpr = kRowBytes / 16, kBytes = kStripK * kRowBytes;
   static constexpr int kInst = kStripK * kCpr / (64 * NW);
   static_assert(kStripK * kCpr % (64 * NW) == 0, "whole instructions");
   const char* base;
@@ -251,37 +255,38 @@ struct StagedTurned {
 // The wave's fragments of NF blocks of 32 rows from `row0` on.
 template <class Op, int NF> struct Fragments;
 
-template <int ROWS, int NW, class Map, int NF>
-struct Fragments<RowsOperand<ROWS, NW, 2, Map>, NF> {
+template <int ROWS, int NW, class Map, int SK, bool NT, int NF>
+struct Fragments<RowsOperand<ROWS, NW, 2, Map, SK, NT>, NF> {
   static constexpr int kReads = NF;  // LDS reads of a step
-  uint32_t at[4];
+  uint32_t at[SK / 16];
   __device__ __forceinline__ void init(int row0) {
     const int r = threadIdx.x & 31, h = (threadIdx.x >> 5) & 1;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) at[u] = uint32_t((row0 + r) * 128 + 16 * ((4 * (u / 2) + 2 * h + u % 2) ^ swz<8>(r)));
+    for (int u = 0; u < SK / 16; ++u)
+      at[u] = uint32_t((row0 + r) * SK * 2 + 16 * ((4 * (u / 2) + 2 * h + u % 2) ^ swz<SK / 8>(r)));
   }
   template <int U>
   __device__ __forceinline__ void read(const char* tile, v8bf (&f)[NF]) {
 #pragma unroll
-    for (int j = 0; j < NF; ++j) f[j] = __builtin_bit_cast(v8bf, lds16(tile + at[U] + j * 32 * 128));
+    for (int j = 0; j < NF; ++j) f[j] = __builtin_bit_cast(v8bf, lds16(tile + at[U] + j * 32 * SK * 2));
   }
 };
 
-template <int ROWS, int NW, class Map, int NF>
-struct Fragments<RowsOperand<ROWS, NW, 1, Map>, NF> {
+template <int ROWS, int NW, class Map, int SK, bool NT, int NF>
+struct Fragments<RowsOperand<ROWS, NW, 1, Map, SK, NT>, NF> {
   static constexpr int kReads = NF;
-  uint32_t at[2];
+  uint32_t at[SK / 32];
   u32x4 raw[NF];
   __device__ __forceinline__ void init(int row0) {
     const int r = threadIdx.x & 31, h = (threadIdx.x >> 5) & 1;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) at[t] = uint32_t((row0 + r) * 64 + 16 * ((2 * t + h) ^ swz<4>(r)));
+    for (int t = 0; t < SK / 32; ++t) at[t] = uint32_t((row0 + r) * SK + 16 * ((2 * t + h) ^ swz<SK / 16>(r)));
   }
   template <int U>
   __device__ __forceinline__ void read(const char* tile, v8bf (&f)[NF]) {
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
-      if constexpr (U % 2 == 0) raw[j] = lds16(tile + at[U / 2] + j * 32 * 64);
+      if constexpr (U % 2 == 0) raw[j] = lds16(tile + at[U / 2] + j * 32 * SK);
       f[j] = U % 2 == 0 ? e4m3x8_to_bf16x8(raw[j].x, raw[j].y) : e4m3x8_to_bf16x8(raw[j].z, raw[j].w);
     }
   }
@@ -318,7 +323,8 @@ struct ProductLayout {
   static constexpr int WX = NW / WY, FM = BM / WY / 32, FN = BN / WX / 32;
   static constexpr int kStage = AOp::kBytes + BOp::kBytes, kLds = S * kStage;
   static constexpr int kLoads = AOp::kInst + BOp::kInst;
-  static_assert(kLds <= 160 * 1024 && (S - 1) * kLoads < 64 && S >= 2, "ring");
+  static constexpr int kStrip = AOp::kStrip;
+  static_assert(kLds <= 160 * 1024 && (S - 1) * kLoads < 64 && S >= 2 && BOp::kStrip == kStrip, "ring");
 };
 
 // The sums of the tile whose operands `a` and `b` were set to, over the strips s0 .. s0 + nk - 1 of K (nk >= 1): acc[i][j][v] belongs to row
@@ -336,7 +342,7 @@ __device__ __forceinline__ void product_tile(
   fb.init(wid % L::WX * (BN / L::WX));
   auto fetch = [&](int64_t s) {
     char* st = lds + int(s % S) * L::kStage;
-    const bool last = (s0 + s + 1) * kStripK >= K, none = s >= nk;
+    const bool last = (s0 + s + 1) * L::kStrip >= K, none = s >= nk;
     a.fetch(st, none ? 0 : s0 + s, last, none);
     b.fetch(st + AOp::kBytes, none ? 0 : s0 + s, last, none);
   };
@@ -360,18 +366,13 @@ __device__ __forceinline__ void product_tile(
   fb.template read<0>(lds + AOp::kBytes, bX);
   auto inner = [&](const char* st) {
     const char* sb = st + AOp::kBytes;
-    fa.template read<1>(st, aY);
-    fb.template read<1>(sb, bY);
-    mma(aX, bX);
-    interleave<NM, 0, kReads, 0>();
-    fa.template read<2>(st, aX);
-    fb.template read<2>(sb, bX);
-    mma(aY, bY);
-    interleave<NM, 0, kReads, 0>();
-    fa.template read<3>(st, aY);
-    fb.template read<3>(sb, bY);
-    mma(aX, bX);
-    interleave<NM, 0, kReads, 0>();
+    static_for<L::kStrip / 16 - 1>([&](auto uc) {
+      constexpr int U = decltype(uc)::value;
+      fa.template read<U + 1>(st, U % 2 ? aX : aY);
+      fb.template read<U + 1>(sb, U % 2 ? bX : bY);
+      mma(U % 2 ? aY : aX, U % 2 ? bY : bX);
+      interleave<NM, 0, kReads, 0>();
+    });
   };
   for (int64_t kt = 0; kt < nk - 1; ++kt) {
     inner(lds + int(kt % S) * L::kStage);
