@@ -595,16 +595,21 @@ __global__ __launch_bounds__(kThreads) void lora_turn_kernel(Turn a, Turn b) {
 
 template <int V> using Int = std::integral_constant<int, V>;
 
-// Rows of a tile: 64 where a group has more than 16 on average.
+// Tiles of more than 16 rows where a group has more on average.
 bool tall(int64_t T, int64_t G) { return T > 16 * G; }
 
 int64_t tile_count(int64_t T, int64_t G, int bm) { return std::min(T, T / bm + G); }
 
-// Parts of the long axis: as many as make 128 blocks, of 512 values at least.  More blocks take the first product
-// less time and the second more, which adds the parts (4096 rows, R = 64, N = 14336: 97 us, 103 with 512 blocks).
+// Rows of the first product's tiles: 32 to R = 32 (4096 rows, R = 16: 16.4 us, 17.4 with 64), 64 beyond (R = 64: 25, 31 with
+// 32, which read the adapters twice as often).
+int shrink_rows(int64_t T, int64_t G, int64_t R) { return !tall(T, G) ? 16 : R <= 32 ? 32 : 64; }
+
+// Parts of the long axis: as many as make 128 blocks, of few rows 256, of 512 values at least.  More blocks take the first
+// product of few rows less time and that of many more (64 rows, K = 4096: 6.0 us, 7.4 with 128; 4096 rows, R = 64: 29 us, 25
+// with 128), and the second product adds the parts.
 int shrink_splits(int64_t T, int64_t G, int64_t K, int64_t R) {
-  const int64_t tiles = tile_count(T, G, tall(T, G) ? 64 : 16) * ((R + 63) / 64);
-  return int(std::max<int64_t>(1, std::min({int64_t(16), (128 + tiles - 1) / tiles, K / 512})));
+  const int64_t tiles = tile_count(T, G, shrink_rows(T, G, R)) * ((R + 63) / 64), blocks = tall(T, G) ? 128 : 256;
+  return int(std::max<int64_t>(1, std::min({int64_t(16), (blocks + tiles - 1) / tiles, K / 512})));
 }
 
 hipError_t launch_shrink(const uint16_t* x, const uint16_t* a, const Groups& g, float* plane, int splits, int64_t K,
@@ -618,11 +623,17 @@ hipError_t launch_shrink(const uint16_t* x, const uint16_t* a, const Groups& g, 
   auto by_rank = [&](auto bm, auto small) {
     constexpr int BM = decltype(bm)::value;
     constexpr bool SMALL = decltype(small)::value;
-    if (R <= 16) return go(lora_shrink_kernel<BM, 1, SMALL>, BM, 1);
-    if (R <= 32) return go(lora_shrink_kernel<BM, 2, SMALL>, BM, 2);
-    return go(lora_shrink_kernel<BM, 4, SMALL>, BM, 4);
+    if constexpr (BM != 64) {
+      if (R <= 16) return go(lora_shrink_kernel<BM, 1, SMALL>, BM, 1);
+      if (R <= 32) return go(lora_shrink_kernel<BM, 2, SMALL>, BM, 2);
+    }
+    if constexpr (BM != 32) return go(lora_shrink_kernel<BM, 4, SMALL>, BM, 4);
+    return hipErrorInvalidValue;  // tiles of 32 rows have no other rank
   };
-  auto by_rows = [&](auto small) { return tall(g.T, g.G) ? by_rank(Int<64>{}, small) : by_rank(Int<16>{}, small); };
+  auto by_rows = [&](auto small) {
+    const int bm = shrink_rows(g.T, g.G, R);
+    return bm == 64 ? by_rank(Int<64>{}, small) : bm == 32 ? by_rank(Int<32>{}, small) : by_rank(Int<16>{}, small);
+  };
   return K < 8 ? by_rows(std::true_type{}) : by_rows(std::false_type{});
 }
 
