@@ -146,6 +146,14 @@ def test_gated_to_128_rows(q, fp8, m, f, k):
     check_forward(q, np.random.default_rng([13, m, f, k]), m, f, k, fp8, "relu", torch.float32, torch.bfloat16)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("addend", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("m,f,k", [(3, 37, 64), (7, 37001, 64), (16, 5504, 2064), (5, 1029, 4112), (13, 515, 8192)])
+def test_addend_of_few_rows(q, fp8, addend, m, f, k):
+    """Wide layers, of which a block has more tiles than it holds addends of, and every length of a row."""
+    check_forward(q, np.random.default_rng([14, m, f, k]), m, f, k, fp8, "silu", torch.bfloat16, addend)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("grad_dtype,pre_dtype", [(torch.bfloat16, torch.float32), (torch.float32, torch.float32),
                                                   (torch.bfloat16, torch.bfloat16), (torch.float32, torch.bfloat16)])

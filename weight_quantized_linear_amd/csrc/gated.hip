@@ -227,9 +227,13 @@ __global__ __launch_bounds__(256) void gated_gemv_kernel(const char* __restrict_
 // stages a row), and the waves' sums meet in LDS at a tile's end.  MFMA 16x16x32: the weights' rows are the
 // result's rows and the tokens its columns: lanes 0 .. 31 end with four gate columns of a token, lanes 32 .. 63
 // with the up ones.  FP8: a lane's 16 bytes are the operands of two steps, and x is held in that order.
-// M = 13, K = 4096, F = 14336: 28 us FP8 (4.2 TB/s), 43 bfloat16 (5.5); K = 2048, F = 5504, bfloat16 13 (3.4: of its three
-// tiles a CU the first loads' and the last sums' latency shows).  Weights kept in the caches: 1 to 2 us more.
-template <int EB, int KS, int S>
+// ADD: the addends of eight tiles at a time wait in LDS; loaded at a tile's end they would come behind all weights on
+// their way (F = 5504, K = 2048, bfloat16 15 us, 12 from LDS).  The form without has no registers for that in FP8.
+// M = 13, K = 4096, F = 14336: 25 us FP8 (4.7 TB/s), 45 bfloat16 (5.3), with addends 32 and 47; K = 2048, F = 5504, bfloat16 11
+// (4.0: of its 1.3 tiles a block the first loads' and the last sums' latency shows).  Weights kept in the caches: 1 to
+// 2 us more.
+constexpr int kAddTiles = 8, kAddBytes = kAddTiles * 16 * 16 * 4;  // tiles whose addends LDS holds
+template <int EB, int KS, int S, bool ADD>
 __global__ __launch_bounds__(512) void gated_rows_kernel(const char* __restrict__ w, const uint16_t* __restrict__ x,
                                                         GatedOut o, int M, int64_t F, int64_t K) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -238,6 +242,7 @@ __global__ __launch_bounds__(512) void gated_rows_kernel(const char* __restrict_
   constexpr int kSteps = kRow / NW / 64;      // loads of 16 bytes a lane per stage
   constexpr int kValues = 16 / EB, E = kValues / 8;  // values of a load, MFMA steps of it
   v4f(*const sums)[kWave] = reinterpret_cast<v4f(*)[kWave]>(lds + S * kStage);
+  float* const adds = reinterpret_cast<float*>(lds + S * kStage + NW * kWave * 16);  // [tile][token][gate, up][8]
   const int lane = threadIdx.x % kWave, wid = threadIdx.x / kWave, i = lane % 16, q = lane / 16;
   const int64_t tiles = (F + 7) / 8, row_bytes = K * EB;
   const int stages = int((tiles - 1 - blockIdx.x) / gridDim.x + 1) * KS;
@@ -287,7 +292,15 @@ __global__ __launch_bounds__(512) void gated_rows_kernel(const char* __restrict_
     else if (ahead == 1) wait_vm<kDma>();
     else wait_vm<0>();
     block_barrier();
-    const int h = j % KS;
+    const int n = j / KS, h = j % KS;
+    if (ADD && h == 0 && n % kAddTiles == 0) {
+#pragma unroll
+      for (int e = 0; e < kAddTiles * 256 / 512; ++e) {
+        const int at = e * 512 + int(threadIdx.x), i2 = at / 16 % 16;
+        const int64_t f = (blockIdx.x + (n + at / 256) * int64_t(gridDim.x)) * 8 + at % 8;
+        if (i2 < M && f < F) adds[at] = get_float(o.addend, (2 * i2 + at / 8 % 2) * F + f, o.addend_bf16);
+      }
+    }
     const char* const row = lds + j % S * kStage + i * kRow;
     u32x4 wv[kSteps];
 #pragma unroll
@@ -314,16 +327,20 @@ __global__ __launch_bounds__(512) void gated_rows_kernel(const char* __restrict_
     block_barrier();  // the slot is read, and at a tile's end the sums are there
     if (j + S < stages) issue(j + S);
     if (last) {
-      const int n = j / KS;
       if (wid == n % NW) {
         v4f sum = sums[0][lane];
 #pragma unroll
         for (int v = 1; v < NW; ++v) sum += sums[v][lane];
+        v4f add[2] = {v4f{}, v4f{}};
+        if (ADD)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            add[e] = *reinterpret_cast<const v4f*>(adds + ((n % kAddTiles * 16 + i) * 2 + e) * 8 + 4 * (q & 1));
         const int64_t f = (blockIdx.x + int64_t(n) * gridDim.x) * 8 + 4 * (q & 1);
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const float up = __shfl_down(sum[v], 32, kWave);
-          if (q < 2 && i < M && f + v < F) gated_put(o, i, f + v, F, sum[v], up);
+          if (q < 2 && i < M && f + v < F) gated_put(o, i, f + v, F, sum[v], up, GatedAdd{add[0][v], add[1][v]});
         }
       }
       acc[0] = acc[1] = v4f{};
@@ -661,8 +678,8 @@ hipError_t launch_product(const uint16_t* a, const uint16_t* b, void* out, int o
 hipError_t launch_gated_gemm(const void* w, int fp8, const uint16_t* x, const GatedOut& o, int64_t M, int64_t F, int64_t K,
                              int num_cus, hipStream_t s) {
   const int eb = fp8 ? 1 : 2;
-  // Few rows.  F = 14336, K = 4096, us (vector ALU, stages in LDS, tiles of 64 rows): FP8 M = 1 19, 27, -; M = 2
-  // 23.6, 27, -; M = 4 38, 27, -; M = 13 -, 28, 41; bfloat16 M = 2 37, 42, -; M = 4 48, 42, -; M = 13 -, 43, 46.
+  // Few rows.  F = 14336, K = 4096, us (vector ALU, stages in LDS, tiles of 64 rows): FP8 M = 1 19, 22, -; M = 2
+  // 22, 22, -; M = 4 38, 22, -; M = 13 -, 25, 31; bfloat16 M = 2 37, 41, -; M = 4 48, 41, -; M = 13 -, 43, 48.
   const bool in_stages = K * eb <= (fp8 ? 4 : 8) * kRowsSpan && aligned16(x) && aligned16(w) && K * eb % 16 == 0 &&
                          K % 8 == 0 && 2 * F * K * eb < kNowhere;
   if (M <= 2 || (M <= 4 && !in_stages)) {
@@ -685,10 +702,12 @@ hipError_t launch_gated_gemm(const void* w, int fp8, const uint16_t* x, const Ga
     // Two blocks a CU with two stages each cover each other's barriers and ends (M = 5 and 13 with an addend, K = 4096, F =
     // 14336: FP8 30 us, one block with four stages 37; bfloat16 44 and 49); K = 8192 in bfloat16 56 and 51.
     auto go = [&](auto bytes, auto parts, auto stages) {
-      constexpr int S = decltype(stages)::value, kLds = S * 16 * kRowsSpan + 8 * kWave * 16;
-      return launch_big_lds<gated_rows_kernel<decltype(bytes)::value, decltype(parts)::value, S>>(
-          kLds, std::min<int64_t>((F + 7) / 8, (S == 2 ? 2 : 1) * num_cus), 512, s, static_cast<const char*>(w), x, o, int(M),
-          F, K);
+      constexpr int EB = decltype(bytes)::value, KS = decltype(parts)::value, S = decltype(stages)::value;
+      constexpr int kLds = S * 16 * kRowsSpan + 8 * kWave * 16;
+      const int64_t blocks = std::min<int64_t>((F + 7) / 8, (S == 2 ? 2 : 1) * num_cus);
+      const char* const wp = static_cast<const char*>(w);
+      return o.addend ? launch_big_lds<gated_rows_kernel<EB, KS, S, true>>(kLds + kAddBytes, blocks, 512, s, wp, x, o, int(M), F, K)
+                      : launch_big_lds<gated_rows_kernel<EB, KS, S, false>>(kLds, blocks, 512, s, wp, x, o, int(M), F, K);
     };
     auto by_parts = [&](auto bytes) {
       if (K * eb <= kRowsSpan) return go(bytes, Int<1>{}, Int<2>{});
