@@ -27,13 +27,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPiece = 8;  // values of a thread that lie together
 
-// The value as the type holds it.
-template <int BF16>
-__device__ __forceinline__ float stored(float v) {
-  if constexpr (BF16) return float(static_cast<__bf16>(v));
-  else return v;
-}
-
 // N sums over the TPR threads of a row; every thread gets the results.  `part`: LDS of its own for two calls in
 // a row, so that a call's one barrier also lies between the reads of one and the writes of the next but one.
 template <int TPR, int N>
@@ -66,7 +59,8 @@ struct NormArgs {
 
 // R, IO, P: element types of the residual, of block output and y, of the parameters.  TAIL: H % 8 != 0.
 // NT: results past the caches.  Bound by HBM: 16384 x 4096, float32
-// residual, 157 us, 5.1 TB/s; 16384 x 2048 in bfloat16 45 us, 6.0; a 2 GiB copy reaches 5.0.
+// residual, 146 us, 5.5 TB/s; 16384 x 2048 in bfloat16 46 us, 5.8; a 1 GiB copy reaches 5.0.  8 x 4096: 4.7 us, the
+// launch and one way to memory and back.
 template <int R, int IO, int P, int TPR, int V, bool TAIL, bool NT>
 __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void norm_kernel(NormArgs a) {
   constexpr int THREADS = TPR > kThreads ? TPR : kThreads, ROWS = THREADS / TPR, C = V / kPiece;
@@ -166,8 +160,10 @@ struct NormGradArgs {
 // [0] of the gate that its range begins in the middle of, [1] of the one that begins in its range.
 // With V = 8 the parameters stay in registers and the next row is on its way while one is worked on; wider
 // rows have no registers for that.  Both means come from sums over the row as it was read, so that a row meets
-// one barrier.  Bound by HBM: 8192 x 2048 in bfloat16 45 us, 4.4 TB/s; 16384 x 4096 203 us, 4.0; results past the
-// caches changed neither.  256 or 1024 blocks take 1.5 and 1.1 times as long at 8192 x 2048.
+// one barrier.  Bound by HBM: 8192 x 2048 in bfloat16 with the residual's gradient coming in 45 us, 4.4 TB/s, without
+// 37, 4.5;
+// 16384 x 4096 159 us, 4.2; results past the caches changed neither.  256 or 1024 blocks take 1.5 and 1.1 times as long
+// at 8192 x 2048.
 template <int R, int IO, int P, int TPR, int V, bool TAIL>
 __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void norm_grad_kernel(NormGradArgs a) {
   constexpr int THREADS = TPR > kThreads ? TPR : kThreads, WORKERS = THREADS / TPR, C = V / kPiece;

@@ -48,26 +48,22 @@ typedef u32x4 u32x4_loose __attribute__((aligned(2)));
 template <int BF16>
 struct Eight {
   u32x4 v[BF16 ? 1 : 2];
+  static __device__ __forceinline__ u32x4 fetch(const void* p) { return *reinterpret_cast<const u32x4_loose*>(p); }
   // NT: past the caches.
-  template <bool NT>
-  static __device__ __forceinline__ u32x4 fetch(const void* p) {
-    if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const u32x4_loose*>(p));
-    else return *reinterpret_cast<const u32x4_loose*>(p);
-  }
   template <bool NT>
   static __device__ __forceinline__ void leave(void* p, u32x4 x) {
     if constexpr (NT) __builtin_nontemporal_store(x, reinterpret_cast<u32x4_loose*>(p));
     else *reinterpret_cast<u32x4_loose*>(p) = x;
   }
-  template <bool TAIL, bool NT = false>
+  template <bool TAIL>
   __device__ __forceinline__ void load(const void* p, int64_t i, int64_t left) {
     using V = typename Elem<BF16>::T;
     const V* q = reinterpret_cast<const V*>(p) + i;
     v[0] = u32x4{0, 0, 0, 0};
     if constexpr (!BF16) v[1] = u32x4{0, 0, 0, 0};
     if (left >= 8) {
-      v[0] = fetch<NT>(q);
-      if constexpr (!BF16) v[1] = fetch<NT>(q + 4);
+      v[0] = fetch(q);
+      if constexpr (!BF16) v[1] = fetch(q + 4);
     } else if (TAIL) {
 #pragma unroll
       for (int e = 0; e < 7; ++e)
@@ -80,8 +76,8 @@ struct Eight {
   // The same without a condition.
   __device__ __forceinline__ void get_at(const void* p, int64_t i) {
     const auto* q = reinterpret_cast<const typename Elem<BF16>::T*>(p) + i;
-    v[0] = fetch<false>(q);
-    if constexpr (!BF16) v[1] = fetch<false>(q + 4);
+    v[0] = fetch(q);
+    if constexpr (!BF16) v[1] = fetch(q + 4);
   }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     if constexpr (BF16) {

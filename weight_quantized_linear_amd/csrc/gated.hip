@@ -229,7 +229,8 @@ __global__ __launch_bounds__(256) void gated_gemv_kernel(const char* __restrict_
 // with the up ones.  FP8: a lane's 16 bytes are the operands of two steps, and x is held in that order.
 // ADD: the addends of eight tiles at a time wait in LDS; loaded at a tile's end they would come behind all weights on
 // their way (F = 5504, K = 2048, bfloat16 15 us, 12 from LDS).  The form without has no registers for that in FP8.
-// M = 13, K = 4096, F = 14336: 25 us FP8 (4.7 TB/s), 45 bfloat16 (5.3), with addends 32 and 47; K = 2048, F = 5504, bfloat16 11
+// M = 13, K = 4096, F = 14336: 25 us FP8 (4.7 TB/s), 45 bfloat16 (5.3), with addends 32 and 47; K = 2048, F = 5504,
+// bfloat16 11
 // (4.0: of its 1.3 tiles a block the first loads' and the last sums' latency shows).  Weights kept in the caches: 1 to
 // 2 us more.
 constexpr int kAddTiles = 8, kAddBytes = kAddTiles * 16 * 16 * 4;  // tiles whose addends LDS holds
@@ -404,7 +405,11 @@ __device__ __forceinline__ void product_out(char* mine, const v16f (&acc)[FM][FN
   }
 }
 
-// TA, TB: operand stored across k.  blockIdx.y: a part of K, whose sums go to the float32 plane of its own behind out.
+// TA, TB: operand stored across k.  Bound by the matrix cores: 8192 x 4096 x 8192 in tiles of 256 x 256 484 us, 1.14
+// PFLOP/s, of whose
+// time the SIMDs' matrix cores work 64 % (dx) and 60 % (dw), bank conflicts take 1 %; 4096 x 2048, K = 11264 (dx) 219
+// us in tiles of 128 x 128, 11264 x 2048, K = 4096 (dw) 178 in tiles of 192 x 128.  blockIdx.y: a part of K, whose sums
+// go to the float32 plane of its own behind out.
 template <bool TA, bool TB, int BM, int BN, int S, int WY, int NW, int OUT>
 __global__ __launch_bounds__(64 * NW) void product_kernel(Operand a, Operand b, void* __restrict__ out, int64_t M,
                                                           int64_t N, int64_t K, int64_t strips, int vec) {
@@ -429,7 +434,10 @@ __global__ __launch_bounds__(64 * NW) void product_kernel(Operand a, Operand b, 
                    tn * BN + wid % L::WX * (BN / L::WX), M, N, vec);
 }
 
-// The same at any address, 128 x 128; K and the widths of turned operands are 8 at least.
+// The same at any address, 128 x 128: 515 x 1023, K = 2730 (dx, split in five) 20 us and 6 for the sum of its parts,
+// 2730 x 1023, K = 515
+// (dw) 20; few blocks whose strips come through registers, so the strips' latency shows.  K and the widths of turned
+// operands are 8 at least.
 template <bool TA, bool TB, int OUT>
 __global__ __launch_bounds__(256) void product_staged_kernel(Operand a, Operand b, void* __restrict__ out, int64_t M,
                                                             int64_t N, int64_t K, int64_t strips) {
@@ -450,7 +458,8 @@ __global__ __launch_bounds__(256) void product_staged_kernel(Operand a, Operand 
   const int wid = threadIdx.x >> 6;
   wait_lds();
   block_barrier();
-  product_out<OUT>(lds + wid * kSlab, acc, reinterpret_cast<char*>(out) + blockIdx.y * M * N * (OUT ? 2 : 4), tm * BM + wid / 2 * 64, tn * BN + wid % 2 * 64, M, N, false);
+  product_out<OUT>(lds + wid * kSlab, acc, reinterpret_cast<char*>(out) + blockIdx.y * M * N * (OUT ? 2 : 4),
+                   tm * BM + wid / 2 * 64, tn * BN + wid % 2 * 64, M, N, false);
 }
 
 // A wave's part of a gated product: its columns are FN / 2 times 32 gate and the 32 up columns beside them.
@@ -506,6 +515,10 @@ __device__ __forceinline__ void gated_out(char* mine, v16f (&acc)[FM][FN], const
   }
 }
 
+// Bound by the matrix cores from 256 rows on, below by the weights' bytes.  bfloat16, M = 4096, F = 5632, K = 2048 with
+// float32
+// pre-activations 208 us, 0.91 PFLOP/s, the matrix cores at work 69 % of the cycles at K = 8192; FP8, F = 14336, K = 4096:
+// M = 500 110 us, 1.06 PFLOP/s, M = 64 32 us, 3.7 TB/s.  SK: values of k in a strip; NT: weights past the caches.
 template <int EB, int BM, int BF, int SK, int S, int NW, bool NT, int OUT>
 __global__ __launch_bounds__(64 * NW) void gated_kernel(Operand x, Operand w, GatedOut o, int64_t M, int64_t F, int64_t K,
                                                         int vec, int pre_vec) {
@@ -530,7 +543,7 @@ __global__ __launch_bounds__(64 * NW) void gated_kernel(Operand x, Operand w, Ga
                  vec, pre_vec);
 }
 
-// The same at any address and size (K >= 8, 16 with FP8).
+// The same at any address and size (K >= 8, 16 with FP8): 515 x 1365, K = 1023 with pre-activations 22 us.
 template <int EB, int BM, int OUT>
 __global__ __launch_bounds__(256) void gated_staged_kernel(Operand x, Operand w, GatedOut o, int64_t M, int64_t F,
                                                           int64_t K) {
@@ -556,7 +569,7 @@ __global__ __launch_bounds__(256) void gated_staged_kernel(Operand x, Operand w,
 // ---------------------------------------------------------------- gradient of the activation
 
 // Eight columns of a row a thread, at any address; TAIL: F % 8 != 0.  Bound by HBM: 4096 x 5632 from float32 pre-activations
-// 54 us, 6.0 TB/s.
+// 53 us, 6.1 TB/s.
 template <int ACT, int DY, int PRE, bool TAIL>
 __global__ __launch_bounds__(kThreads) void gated_grad_kernel(const void* __restrict__ dy, const void* __restrict__ pre,
                                                              uint16_t* __restrict__ dpre, int64_t M, int64_t F) {
@@ -736,9 +749,11 @@ hipError_t launch_gated_gemm(const void* w, int fp8, const uint16_t* x, const Ga
     // To 128 rows one tile has them all and the weights are read once, past the caches where a strip's rows are whole
     // 128-byte lines (F = 14336, K = 4096, M = 64: bfloat16 48 us, 54 through them), as many bytes of them on their way as
     // LDS holds.  32 columns where tiles of 64 leave half the CUs idle (F = 5504, K = 2048, M = 64: 16 us, 17 FP8 and 20
-    // bfloat16 with 64; F = 14336 40 us FP8, 32 with 64).  Strips of 128: FP8 M = 64 32 us, 34 in strips of 64; M = 128 46, 48.
+    // bfloat16 with 64; F = 14336 40 us FP8, 32 with 64).  Strips of 128: FP8 M = 64 32 us, 34 in strips of 64; M =
+    // 128 46, 48.
     const bool narrow = 2 * ((F + 63) / 64) <= num_cus;
-    // Beyond, tiles of 256 x 128 columns with a CU to themselves, or of 128 x 64 of which two blocks share one, by the time of
+    // Beyond, tiles of 256 x 128 columns with a CU to themselves, or of 128 x 64 of which two blocks share one, by
+    // the time of
     // their rounds as for the products above: M = 256, F = 14336, K = 4096 91 and 70 us, M = 500 105 and 125.
     const bool wide = 1.75 * rounds(M, F, 256, 128, num_cus) <= 1.05 * rounds(M, F, 128, 64, 2 * num_cus);
     auto by_tile = [&](auto bytes, auto out) {
@@ -753,7 +768,7 @@ hipError_t launch_gated_gemm(const void* w, int fp8, const uint16_t* x, const Ga
     return fp8 ? by_out(Int<1>{}) : by_out(Int<2>{});
   }
   if (K >= 16 / eb) {
-    // 64 rows a tile also where tiles of 128 leave CUs idle (515 x 1365, K = 1023: 17 us, 23 with 128).
+    // 64 rows a tile also where tiles of 128 leave CUs idle (515 x 1365, K = 1023, a call among others: 17 us, 23 with 128).
     const int64_t bm = M <= 64 || (M + 127) / 128 * ((F + 63) / 64) <= num_cus ? 64 : 128;
     const int64_t blocks = (M + bm - 1) / bm * ((F + 63) / 64);
     if (blocks > kMaxGrid) return hipErrorInvalidValue;

@@ -144,7 +144,11 @@ __device__ __forceinline__ int find_tile(const Groups& g, int* cum, int tile, in
 
 // plane[split][t][r] = sum over the split's part of K of x[t, k] a[l, r, k].  Block: a tile of
 // BM rows, a part of K, 16 FR of the R; its waves take 64 values of k in turn, the next ones on their way, and
-// add up at the end through LDS.  Both operands come straight from memory: neither is used by two waves.
+// add up at the end through LDS.  Both operands come straight from memory: neither is used by two waves.  Bound by
+// the way to memory, at 64-byte pieces of 16 rows a load: 4096 rows, K = 4096 16 us at R = 16, 25 at R = 64; 4099 rows,
+// K = 8192 28 us,
+// 2.4 TB/s.  64 rows of 64 groups, K = 4096: 6.0 us.  Twice the loads on their way, 8 waves a block, blocks that begin at
+// different k change nothing; x past the caches costs a tenth more.
 template <int BM, int FR, bool SMALL>
 __global__ __launch_bounds__(kThreads) void lora_shrink_kernel(const uint16_t* __restrict__ x,
                                                               const uint16_t* __restrict__ a, Groups g,
@@ -248,7 +252,10 @@ __global__ __launch_bounds__(kThreads) void lora_shrink_kernel(const uint16_t* _
 // are eight consecutive columns: one 16-byte store of bfloat16.  LDS: the pieces of z as eights of r, the last one
 // the row's last eight values with zeros for those that it repeats, as b's eights are loaded.
 // WHOLE: an MFMA step is four eights of one piece, and b's are loaded once for all pieces; else the pieces' eights
-// follow each other.  SMALL: R < 8.  TAIL: N % 8 != 0.
+// follow each other.  SMALL: R < 8.  TAIL: N % 8 != 0.  Bound by base and out: 4096 rows, N = 14336, bfloat16, R = 64 68
+// us, 3.5 TB/s,
+// R = 16 50, 4.7; 4099 rows, N = 8192, R = 16 38, 3.5; 64 rows, N = 4096 6.6.  From R = 64 on the matrix cores' and LDS's
+// part shows beside the bytes.
 constexpr int kSpan = 1024;
 
 // Even lanes' second against odd lanes' first pieces.  Lanes 2 j and 2 j + 1 that hold pieces (first, second) of their
@@ -416,7 +423,9 @@ __global__ __launch_bounds__(kThreads) void lora_expand_kernel(const float* __re
 // dA[l, r, c] = s sum_t z[t, r] p[t, c] with z = dz, p = x, or dB[l, c, r] with z, p = dout, over the rows of adapter
 // l's groups.  Block: one adapter, 16 FR of the R, 512 columns (128 a wave), every splits-th step of 32 rows, the next
 // one on its way.  A lane loads 8 rows x 8 columns and turns them by byte permutations into its pieces of eight MFMA
-// operands, whose row i is column 8 i + j of the wave's 128.  P: pieces of z.
+// operands, whose row i is column 8 i + j of the wave's 128.  P: pieces of z.  Bound by x and dout: 4099 rows, K = 2048,
+// N = 8192 30 us at R = 16,
+// 2.8 TB/s; at R = 64 64, since each 32 of R read them again.
 struct SumArgs {
   const uint16_t* p;
   const float* z;

@@ -4,7 +4,8 @@
 // * A block of NW waves owns BM x BN, a wave (BM / WY) x (BN / WX) of 32 x 32 MFMA blocks. K goes in strips of 64 (or 128)
 //   through a ring of S LDS stages, filled by loads that write LDS directly; a strip is
 //   steps of 16, and while the matrix cores work on one, the operands of the next are read.
-// * Rows operands lie in LDS as 128-byte rows (FP8: 64; twice that in strips of 128) with their 16-byte pieces permuted; a lane
+// * Rows operands lie in LDS as 128-byte rows (FP8: 64; twice that in strips of 128) with their 16-byte pieces permuted;
+// a lane
 //   reads the 8 values of its row with one load (FP8: 16 values for two steps, widened exactly).
 // * Turned operands lie as 64 rows of k.  The transposing LDS read hands lane l of 16 the values k .. k + 3
 //   of column l from four rows: two reads give the 8 values that the MFMA wants.  Their 64-byte pieces
@@ -327,7 +328,8 @@ struct ProductLayout {
   static_assert(kLds <= 160 * 1024 && (S - 1) * kLoads < 64 && S >= 2 && BOp::kStrip == kStrip, "ring");
 };
 
-// The sums of the tile whose operands `a` and `b` were set to, over the strips s0 .. s0 + nk - 1 of K (nk >= 1): acc[i][j][v] belongs to row
+// The sums of the tile whose operands `a` and `b` were set to, over the strips s0 .. s0 + nk - 1 of K (nk >= 1):
+// acc[i][j][v] belongs to row
 // 32 i + 8 (v / 4) + 4 h + v % 4 and column 32 j + lane % 32 of the wave's part.
 template <class AOp, class BOp, int BM, int BN, int S, int WY, int NW>
 __device__ __forceinline__ void product_tile(
