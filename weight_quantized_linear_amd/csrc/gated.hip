@@ -408,7 +408,7 @@ __device__ __forceinline__ void product_out(char* mine, const v16f (&acc)[FM][FN
 // TA, TB: operand stored across k.  Bound by the matrix cores: 8192 x 4096 x 8192 in tiles of 256 x 256 484 us, 1.14
 // PFLOP/s, of whose
 // time the SIMDs' matrix cores work 64 % (dx) and 60 % (dw), bank conflicts take 1 %; 4096 x 2048, K = 11264 (dx) 219
-// us in tiles of 128 x 128, 11264 x 2048, K = 4096 (dw) 178 in tiles of 192 x 128.  blockIdx.y: a part of K, whose sums
+// us in tiles of 128 x 128, 11264 x 2048, K = 4096 (dw) 180 in tiles of 192 x 128.  blockIdx.y: a part of K, whose sums
 // go to the float32 plane of its own behind out.
 template <bool TA, bool TB, int BM, int BN, int S, int WY, int NW, int OUT>
 __global__ __launch_bounds__(64 * NW) void product_kernel(Operand a, Operand b, void* __restrict__ out, int64_t M,
