@@ -55,7 +55,8 @@ typedef enum qlinear_status {
   QLINEAR_ERR_INVALID_ARG = 1,  /* null pointer, size <= 0, bad dtype, bad layout */
   QLINEAR_ERR_UNSUPPORTED = 2,  /* device is not gfx950, or a forced kernel family cannot run the call */
   QLINEAR_ERR_DEVICE = 3,       /* no usable HIP device / device query failed */
-  QLINEAR_ERR_LAUNCH = 4,       /* a kernel launch reported an error */
+  QLINEAR_ERR_LAUNCH = 4,       /* a kernel launch reported an error, or its grid would have 2^32 threads or more
+                                   along an axis (products of more than some 10^9 rows) */
   QLINEAR_ERR_SCRATCH_LIMIT = 5 /* qlinear_fp8_gemm_noalloc: the shape needs more split-K
                                    scratch than the library's fixed buffer holds */
 } qlinear_status;

@@ -33,9 +33,15 @@ template <typename T> struct same_type { using type = T; };
 // Launch through hipLaunchKernel so the launch status comes back directly
 // (no reliance on the thread's sticky last-error state).  Arguments are
 // converted to the kernel's own parameter types first.
+// The dispatch counts an axis' threads in 32 bits and takes what passes them modulo 2^32, without an error: the
+// blocks behind would never run.  Such a grid is refused here.
+constexpr uint64_t kMaxAxisThreads = (uint64_t(1) << 32) - 1;
 template <typename... Params>
 hipError_t launch(void (*kernel)(Params...), dim3 grid, dim3 block, size_t shmem, hipStream_t s,
                   typename same_type<Params>::type... args) {
+  if (uint64_t(grid.x) * block.x > kMaxAxisThreads || uint64_t(grid.y) * block.y > kMaxAxisThreads ||
+      uint64_t(grid.z) * block.z > kMaxAxisThreads)
+    return hipErrorInvalidConfiguration;
   void* argv[] = {static_cast<void*>(&args)...};
   return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, argv, shmem, s);
 }
