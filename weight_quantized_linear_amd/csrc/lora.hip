@@ -571,8 +571,7 @@ __global__ __launch_bounds__(kThreads) void lora_join_kernel(const float* __rest
 }
 
 __global__ __launch_bounds__(kThreads) void clear_kernel(uint16_t* __restrict__ p, int64_t count) {
-  const int64_t at = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-  if (at < count) p[at] = 0;
+  for (int64_t at = int64_t(blockIdx.x) * kThreads + threadIdx.x; at < count; at += int64_t(gridDim.x) * kThreads) p[at] = 0;
 }
 
 // turned[l, c, r] = in[l, r, c] of A [L, R, K] and of B [L, N, R], in pieces of 32 x 32 through LDS; block columns of A's
@@ -735,8 +734,8 @@ struct GradSpace {
 hipError_t launch_clear(void* p, int64_t bytes, hipStream_t s) {
   const int64_t count = bytes / 2;
   if (count == 0) return hipSuccess;
-  return launch(clear_kernel, dim3(unsigned((count + kThreads - 1) / kThreads)), dim3(kThreads), 0, s,
-                static_cast<uint16_t*>(p), count);
+  const int64_t blocks = std::min<int64_t>((count + kThreads - 1) / kThreads, 65536);
+  return launch(clear_kernel, dim3(unsigned(blocks)), dim3(kThreads), 0, s, static_cast<uint16_t*>(p), count);
 }
 
 size_t lora_ws_bytes(int64_t T, int64_t G, int64_t K, int64_t R) {
