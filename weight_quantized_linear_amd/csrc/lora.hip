@@ -420,6 +420,27 @@ __global__ __launch_bounds__(kThreads) void lora_expand_kernel(const float* __re
 
 // ---------------------------------------------------------------- sums over rows
 
+// The highest end of the groups before this lane's: `top`, that of all earlier waves of groups, and those of the lanes
+// below.  b, e: the lane's group, clipped, 0 for lanes without one; `last`: the last lane with one.  `top` moves
+// on.  Where no end in the wave falls a group begins at the end before it, so only what came before the wave counts.
+__device__ __forceinline__ uint32_t ends_before(uint32_t b, uint32_t e, int last, uint32_t& top) {
+  const int lane = threadIdx.x % kWave;
+  uint32_t before = top, ends = e;
+  if (__ballot(e < b) != 0) {
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+      const uint32_t o = __shfl_up(ends, d, kWave);
+      if (lane >= d) ends = ends > o ? ends : o;
+    }
+    const uint32_t o = __shfl_up(ends, 1, kWave);
+    if (lane > 0) before = before > o ? before : o;
+    last = kWave - 1;
+  }
+  const uint32_t highest = __builtin_amdgcn_readlane(ends, last);
+  top = top > highest ? top : highest;
+  return before;
+}
+
 // dA[l, r, c] = s sum_t z[t, r] p[t, c] with z = dz, p = x, or dB[l, c, r] with z, p = dout, over the rows of adapter
 // l's groups.  Block: one adapter, 16 FR of the R, 512 columns (128 a wave), every splits-th step of 32 rows, the next
 // one on its way.  A lane loads 8 rows x 8 columns and turns them by byte permutations into its pieces of eight MFMA
@@ -491,11 +512,20 @@ __device__ __forceinline__ void lora_sum(const SumArgs& w, const Groups& g, cons
     }
   };
 
+  // The groups that the other kernels give tiles: a group that begins before an earlier one's end has no dz, and its
+  // rows may be another's.
   int turn = split;  // steps to skip until this block's next one
+  uint32_t top = 0;
   for (int64_t z0 = 0; z0 < g.G; z0 += kWave) {
-    const int64_t z = z0 + lane < g.G ? z0 + lane : g.G - 1;
-    const int64_t b = g.offsets[z], e0 = g.offsets[z + 1], e = e0 < g.T ? e0 : g.T;
-    const bool mine = g.ids[z] == l && b < e && z0 + lane < g.G;
+    const int last = int(g.G - 1 - z0 < kWave - 1 ? g.G - 1 - z0 : kWave - 1);
+    const int64_t z = z0 + (lane < last ? lane : last);
+    const uint32_t limit = uint32_t(g.T);
+    uint32_t b = g.offsets[z], e = g.offsets[z + 1];
+    b = b < limit ? b : limit;
+    e = e < limit ? e : limit;
+    if (lane > last) b = e = 0;
+    const uint32_t before = ends_before(b, e, last, top);  // by the whole wave
+    const bool mine = g.ids[z] == l && b < e && b >= before;
     for (uint64_t left = __ballot(mine); left; left &= left - 1) {
       const int src = __builtin_ctzll(left);
       const int64_t begin = __builtin_amdgcn_readlane(int(b), src), end = __builtin_amdgcn_readlane(int(e), src);
