@@ -153,13 +153,13 @@ template <int BM, int FR, bool SMALL>
 __global__ __launch_bounds__(kThreads) void lora_shrink_kernel(const uint16_t* __restrict__ x,
                                                               const uint16_t* __restrict__ a, Groups g,
                                                               float* __restrict__ plane, int64_t K, int64_t R,
-                                                              int64_t per) {
+                                                              int64_t per, int tile0) {
   extern __shared__ int cum[];
   __shared__ v4f sums[kWaves][FR][kWave];
   constexpr int FM = BM / 16, KS = 2;  // KS MFMA steps of 32 at a time
   int64_t row0 = 0;
   int id = -1;
-  const int rows = find_tile<BM>(g, cum, int(blockIdx.x), &row0, &id);
+  const int rows = find_tile<BM>(g, cum, tile0 + int(blockIdx.x), &row0, &id);
   if (rows <= 0) return;
   const int lane = threadIdx.x % kWave, wid = threadIdx.x / kWave, i = lane % 16, q = lane / 16;
   const int64_t r0 = int64_t(blockIdx.z) * 16 * FR;
@@ -276,7 +276,7 @@ __global__ __launch_bounds__(kThreads) void lora_expand_kernel(const float* __re
                                                               const float* __restrict__ scale,
                                                               const void* base, void* out,
                                                               float* __restrict__ z_out, int64_t N, int64_t R,
-                                                              int64_t span) {
+                                                              int64_t span, int tile0) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   constexpr int FM = BM / 16, P = pieces_of(OUT);
   constexpr bool kPaired = OUT == 1;  // whole 128-byte lines a load and a store; float32 pieces are 32 bytes a lane
@@ -285,7 +285,7 @@ __global__ __launch_bounds__(kThreads) void lora_expand_kernel(const float* __re
   int* const cum = reinterpret_cast<int*>(lds + BM * row_bytes);
   int64_t row0 = 0;
   int id = -1;
-  const int rows = find_tile<BM>(g, cum, int(blockIdx.x), &row0, &id);
+  const int rows = find_tile<BM>(g, cum, tile0 + int(blockIdx.x), &row0, &id);
   if (rows <= 0) return;
   const int lane = threadIdx.x % kWave, wid = threadIdx.x / kWave, i = lane % 16, q = lane / 16;
   const float s = id >= 0 && scale ? scale[id] : 1.f;
@@ -638,6 +638,16 @@ bool tall(int64_t T, int64_t G) { return T > 16 * G; }
 
 int64_t tile_count(int64_t T, int64_t G, int bm) { return std::min(T, T / bm + G); }
 
+// go(first tile, tiles) for launches of at most 2^23 tiles: a launch has fewer than 2^32 threads along an axis, and the
+// 2^30 rows that a call may have are 2^25 tiles and more.
+template <typename F>
+hipError_t by_launches(int64_t tiles, F&& go) {
+  constexpr int64_t kMost = int64_t(1) << 23;
+  for (int64_t t = 0; t < tiles; t += kMost)
+    if (hipError_t e = go(int(t), unsigned(std::min(tiles - t, kMost)))) return e;
+  return hipSuccess;
+}
+
 // Rows of the first product's tiles: 32 to R = 32 (4096 rows, R = 16: 16.4 us, 17.4 with 64), 64 beyond (R = 64: 25, 31 with
 // 32, which read the adapters twice as often).
 int shrink_rows(int64_t T, int64_t G, int64_t R) { return !tall(T, G) ? 16 : R <= 32 ? 32 : 64; }
@@ -655,8 +665,10 @@ hipError_t launch_shrink(const uint16_t* x, const uint16_t* a, const Groups& g, 
   const int64_t per = (((K + splits - 1) / splits + 255) / 256) * 256;
   const size_t lds = size_t(g.G + 1) * 4;
   auto go = [&](auto kernel, int bm, int fr) {
-    const dim3 grid(unsigned(tile_count(g.T, g.G, bm)), unsigned(splits), unsigned((R + 16 * fr - 1) / (16 * fr)));
-    return launch(kernel, grid, dim3(kThreads), lds, s, x, a, g, plane, K, R, per);
+    return by_launches(tile_count(g.T, g.G, bm), [&](int tile0, unsigned tiles) {
+      const dim3 grid(tiles, unsigned(splits), unsigned((R + 16 * fr - 1) / (16 * fr)));
+      return launch(kernel, grid, dim3(kThreads), lds, s, x, a, g, plane, K, R, per, tile0);
+    });
   };
   auto by_rank = [&](auto bm, auto small) {
     constexpr int BM = decltype(bm)::value;
@@ -684,9 +696,11 @@ hipError_t launch_expand(const float* plane, int splits, const uint16_t* b, cons
   const int bm = !tall(g.T, g.G) ? 16 : R <= 32 ? 32 : lds_of(64) <= 64 * 1024 ? 64 : 16;
   const int64_t tiles = tile_count(g.T, g.G, bm);
   const int64_t span = tiles * ((N + kSpan - 1) / kSpan) >= 1024 ? kSpan : 256;
-  const dim3 grid(unsigned(tiles), unsigned((N + span - 1) / span));
   auto go = [&](auto kernel) {
-    return launch(kernel, grid, dim3(kThreads), lds_of(bm), s, plane, splits, b, g, scale, base, out, z_out, N, R, span);
+    return by_launches(tiles, [&](int tile0, unsigned count) {
+      return launch(kernel, dim3(count, unsigned((N + span - 1) / span)), dim3(kThreads), lds_of(bm), s, plane, splits, b, g,
+                    scale, base, out, z_out, N, R, span, tile0);
+    });
   };
   auto by_rank = [&](auto rows, auto o, auto tail) {
     constexpr int BM = decltype(rows)::value, OUT = decltype(o)::value;
