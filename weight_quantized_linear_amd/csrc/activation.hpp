@@ -56,14 +56,15 @@ __device__ __forceinline__ float gelu_one(float g, float u) {
   return (g * near * half) * (u * half);
 }
 
-// d(g sigmoid(z))/dg = sigmoid(z) (1 + g sigmoid(-z) z').
+// d(g sigmoid(z))/dg = sigmoid(z) (1 + g sigmoid(-z) z').  Beyond |g| = 32 either sigmoid is 0, and g z' would
+// pass float32's range from 1.5e36 on: g is clamped there too, a NaN stays.
 __device__ __forceinline__ void gelu_grad(float g, float u, float dy, float& dg, float& du) {
   const float c = fminf(fmaxf(g, -32.f), 32.f);
   float near, half, rest;
   sigmoids(kGeluRate * c * fmaf(kGeluCube * c, c, 1.f), near, half, rest);
   const float slope = kGeluRate * fmaf(3.f * kGeluCube * c, c, 1.f);
   const float dh = dy * half;
-  dg = dh * (u * half) * (near * fmaf(g, rest * slope, 1.f));
+  dg = dh * (u * half) * (near * fmaf(fabsf(g) > 32.f ? c : g, rest * slope, 1.f));
   du = dh * (g * near * half);
 }
 
