@@ -627,7 +627,8 @@ int qlinear_gated_gemm(const void* w, int weight_format, const void* x, const vo
  *     grad_pre[:, F .. 2F-1] = grad_out * activation(g)
  * grad_out: [M, F] of grad_dtype; pre: [M, 2F] of pre_dtype, as the forward
  * call left it; grad_pre: bfloat16 [M, 2F], the operand of the two calls below
- * and the gradient of the addend.  ReLU's slope at 0 is 0.
+ * and the gradient of the addend.  ReLU's slope at 0 is 0.  Where the forward call had an alpha or
+ * alpha_up other than 1, the products below lack that factor.
  */
 int qlinear_gated_backward(const void* grad_out, int grad_dtype, const void* pre, int pre_dtype,
                            void* grad_pre, int64_t M, int64_t F, int activation, void* stream);

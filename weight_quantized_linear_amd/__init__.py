@@ -954,11 +954,16 @@ def gated_gemm(w: torch.Tensor, x: torch.Tensor, out: torch.Tensor | None = None
 
 def gated_gemm_backward(grad_out: torch.Tensor, pre: torch.Tensor, w: torch.Tensor, x: torch.Tensor,
                         activation: str = "silu", need_x: bool = True, need_w: bool = True,
-                        grad_x_dtype: torch.dtype = torch.bfloat16, grad_w_dtype: torch.dtype = torch.bfloat16):
-    """Gradients of ``gated_gemm`` with bfloat16 weights and alpha 1 from its ``pre`` ->
+                        grad_x_dtype: torch.dtype = torch.bfloat16, grad_w_dtype: torch.dtype = torch.bfloat16,
+                        alpha: float = 1.0, alpha_up: float | None = None):
+    """Gradients of ``gated_gemm`` with bfloat16 weights from its ``pre`` ->
     (grad_pre bfloat16 [M, 2F], which is the addend's gradient, grad_x [M, K], grad_w [2F, K];
     None for what is not needed) (``qlinear_gated_backward``, ``qlinear_bf16_gemm_grad_x``,
-    ``qlinear_bf16_gemm_grad_w``)."""
+    ``qlinear_bf16_gemm_grad_w``).  alpha, alpha_up: as the forward call had them.  grad_pre does not depend
+    on them; the products behind grad_x and grad_w have no such factor, so others than 1 are refused
+    where either is needed."""
+    if (need_x or need_w) and (float(alpha) != 1.0 or float(alpha if alpha_up is None else alpha_up) != 1.0):
+        raise ValueError("grad_x and grad_w are those of alpha = alpha_up = 1")
     w, x = _bf16_matrix(w, "w"), _bf16_matrix(x, "x")
     if w.shape[0] % 2 != 0 or x.shape[1] != w.shape[1]:
         raise ValueError(f"shapes: w {tuple(w.shape)} must be [2F, K], x {tuple(x.shape)} must be [M, K]")
