@@ -715,8 +715,8 @@ int qlinear_lora_gemm_backward(const void* grad_out, const void* x, const float*
  * T: one a row; gates divides T), or NULL with gates = 0 (all 1).  residual and residual_out:
  * [T, H] of residual_dtype; block and out: [T, H] of dtype; weight and
  * block_weight: [H] of param_dtype.  All F32 or BF16, a BF16 residual with a BF16
- * block only.  residual_out may be residual.  1 <= H <= 16384, eps > 0; float32 inside, so squares
- * have to stay in its range (values below 2^63).  T = 0 is allowed and does nothing.
+ * block only.  residual_out may be residual.  1 <= H <= 16384, eps > 0; float32 inside, so the sum
+ * of a row's squares has to stay in its range: values below 2^56 (2^63 / sqrt(H)).  T = 0 is allowed and does nothing.
  */
 int qlinear_block_norm(const void* residual, int residual_dtype, const void* weight,
                        int param_dtype, const void* block, int dtype, const void* block_weight,
@@ -731,8 +731,9 @@ int qlinear_block_norm(const void* residual, int residual_dtype, const void* wei
  * residual_out: grad_residual = residual_scale * D (residual_dtype, may be
  * grad_residual_out; without a block D itself), grad_block (dtype), and the sums over rows grad_weight,
  * grad_block_weight [H] and grad_gate [gates, H] (param_dtype), each NULL
- * where its input is.  float32 sums in a fixed order.  workspace: at least the bytes of
- * qlinear_block_norm_backward_workspace_size (post: block_weight is given; gated:
+ * where its input is.  float32 sums in a fixed order, of products of any two
+ * of residual_out, block, its gated part, grad_residual_out and grad_out * weight over a row: all of them below
+ * 2^56.  workspace: at least the bytes of qlinear_block_norm_backward_workspace_size (post: block_weight is given; gated:
  * gate is), 16-byte aligned.  T = 0: grad_weight, grad_block_weight and grad_gate are cleared.
  */
 int qlinear_block_norm_backward_workspace_size(int64_t T, int64_t H, int post, int gated,

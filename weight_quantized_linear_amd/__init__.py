@@ -1154,7 +1154,8 @@ def block_norm(residual: torch.Tensor, weight: torch.Tensor, block: torch.Tensor
     with x normed by w = x * w / sqrt(mean(x^2) + eps) over a row.  block_weight None: the block
     as it is; gate [G, H] (or [H]): row t takes row t * G / T, None: 1; block None: the plain norm
     of residual, which is residual_out then.  out has the block's dtype (without a block out_dtype,
-    None: residual's); residual_out, in residual's dtype, may be residual."""
+    None: residual's); residual_out, in residual's dtype, may be residual.  Values of block and
+    residual_out below 2^56: the sum of a row's squares is a float32."""
     t, h, gates = _norm_operands(residual, weight, block, block_weight, gate)
     if block is None:
         if residual_out is not None:
