@@ -667,7 +667,7 @@ int qlinear_bf16_gemm_grad_w(const void* grad_out, const void* x, void* grad_w, 
  * values in a, b or x give results that are not finite.
  * Groups as in qlinear_fp8_grouped_gemm: an id outside 0 .. L-1 has no adapter
  * (out = base, z = 0), rows in no group are left as they were, offsets are clipped
- * to T and must not decrease.  1 <= num_groups <= 4096, 1 <= L <= 4096,
+ * to T and must not decrease (a group that begins before an earlier one's end has no rows).  1 <= num_groups <= 4096, 1 <= L <= 4096,
  * 1 <= R <= 256, N and K <= 2^20, T <= 2^30.  workspace: at least the bytes of
  * qlinear_lora_workspace_size, 16-byte aligned; a smaller one is
  * QLINEAR_ERR_INVALID_ARG.  T = 0 is allowed and does nothing.

@@ -1075,7 +1075,8 @@ def lora_gemm(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, a_offsets: torc
     b [L, N, R] of many requests beside a projection whose result is ``base`` [T, N] (None: 0;
     ``out`` may be ``base``).  An id outside 0 .. L - 1 has no adapter (out = base); rows in no
     group keep whatever ``out`` held (a new ``out`` starts uninitialised).  scale: float32 [L]
-    (None: 1).  return_z: (out, z), z = x a^T float32 [T, R] for ``lora_gemm_backward``."""
+    (None: 1).  return_z: (out, z), z = x a^T float32 [T, R] for ``lora_gemm_backward``, in whose
+    rows of no group nothing is written either."""
     x, a, b, t, k, n, r, g, l = _adapters(x, a, b, a_offsets, adapter_ids, scale)
     code = _float_code(out_dtype, "out_dtype")
     if base is not None:

@@ -59,7 +59,8 @@ struct NormArgs {
 
 // R, IO, P: element types of the residual, of block output and y, of the parameters.  TAIL: H % 8 != 0.
 // NT: results past the caches.  Bound by HBM: 16384 x 4096, float32
-// residual, 146 us, 5.5 TB/s; 16384 x 2048 in bfloat16 46 us, 5.8; a 1 GiB copy reaches 5.0.  8 x 4096: 4.7 us, the
+// residual, 146 us, 5.5 TB/s; 16384 x 2048 in bfloat16 46 to 48 us, 5.7 (here and below: the kernel alone, no operand in a
+// cache, if nothing else is said); a 1 GiB copy reaches 5.0.  8 x 4096: 4.7 us, the
 // launch and one way to memory and back.
 template <int R, int IO, int P, int TPR, int V, bool TAIL, bool NT>
 __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void norm_kernel(NormArgs a) {
@@ -162,7 +163,9 @@ struct NormGradArgs {
 // rows have no registers for that.  Both means come from sums over the row as it was read, so that a row meets
 // one barrier.  Bound by HBM: 8192 x 2048 in bfloat16 with the residual's gradient coming in 45 us, 4.4 TB/s, without
 // 37, 4.5;
-// 16384 x 4096 159 us, 4.2; results past the caches changed neither.  256 or 1024 blocks take 1.5 and 1.1 times as long
+// 16384 x 4096 159 us, 4.2; results past the caches changed neither.  4096 rows of H = 5120 79 us, 2.7 TB/s (a thread's
+// second eight values lie past the row's end for three threads of four), of 8192 95, 3.5, of 16384 861, 0.8: 32 values a
+// thread take 540 to 730 bytes of scratch a lane, 16 none or, with float32 parameters where H % 8 != 0, 8 to 16.  256 or 1024 blocks take 1.5 and 1.1 times as long
 // at 8192 x 2048.
 template <int R, int IO, int P, int TPR, int V, bool TAIL>
 __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void norm_grad_kernel(NormGradArgs a) {
@@ -412,11 +415,13 @@ hipError_t by_types(int r, int io, int p, bool tail, F&& go) {
   return tail ? with(std::true_type{}) : with(std::false_type{});
 }
 
-// Calls that move more leave their results past the caches: 16384 x 2048 in bfloat16 (268 MB) 43 us, 55 through
-// them; 4096 x 4096 (134 MB) 23.5 us either way, and the next operator finds the rows.
+// Calls that move more leave their results past the caches, as calls among others, which find part of their operands
+// there: 16384 x 2048 in bfloat16 (268 MB) 43 us, 55 through them; 4096 x 4096 (134 MB) 23.5 us either way, and the next
+// operator finds the rows.
 constexpr int64_t kNtBytes = int64_t(160) << 20;
 
-// Workers of the backward pass: two blocks per CU of a 256 CU card, a row each at least.  Where a gate's
+// Workers of the backward pass: two blocks per CU of a 256 CU card, a row each at least.  Not the current device's CUs:
+// the workspace's size is a function of the sizes alone, asked for before there is a device.  Where a gate's
 // rows are fewer than a worker's, these are a multiple of them.
 constexpr int64_t kGradBlocks = 512;
 void grad_split(int64_t T, int64_t per, int rows_per_block, int64_t* rows, int64_t* workers) {

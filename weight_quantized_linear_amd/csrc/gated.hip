@@ -141,8 +141,8 @@ __device__ __forceinline__ u32x4 ld16_loose_stream(const void* p) {
 
 // M <= 4 rows at any size and address, on the vector ALU: a wave has one column, whose gate and up rows it reads in
 // contiguous KiB, 2 U loads in flight a lane; products of pairs by the bfloat16 dot instruction (exact,
-// float32 sums).  Bound by HBM: one row of x, F = 14336, K = 4096, FP8: 19 us, 6.2 TB/s;
-// bfloat16 35.5, 6.6 TB/s.
+// float32 sums).  Bound by HBM: one row of x, F = 14336, K = 4096, FP8: 18.6 us, 6.3 TB/s;
+// bfloat16 35, 6.7 TB/s (here and below: the kernel alone, no operand in a cache, if nothing else is said).
 template <int EB, int M, int U>
 __global__ __launch_bounds__(256) void gated_gemv_kernel(const char* __restrict__ w, const uint16_t* __restrict__ x,
                                                         GatedOut o, int64_t F, int64_t K) {
@@ -229,7 +229,7 @@ __global__ __launch_bounds__(256) void gated_gemv_kernel(const char* __restrict_
 // with the up ones.  FP8: a lane's 16 bytes are the operands of two steps, and x is held in that order.
 // ADD: the addends of eight tiles at a time wait in LDS; loaded at a tile's end they would come behind all weights on
 // their way (F = 5504, K = 2048, bfloat16 15 us, 12 from LDS).  The form without has no registers for that in FP8.
-// M = 13, K = 4096, F = 14336: 25 us FP8 (4.7 TB/s), 45 bfloat16 (5.3), with addends 32 and 47; K = 2048, F = 5504,
+// M = 13, K = 4096, F = 14336: 25 us FP8 (4.7 TB/s), 43 bfloat16 (5.4), with addends 32 and 46 to 49; K = 2048, F = 5504,
 // bfloat16 11
 // (4.0: of its 1.3 tiles a block the first loads' and the last sums' latency shows).  Weights kept in the caches: 1 to
 // 2 us more.
@@ -568,7 +568,9 @@ __global__ __launch_bounds__(256) void gated_staged_kernel(Operand x, Operand w,
 
 // ---------------------------------------------------------------- gradient of the activation
 
-// Eight columns of a row a thread, at any address; TAIL: F % 8 != 0.  Bound by HBM: 4096 x 5632 from float32 pre-activations
+// Eight columns of a row a thread, at any address; TAIL: F % 8 != 0.  dpre is rounded to bfloat16, half a step of 2^-8 a
+// value: it is the operand of the matrix cores in both products behind it, where a form of more pieces would be two or
+// three times the work; the gradients are off by 0.0023 of their norm for it, 0.0017 from a float32 dpre.  Bound by HBM: 4096 x 5632 from float32 pre-activations
 // 53 us, 6.1 TB/s.
 template <int ACT, int DY, int PRE, bool TAIL>
 __global__ __launch_bounds__(kThreads) void gated_grad_kernel(const void* __restrict__ dy, const void* __restrict__ pre,
@@ -712,8 +714,11 @@ hipError_t launch_gated_gemm(const void* w, int fp8, const uint16_t* x, const Ga
                     : go(gated_gemv_kernel<2, 4, 2>);
   }
   if (M <= 16 && in_stages) {
-    // Two blocks a CU with two stages each cover each other's barriers and ends (M = 5 and 13 with an addend, K = 4096, F =
-    // 14336: FP8 30 us, one block with four stages 37; bfloat16 44 and 49); K = 8192 in bfloat16 56 and 51.
+    // Two blocks a CU with two stages each cover each other's barriers and ends, one with four has as many bytes on their
+    // way.  Two pay where a block has few tiles or a row few stages, us, M = 13 (two stages, four): K = 1024, F = 14336 FP8
+    // 11.7, 14.6, bfloat16 13.0, 15.5; K = 2048, F = 5504 8.9, 9.9 and 11.2, 12.6, with addends 9.3, 10.7 and 11.7, 14.0;
+    // K = 4096, F = 14336 25.3 and 43 either way, with addends 31.8, 29.7 and 48.7, 45.8.  K = 8192 in bfloat16, F = 8192:
+    // 55.9, 50.2.
     auto go = [&](auto bytes, auto parts, auto stages) {
       constexpr int EB = decltype(bytes)::value, KS = decltype(parts)::value, S = decltype(stages)::value;
       constexpr int kLds = S * 16 * kRowsSpan + 8 * kWave * 16;
@@ -754,7 +759,8 @@ hipError_t launch_gated_gemm(const void* w, int fp8, const uint16_t* x, const Ga
     const bool narrow = 2 * ((F + 63) / 64) <= num_cus;
     // Beyond, tiles of 256 x 128 columns with a CU to themselves, or of 128 x 64 of which two blocks share one, by
     // the time of
-    // their rounds as for the products above: M = 256, F = 14336, K = 4096 91 and 70 us, M = 500 105 and 125.
+    // their rounds as for the products above: M = 256, F = 14336, K = 4096 FP8 107 and 67 us, bfloat16 116 and 85; M = 500
+    // 112 and 126, 115 and 148.
     const bool wide = 1.75 * rounds(M, F, 256, 128, num_cus) <= 1.05 * rounds(M, F, 128, 64, 2 * num_cus);
     auto by_tile = [&](auto bytes, auto out) {
       constexpr bool kFp8 = decltype(bytes)::value == 1;

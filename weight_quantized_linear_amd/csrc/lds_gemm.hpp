@@ -35,7 +35,7 @@ __device__ __forceinline__ void bdma4(__amdgpu_buffer_rsrc_t rsrc, char* lds, ui
 
 __device__ __forceinline__ u32x4 lds16(const char* p) { return *reinterpret_cast<const u32x4*>(p); }
 
-// Slot permutation of a row with CPR 16-byte chunks (CPR in {2, 4, 8}): rows
+// Slot permutation of a row with CPR 16-byte chunks (CPR in {2, 4, 8, 16}): rows
 // r and r' of one 16-row group collide in a bank group only if they also
 // agree in r / (16 / CPR), which the XOR then separates.
 template <int CPR>

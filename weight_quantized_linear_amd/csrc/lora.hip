@@ -146,8 +146,8 @@ __device__ __forceinline__ int find_tile(const Groups& g, int* cum, int tile, in
 // BM rows, a part of K, 16 FR of the R; its waves take 64 values of k in turn, the next ones on their way, and
 // add up at the end through LDS.  Both operands come straight from memory: neither is used by two waves.  Bound by
 // the way to memory, at 64-byte pieces of 16 rows a load: 4096 rows, K = 4096 16 us at R = 16, 25 at R = 64; 4099 rows,
-// K = 8192 28 us,
-// 2.4 TB/s.  64 rows of 64 groups, K = 4096: 6.0 us.  Twice the loads on their way, 8 waves a block, blocks that begin at
+// K = 8192 28 us, 2.4 TB/s (here and below: the kernel alone, no operand in a cache, if nothing else is said).  64 rows of
+// 64 groups, K = 4096: 6.0 us.  Twice the loads on their way, 8 waves a block, blocks that begin at
 // different k change nothing; x past the caches costs a tenth more.
 template <int BM, int FR, bool SMALL>
 __global__ __launch_bounds__(kThreads) void lora_shrink_kernel(const uint16_t* __restrict__ x,
@@ -252,9 +252,9 @@ __global__ __launch_bounds__(kThreads) void lora_shrink_kernel(const uint16_t* _
 // are eight consecutive columns: one 16-byte store of bfloat16.  LDS: the pieces of z as eights of r, the last one
 // the row's last eight values with zeros for those that it repeats, as b's eights are loaded.
 // WHOLE: an MFMA step is four eights of one piece, and b's are loaded once for all pieces; else the pieces' eights
-// follow each other.  SMALL: R < 8.  TAIL: N % 8 != 0.  Bound by base and out: 4096 rows, N = 14336, bfloat16, R = 64 68
-// us, 3.5 TB/s,
-// R = 16 50, 4.7; 4099 rows, N = 8192, R = 16 38, 3.5; 64 rows, N = 4096 6.6.  From R = 64 on the matrix cores' and LDS's
+// follow each other.  SMALL: R < 8.  TAIL: N % 8 != 0.  Bound by base and out: 4096 rows of 12
+// groups, N = 14336, bfloat16, R = 64 68 us, 3.5 TB/s, R = 16 50, 4.7; of 8 groups, whose fewer tiles get spans of 256, R = 64
+// 85, 3.2, float32 167, 3.0; 4099 rows, N = 8192, R = 16 38, 3.5; 64 rows, N = 4096 6.6.  From R = 64 on the matrix cores' and LDS's
 // part shows beside the bytes.
 constexpr int kSpan = 1024;
 
@@ -445,8 +445,9 @@ __device__ __forceinline__ uint32_t ends_before(uint32_t b, uint32_t e, int last
 // l's groups.  Block: one adapter, 16 FR of the R, 512 columns (128 a wave), every splits-th step of 32 rows, the next
 // one on its way.  A lane loads 8 rows x 8 columns and turns them by byte permutations into its pieces of eight MFMA
 // operands, whose row i is column 8 i + j of the wave's 128.  P: pieces of z.  Bound by x and dout: 4099 rows, K = 2048,
-// N = 8192 30 us at R = 16,
-// 2.8 TB/s; at R = 64 64, since each 32 of R read them again.
+// N = 8192 30 us at R = 16, 2.8 TB/s; at R = 64 64, since each 32 of R read them again.  Blocks are shared out by the
+// adapters that there are, not by their rows: 512 rows of each of 8 take 42 and 141 us, and 4096 rows of one of 32 (R = 16,
+// K = N = 4096) 266, 25 where it is the only one.
 struct SumArgs {
   const uint16_t* p;
   const float* z;
@@ -633,7 +634,8 @@ __global__ __launch_bounds__(kThreads) void lora_turn_kernel(Turn a, Turn b) {
 
 template <int V> using Int = std::integral_constant<int, V>;
 
-// Tiles of more than 16 rows where a group has more on average.
+// Tiles of more than 16 rows where a group has more on average.  The longest group is on the device: 900 rows beside 63
+// groups of one row (R = 16, K = N = 4096) take 9 and 12 us in tiles of 16, alone 7.5 and 8.2 in tiles of 32.
 bool tall(int64_t T, int64_t G) { return T > 16 * G; }
 
 int64_t tile_count(int64_t T, int64_t G, int bm) { return std::min(T, T / bm + G); }
